@@ -179,16 +179,17 @@ def _w4_quantize(x, fmt, group):
     n, k = x.shape
     g = x.view(n, k // group, group)
     if fmt == "e2m1":
-        s = (g.abs().amax(-1).clamp(min=AMAX_FLOOR) / 6).bfloat16()
+        # by a tensor: a division by a Python number may be done as a product with its rounded reciprocal
+        s = (g.abs().amax(-1).clamp(min=AMAX_FLOOR) / torch.full((), 6.0, device=x.device)).bfloat16()
         y = g / s.float().unsqueeze(-1)
         a = y.abs()
         # nearest value, ties to the even code: how many midpoints are passed
         c = ((a > 0.25).byte() + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5)
-             + 8 * torch.signbit(y))
+             + torch.signbit(y).byte() * 8)
         zeros = None
     else:
         lo, hi = g.amin(-1).clamp(max=0), g.amax(-1).clamp(min=0)
-        s = ((hi - lo).clamp(min=AMAX_FLOOR) / 15).bfloat16()
+        s = ((hi - lo).clamp(min=AMAX_FLOOR) / torch.full((), 15.0, device=x.device)).bfloat16()
         zeros = torch.round(-lo / s.float()).clamp(max=15)
         c = (torch.round(g / s.float().unsqueeze(-1)) + zeros.unsqueeze(-1)).clamp(0, 15).byte()
         zeros = zeros.byte()
