@@ -15,6 +15,12 @@ Layouts (all row-major, packed):
   hq   (SwiGLU) e4m3 [g, max_m, inter]; hs fp32 [g, inter/128, get_sfa_ld(max_m)]
   FP4  a [m, k/2], b [n, k/2] uint8, two e2m1 codes per byte (low nibble first),
        with the FP8 scale layouts
+  W4   (codes, scales, zeros): uint8 [n, k/2], two codes per byte (low nibble
+       first), bf16 [n, k/group], and uint8 [n, k/group] or None; without zeros
+       the codes are e2m1, with them integers 0..15
+  KV8  (k_codes, v_codes, k_scales, v_scales): e4m3 [blocks, h_kv, block, d],
+       e4m3 [blocks, h_kv, d, block], fp32 [blocks, h_kv] each; block tables
+       int32 [batch, max_blocks]
 """
 
 import ctypes
@@ -34,6 +40,8 @@ __all__ = [
     "k_grouped_fp8_gemm_nt", "bf16_gemm_nt", "fp4_gemm_nt", "quantize_a_1x128_fp4", "quantize_b_128x128_fp4", "get_m_alignment_for_contiguous_layout", "get_sfa_ld", "empty_sfa",
     "profile_next_launch",
     "reserve_workspace", "dense_workspace_size",
+    "bf16_w4_gemm_nt", "quantize_b_w4", "dequantize_b_w4",
+    "empty_kv8_cache", "kv8_append", "kv8_attention", "kv8_attention_workspace_size",
 ]
 
 
@@ -46,7 +54,7 @@ class DGError(RuntimeError):
 
 
 _lib = None
-_vp, _ci = ctypes.c_void_p, ctypes.c_int
+_vp, _ci, _cl = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
 _SIGNATURES = {
     "dg_fp8_gemm_nt": [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _vp],
     "dg_fp8_gemm_nt_noalloc": [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _vp],
@@ -69,6 +77,12 @@ _SIGNATURES = {
     "dg_profile_next_launch": [_vp, _vp],
     "dg_reserve_workspace": [ctypes.c_size_t, _vp],
     "dg_dense_workspace_size": [_ci, _ci, _ci, _ci, ctypes.POINTER(ctypes.c_size_t)],
+    "dg_bf16_w4_gemm_nt": [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _vp],
+    "dg_quantize_b_w4": [_vp, _ci, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _vp],
+    "dg_dequantize_b_w4": [_vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _vp],
+    "dg_kv8_append": [_vp, _cl, _vp, _cl] + [_vp] * 7 + [_ci] * 8 + [_vp],
+    "dg_kv8_attention": [_vp, _cl] + [_vp] * 9 + [ctypes.c_float] + [_ci] * 11 + [_vp],
+    "dg_kv8_attention_workspace_size": [_ci, ctypes.POINTER(ctypes.c_size_t)],
 }
 _RESTYPES = {"dg_status_string": ctypes.c_char_p, "dg_last_error_message": ctypes.c_char_p,
              "dg_version": ctypes.c_char_p}
@@ -436,3 +450,157 @@ def quantize_b_128x128_fp4(x, q=None, sfb=None):
         raise ValueError("output shape mismatch")
     _check(lib().dg_quantize_b_128x128_fp4(_ptr(x), _ptr(q), _ptr(sfb), n, k, _stream()))
     return q, sfb
+
+
+_W4_FORMATS = {"e2m1": 0, "u4": 1}
+
+
+def _w4_shape(b_triple):
+    """(codes, scales, zeros, n, k, group, format) of a W4 triple, checked."""
+    codes, scales, zeros = b_triple
+    _need(codes, "codes", (torch.uint8,), 2)
+    _need(scales, "scales", (torch.bfloat16,), 2)
+    n, kh = codes.shape
+    groups = scales.shape[1]
+    if groups < 1 or scales.shape[0] != n or 2 * kh % groups:
+        raise ValueError(f"scales {tuple(scales.shape)} do not fit codes {tuple(codes.shape)}")
+    if zeros is not None:
+        _need(zeros, "zeros", (torch.uint8,), 2)
+        if zeros.shape != scales.shape:
+            raise ValueError(f"zeros {tuple(zeros.shape)} do not fit scales {tuple(scales.shape)}")
+    return codes, scales, zeros, n, 2 * kh, 2 * kh // groups, 0 if zeros is None else 1
+
+
+def bf16_w4_gemm_nt(a, b_triple, d):
+    """d (bf16 [m, n], in place) = a (bf16 [m, k]) . w^T for 4-bit weights
+    w = scales * (codes - zeros), b_triple = (codes, scales, zeros or None)."""
+    _need(a, "a", (torch.bfloat16,), 2)
+    _need(d, "d", (torch.bfloat16,), 2)
+    codes, scales, zeros, n, k, group, fmt = _w4_shape(b_triple)
+    m = a.shape[0]
+    if a.shape[1] != k or d.shape[0] != m or d.shape[1] != n:
+        raise ValueError(f"shape mismatch a{tuple(a.shape)} w({n}, {k}) d{tuple(d.shape)}")
+    _check(lib().dg_bf16_w4_gemm_nt(a.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                    None if zeros is None else zeros.data_ptr(), d.data_ptr(), m, n, k, group, fmt,
+                                    _stream()))
+    return d
+
+
+def quantize_b_w4(x, fmt="e2m1", group=128):
+    """bf16 or fp32 weights [n, k] -> (codes, scales, zeros or None), fmt "e2m1" or "u4"."""
+    _need(x, "x", (torch.bfloat16, torch.float32), 2)
+    if fmt not in _W4_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(_W4_FORMATS)}")
+    n, k = x.shape
+    if group not in (32, 64, 128) or k < group or k % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide k = {k}, got {group}")
+    codes = torch.empty((n, k // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((n, k // group), dtype=torch.bfloat16, device=x.device)
+    zeros = torch.empty((n, k // group), dtype=torch.uint8, device=x.device) if fmt == "u4" else None
+    _check(lib().dg_quantize_b_w4(x.data_ptr(), int(x.dtype == torch.bfloat16), codes.data_ptr(), scales.data_ptr(),
+                                  None if zeros is None else zeros.data_ptr(), n, k, group, _W4_FORMATS[fmt], _stream()))
+    return codes, scales, zeros
+
+
+def dequantize_b_w4(b_triple, w=None):
+    """(codes, scales, zeros or None) -> the bf16 weights [n, k] they stand for."""
+    codes, scales, zeros, n, k, group, fmt = _w4_shape(b_triple)
+    w = torch.empty((n, k), dtype=torch.bfloat16, device=codes.device) if w is None else w
+    _need(w, "w", (torch.bfloat16,), 2)
+    if tuple(w.shape) != (n, k):
+        raise ValueError(f"w must be {(n, k)}, got {tuple(w.shape)}")
+    _check(lib().dg_dequantize_b_w4(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                                    w.data_ptr(), n, k, group, fmt, _stream()))
+    return w
+
+
+def empty_kv8_cache(num_blocks, h_kv, d, block=64, device="cuda"):
+    """An 8-bit key/value cache of num_blocks blocks of `block` tokens."""
+    return (torch.empty((num_blocks, h_kv, block, d), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((num_blocks, h_kv, d, block), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((num_blocks, h_kv), dtype=torch.float32, device=device),
+            torch.empty((num_blocks, h_kv), dtype=torch.float32, device=device))
+
+
+def _kv8_shape(cache, block_table, lens, cu):
+    """(num_blocks, h_kv, block, d, batch, max_blocks) of a cache and its tables, checked."""
+    k_codes, v_codes, k_scales, v_scales = cache
+    _need(k_codes, "k_codes", _FP8, 4)
+    _need(v_codes, "v_codes", _FP8, 4)
+    _need(k_scales, "k_scales", (torch.float32,), 2)
+    _need(v_scales, "v_scales", (torch.float32,), 2)
+    _need(block_table, "block_table", (torch.int32,), 2)
+    _need(lens, "lens", (torch.int32,), 1)
+    _need(cu, "cu", (torch.int32,), 1)
+    num_blocks, h_kv, block, d = k_codes.shape
+    if (tuple(v_codes.shape) != (num_blocks, h_kv, d, block) or tuple(k_scales.shape) != (num_blocks, h_kv)
+            or tuple(v_scales.shape) != (num_blocks, h_kv)):
+        raise ValueError("cache shape mismatch")
+    batch, max_blocks = block_table.shape
+    if lens.shape[0] != batch or cu.shape[0] != batch + 1:
+        raise ValueError("the block table, the lengths and cu (batch + 1) disagree on the batch")
+    return num_blocks, h_kv, block, d, batch, max_blocks
+
+
+def _packed(x, name, heads, d):
+    """Checks bf16 [total, heads, d] with packed heads; returns (total, elements from token to token)."""
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 3 or not x.is_cuda:
+        raise TypeError(f"{name} must be a bf16 device tensor [tokens, heads, d]")
+    total, h, dim = x.shape
+    if h != heads or dim != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(x.shape)}")
+    stride, s1, s2 = x.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+        raise ValueError(f"the heads of a token of {name} must lie packed")
+    return total, stride if total > 1 else heads * d
+
+
+def kv8_append(k, v, cache, block_table, ctx_lens, cu_new, max_new):
+    """Append packed new keys and values (bf16 [total, h_kv, d]; slices of a
+    wider projection serve) behind the ctx_lens[i] cached tokens of each
+    sequence, in place.  cu_new: int32 [batch + 1] running sums of the new
+    tokens; max_new: the most of one sequence."""
+    num_blocks, h_kv, block, d, batch, max_blocks = _kv8_shape(cache, block_table, ctx_lens, cu_new)
+    total, ks = _packed(k, "k", h_kv, d)
+    total_v, vs = _packed(v, "v", h_kv, d)
+    if total != total_v:
+        raise ValueError(f"k holds {total} tokens, v {total_v}")
+    k_codes, v_codes, k_scales, v_scales = cache
+    _check(lib().dg_kv8_append(k.data_ptr(), ks, v.data_ptr(), vs, k_codes.data_ptr(), v_codes.data_ptr(),
+                               k_scales.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(),
+                               cu_new.data_ptr(), batch, total, max_new, h_kv, d, block, num_blocks, max_blocks,
+                               _stream()))
+    return cache
+
+
+def kv8_attention(q, cache, block_table, kv_lens, cu_q, max_q, out, lse=None, scale=None, causal=True, window=0):
+    """Attention of packed queries (bf16 [total, h_q, d]) over the cache; out
+    bf16 [total, h_q, d] and lse fp32 [total, h_q] (or None) are written in
+    place.  kv_lens counts the queries' own tokens; cu_q: int32 [batch + 1]
+    running sums of the queries; max_q: the most of one sequence; scale:
+    d ** -0.5 if None; window: the last so many tokens only (0: all)."""
+    num_blocks, h_kv, block, d, batch, max_blocks = _kv8_shape(cache, block_table, kv_lens, cu_q)
+    _need(out, "out", (torch.bfloat16,), 3)
+    h_q = out.shape[1]
+    total, stride = _packed(q, "q", h_q, d)
+    if out.shape[0] != total or out.shape[2] != d:
+        raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), 2)
+        if lse.shape[0] != total or lse.shape[1] != h_q:
+            raise ValueError(f"lse must be {(total, h_q)}, got {tuple(lse.shape)}")
+    k_codes, v_codes, k_scales, v_scales = cache
+    _check(lib().dg_kv8_attention(q.data_ptr(), stride, k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                  v_scales.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), cu_q.data_ptr(),
+                                  out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                  d ** -0.5 if scale is None else scale, causal, window, batch, total, max_q, h_q,
+                                  h_kv, d, block, num_blocks, max_blocks, _stream()))
+    return out
+
+
+def kv8_attention_workspace_size(d):
+    """Bytes of a stream's workspace that kv8_attention takes; give it to
+    reserve_workspace before capturing such calls."""
+    size = ctypes.c_size_t(0)
+    _check(lib().dg_kv8_attention_workspace_size(int(d), ctypes.byref(size)))
+    return size.value

@@ -22,8 +22,10 @@
 #include <vector>
 
 #include "gemm_kernel.h"
+#include "kv8_kernel.h"
 #include "quant_kernel.h"
 #include "skinny_kernel.h"
+#include "w4_kernel.h"
 
 namespace {
 
@@ -846,6 +848,114 @@ int fp8_gemm(const uint8_t* a, const float* sfa, const uint8_t* b, const float* 
   return launch_dense(c, p, dev, info, m, n, k, k / 128, stream, ws);
 }
 
+// ---- 4-bit weights with group scales (w4_kernel.h)
+
+int check_w4(int n, int k, int group, int format, const void* zeros) {
+  if (format != DG_W4_E2M1 && format != DG_W4_U4)
+    return fail(DG_ERR_INVALID_ARGUMENT, "unknown 4-bit format %d", format);
+  if ((format == DG_W4_U4) != (zeros != nullptr))
+    return fail(DG_ERR_INVALID_ARGUMENT, "zeros go with DG_W4_U4 and with it only");
+  if (n < 1) return fail(DG_ERR_INVALID_ARGUMENT, "n must be >= 1 (got %d)", n);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "group must be 32, 64 or 128 (got %d)", group);
+  if (k < group || k % group != 0)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "k must be a positive multiple of the group of %d (got %d)", group, k);
+  return DG_OK;
+}
+
+struct W4Kernel {
+  const void* fn;
+  int rows, cols, threads;  // of d, per workgroup; threads of it
+};
+
+template <int FMT, int GROUP>
+W4Kernel w4_pick(int m) {
+  if (m <= 16)
+    return {reinterpret_cast<const void*>(&dg::w4_gemm_kernel<FMT, GROUP, 1, 1, 8, 2>), 16, 16, 512};
+  if (m <= 32)
+    return {reinterpret_cast<const void*>(&dg::w4_gemm_kernel<FMT, GROUP, 2, 2, 8, 1>), 32, 32, 512};
+  return {reinterpret_cast<const void*>(&dg::w4_gemm_kernel<FMT, GROUP, 4, 2, 8, 1>), 64, 32, 512};
+}
+
+template <int FMT>
+W4Kernel w4_pick(int m, int group) {
+  return group == 32 ? w4_pick<FMT, 32>(m) : group == 64 ? w4_pick<FMT, 64>(m) : w4_pick<FMT, 128>(m);
+}
+
+template <int FMT, bool BF16>
+const void* w4_quant_fn(int group) {
+  return group == 32   ? reinterpret_cast<const void*>(&dg::w4_quant_kernel<FMT, 32, BF16>)
+         : group == 64 ? reinterpret_cast<const void*>(&dg::w4_quant_kernel<FMT, 64, BF16>)
+                       : reinterpret_cast<const void*>(&dg::w4_quant_kernel<FMT, 128, BF16>);
+}
+
+template <int FMT>
+const void* w4_dequant_fn(int group) {
+  return group == 32   ? reinterpret_cast<const void*>(&dg::w4_dequant_kernel<FMT, 32>)
+         : group == 64 ? reinterpret_cast<const void*>(&dg::w4_dequant_kernel<FMT, 64>)
+                       : reinterpret_cast<const void*>(&dg::w4_dequant_kernel<FMT, 128>);
+}
+
+int launch_plain(const char* what, const void* fn, dim3 grid, int threads, void** args, dg_stream_t stream) {
+  if (log_enabled())
+    fprintf(stderr, "[dg] %s grid=%ux%ux%u threads=%d\n", what, grid.x, grid.y, grid.z, threads);
+  hipError_t e = hipLaunchKernel(fn, grid, dim3(threads), args, 0, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(DG_ERR_HIP, "launch of %s failed: %s", what, hipGetErrorString(e));
+  return ok();
+}
+
+// ---- 8-bit key/value cache (kv8_kernel.h)
+
+int check_cache(const void* k_codes, const void* v_codes, const void* k_scales, const void* v_scales,
+                const void* table, int h_kv, int d, int block, int num_blocks, int max_blocks, dg::Kv8Cache* c) {
+  if (!k_codes || !v_codes || !k_scales || !v_scales || !table)
+    return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (h_kv < 1 || h_kv > 32767) return fail(DG_ERR_INVALID_ARGUMENT, "h_kv must be 1..32767 (got %d)", h_kv);
+  if (num_blocks < 0 || max_blocks < 0) return fail(DG_ERR_INVALID_ARGUMENT, "block counts must be >= 0");
+  if (d != 64 && d != 128 && d != 256)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "head dimension must be 64, 128 or 256 (got %d)", d);
+  int log2 = 4;
+  while (log2 < 7 && (1 << log2) != block) ++log2;
+  if ((1 << log2) != block)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "block must be 16, 32, 64 or 128 tokens (got %d)", block);
+  if (((long long)max_blocks << log2) > (1LL << 30))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "a sequence's table may span at most 2^30 tokens");
+  if (!aligned16(k_codes) || !aligned16(v_codes) || (reinterpret_cast<uintptr_t>(k_scales) & 3u) ||
+      (reinterpret_cast<uintptr_t>(v_scales) & 3u) || (reinterpret_cast<uintptr_t>(table) & 3u))
+    return fail(DG_ERR_MISALIGNED, "codes must be 16-byte aligned, scales and block table 4-byte");
+  c->k_codes = (uint8_t*)k_codes;
+  c->v_codes = (uint8_t*)v_codes;
+  c->k_scales = (float*)k_scales;
+  c->v_scales = (float*)v_scales;
+  c->table = (const int32_t*)table;
+  c->h_kv = h_kv;
+  c->block = block;
+  c->block_log2 = log2;
+  c->num_blocks = num_blocks;
+  c->max_blocks = max_blocks;
+  return DG_OK;
+}
+
+int check_packed(const void* x, int64_t stride, int heads, int d, const char* name) {
+  if (!aligned16(x)) return fail(DG_ERR_MISALIGNED, "%s must be 16-byte aligned", name);
+  if (stride < (int64_t)heads * d || stride % 8 != 0)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: the stride between tokens must be a multiple of 8 elements and at least "
+                "heads * d (got %lld)", name, (long long)stride);
+  return DG_OK;
+}
+
+int check_batch(int batch, int total, int most) {
+  if (batch < 0 || total < 0 || most < 0)
+    return fail(DG_ERR_INVALID_ARGUMENT, "batch, token counts and the longest sequence must be >= 0");
+  if (batch > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "at most 65535 sequences (got %d)", batch);
+  return DG_OK;
+}
+
+// Workgroups that share an attention call: two per CU (each keeps 64 KB of
+// codes in flight).  Each leaves at most two unfinished 16-row tiles.
+int kv8_workers(const DeviceInfo* info) { return 2 * info->cus; }
+size_t kv8_part_floats(int workers, int d) { return (size_t)workers * 2 * 16 * (d + 2); }
+
 }  // namespace
 
 extern "C" {
@@ -1230,6 +1340,162 @@ int dg_quantize_a_1x128_fp4(const float* x, uint8_t* q, float* sfa, int m, int k
 
 int dg_quantize_b_128x128_fp4(const float* x, uint8_t* q, float* sfb, int n, int k, dg_stream_t stream) {
   return quantize_b(reinterpret_cast<const void*>(&dg::quant_b_fp4_kernel), x, q, sfb, n, k, stream);
+}
+
+int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                       uint16_t* d, int m, int n, int k, int group, int format, dg_stream_t stream) {
+  if (!codes || !scales || (m > 0 && (!a || !d))) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (m < 0) return fail(DG_ERR_INVALID_ARGUMENT, "m must be >= 0 (got %d)", m);
+  if (int s = check_w4(n, k, group, format, zeros)) return s;
+  if (!aligned16(a) || !aligned16(codes) || !aligned16(scales) || !aligned16(d) || !aligned16(zeros))
+    return fail(DG_ERR_MISALIGNED, "pointers must be 16-byte aligned");
+  if (m == 0) return ok();
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  const W4Kernel w = format == DG_W4_E2M1 ? w4_pick<dg::kW4E2m1>(m, group) : w4_pick<dg::kW4U4>(m, group);
+  if ((m + w.rows - 1) / w.rows > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m too large (%d)", m);
+  dg::W4Params p{a, codes, scales, zeros, d, m, n, k};
+  void* args[] = {&p};
+  return launch_plain("w4_gemm", w.fn, dim3((n + w.cols - 1) / w.cols, (m + w.rows - 1) / w.rows), w.threads, args, stream);
+}
+
+int dg_quantize_b_w4(const void* x, int x_bf16, uint8_t* codes, uint16_t* scales, uint8_t* zeros, int n, int k,
+                     int group, int format, dg_stream_t stream) {
+  if (!x || !codes || !scales) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (int s = check_w4(n, k, group, format, zeros)) return s;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(zeros))
+    return fail(DG_ERR_MISALIGNED, "pointers must be 16-byte aligned");
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  long long total8 = (long long)n * k / 8;
+  const long long blocks = (total8 + 255) / 256;
+  if (blocks >= (1LL << 24)) return fail(DG_ERR_UNSUPPORTED_SHAPE, "weight too large (%d x %d)", n, k);
+  const void* fn = format == DG_W4_E2M1
+                       ? (x_bf16 ? w4_quant_fn<dg::kW4E2m1, true>(group) : w4_quant_fn<dg::kW4E2m1, false>(group))
+                       : (x_bf16 ? w4_quant_fn<dg::kW4U4, true>(group) : w4_quant_fn<dg::kW4U4, false>(group));
+  void* args[] = {&x, &codes, &scales, &zeros, &total8};
+  return launch_plain("w4_quant", fn, dim3((unsigned)blocks), 256, args, stream);
+}
+
+int dg_dequantize_b_w4(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, uint16_t* w, int n, int k,
+                       int group, int format, dg_stream_t stream) {
+  if (!codes || !scales || !w) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (int s = check_w4(n, k, group, format, zeros)) return s;
+  if (!aligned16(w) || !aligned16(codes) || !aligned16(scales) || !aligned16(zeros))
+    return fail(DG_ERR_MISALIGNED, "pointers must be 16-byte aligned");
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  long long total8 = (long long)n * k / 8;
+  const long long blocks = (total8 + 255) / 256;
+  if (blocks >= (1LL << 24)) return fail(DG_ERR_UNSUPPORTED_SHAPE, "weight too large (%d x %d)", n, k);
+  const void* fn = format == DG_W4_E2M1 ? w4_dequant_fn<dg::kW4E2m1>(group) : w4_dequant_fn<dg::kW4U4>(group);
+  void* args[] = {&codes, &scales, &zeros, &w, &total8};
+  return launch_plain("w4_dequant", fn, dim3((unsigned)blocks), 256, args, stream);
+}
+
+int dg_kv8_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint8_t* k_codes,
+                  uint8_t* v_codes, float* k_scales, float* v_scales, const int32_t* block_table,
+                  const int32_t* ctx_lens, const int32_t* cu_new, int batch, int total, int max_new, int h_kv, int d,
+                  int block, int num_blocks, int max_blocks, dg_stream_t stream) {
+  if (!ctx_lens || !cu_new || (total > 0 && (!k || !v))) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  dg::Kv8AppendParams p{};
+  if (int s = check_cache(k_codes, v_codes, k_scales, v_scales, block_table, h_kv, d, block, num_blocks, max_blocks,
+                          &p.c)) return s;
+  if (int s = check_batch(batch, total, max_new)) return s;
+  if (int s = check_packed(k, k_stride, h_kv, d, "k")) return s;
+  if (int s = check_packed(v, v_stride, h_kv, d, "v")) return s;
+  if ((reinterpret_cast<uintptr_t>(ctx_lens) & 3u) || (reinterpret_cast<uintptr_t>(cu_new) & 3u))
+    return fail(DG_ERR_MISALIGNED, "lengths must be 4-byte aligned");
+  if (batch == 0 || total == 0 || max_new == 0 || num_blocks == 0 || max_blocks == 0) return ok();
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  p.k = k;
+  p.v = v;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.ctx = ctx_lens;
+  p.cu = cu_new;
+  p.total = total;
+  p.most = max_new < total ? max_new : total;
+  // blocks that max_new tokens can touch, wherever the first one stands
+  const int slots = (p.most + block - 2) / block + 1;
+  if ((long long)slots >= (1LL << 24)) return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many new tokens (%d)", p.most);
+  const void* fn = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<64>)
+                   : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<128>)
+                              : reinterpret_cast<const void*>(&dg::kv8_append_kernel<256>);
+  void* args[] = {&p};
+  return launch_plain("kv8_append", fn, dim3(slots, 2 * h_kv, batch), 256, args, stream);
+}
+
+int dg_kv8_attention_workspace_size(int d, size_t* bytes) {
+  if (!bytes) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  *bytes = 0;
+  if (d != 64 && d != 128 && d != 256)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "head dimension must be 64, 128 or 256 (got %d)", d);
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  *bytes = kv8_part_floats(kv8_workers(info), d) * sizeof(float);
+  return ok();
+}
+
+int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes, const uint8_t* v_codes,
+                     const float* k_scales, const float* v_scales, const int32_t* block_table,
+                     const int32_t* kv_lens, const int32_t* cu_q, uint16_t* out, float* lse, float scale, int causal,
+                     int window, int batch, int total, int max_q, int h_q, int h_kv, int d, int block, int num_blocks,
+                     int max_blocks, dg_stream_t stream) {
+  if (!kv_lens || !cu_q || (total > 0 && (!q || !out))) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  dg::Kv8AttnParams p{};
+  if (int s = check_cache(k_codes, v_codes, k_scales, v_scales, block_table, h_kv, d, block, num_blocks, max_blocks,
+                          &p.c)) return s;
+  if (int s = check_batch(batch, total, max_q)) return s;
+  if (h_q < 1 || h_q % h_kv != 0)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "h_q must be a positive multiple of h_kv = %d (got %d)", h_kv, h_q);
+  if (window < 0) return fail(DG_ERR_INVALID_ARGUMENT, "window must be >= 0 (got %d)", window);
+  if (window > 0 && !causal) return fail(DG_ERR_INVALID_ARGUMENT, "a window goes with causal attention only");
+  if (int s = check_packed(q, q_stride, h_q, d, "q")) return s;
+  if (!aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(kv_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(cu_q) & 3u))
+    return fail(DG_ERR_MISALIGNED, "out must be 16-byte aligned, lse and lengths 4-byte");
+  if (batch == 0 || total == 0 || max_q == 0) return ok();
+  p.most = max_q < total ? max_q : total;
+  const long long tiles = ((long long)p.most * (h_q / h_kv) + 15) / 16;
+  if ((long long)p.most * h_q > 0x3FFFFFFFLL || tiles >= (1LL << 24))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many queries per sequence (%d of %d heads)", p.most, h_q);
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.kv_lens = kv_lens;
+  p.cu = cu_q;
+  p.out = out;
+  p.lse = lse;
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.causal = causal != 0;
+  p.window = window;
+  p.batch = batch;
+  p.total = total;
+  p.h_q = h_q;
+  p.group = h_q / h_kv;
+  p.workers = kv8_workers(info);
+  char* base = nullptr;
+  if (int s = ensure_workspace(dev, (hipStream_t)stream, kv8_part_floats(p.workers, d) * sizeof(float), &base)) return s;
+  p.part_u = (float*)(base + kWsHeader);
+  p.part_ml = p.part_u + (size_t)p.workers * 2 * 16 * d;
+  const void* fn = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_attn_kernel<64>)
+                   : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_attn_kernel<128>)
+                              : reinterpret_cast<const void*>(&dg::kv8_attn_kernel<256>);
+  const void* join = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_join_kernel<64>)
+                     : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_join_kernel<128>)
+                                : reinterpret_cast<const void*>(&dg::kv8_join_kernel<256>);
+  void* args[] = {&p};
+  if (int s = launch_plain("kv8_attn", fn, dim3(p.workers), 256, args, stream)) return s;
+  return launch_plain("kv8_join", join, dim3((unsigned)tiles, h_kv, batch), 256, args, stream);
 }
 
 }  // extern "C"

@@ -310,6 +310,127 @@ int dg_quantize_a_1x128_fp4(const float* x, uint8_t* q, float* sfa, int m, int k
 int dg_quantize_b_128x128_fp4(const float* x, uint8_t* q, float* sfb, int n, int k, dg_stream_t stream);
 
 /*
+ * ---- 4-bit weights with bf16 activations
+ *
+ * A weight matrix [n][k] in 4 bits with one bf16 scale for every row and group
+ * of 32, 64 or 128 values along K:
+ *
+ *   w[n][k] = s[n][k / group] * (c[n][k] - z[n][k / group])
+ *
+ *   codes  [n][k/2] bytes, two codes per byte (element 2i in the low nibble)
+ *   scales [n][k/group] bf16 bits
+ *   zeros  [n][k/group] bytes 0..15: DG_W4_U4 only, NULL for DG_W4_E2M1
+ *
+ * DG_W4_E2M1: c is the e2m1 value of the code (as dg_fp4_gemm_nt), z = 0.
+ * DG_W4_U4: c is the code itself, 0..15.
+ * k must be a positive multiple of group; every pointer 16-byte aligned.
+ */
+typedef enum { DG_W4_E2M1 = 0, DG_W4_U4 = 1 } dg_w4_format;
+
+/*
+ * d[m][n] = bf16( sum_g s[n][g] * (sum_{k in g} c[n][k] a[m][k] - z[n][g] * sum_{k in g} a[m][k]) )
+ * for bf16 a [m][k]: the projections of a decode step, where a handful of
+ * tokens meet weights that are read once.  Products and sums are fp32 (the
+ * scale meets the fp32 sum of its group, so no weight is rounded after
+ * scaling), one launch, no scratch memory, the same bits on every call.  Any
+ * m >= 0 (0: a no-op) is computed; up to 64 rows share one read of the
+ * weights, more rows read them again for every 64, so a long prompt is better
+ * served by dg_dequantize_b_w4 and dg_bf16_gemm_nt.
+ */
+int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                       uint16_t* d, int m, int n, int k, int group, int format, dg_stream_t stream);
+
+/*
+ * Quantise a weight matrix x[n][k] (bf16 bits if x_bf16, else fp32) into that
+ * form; x must be finite.  Per row and group:
+ *   DG_W4_E2M1: s = bf16(max(amax, 1e-4) / 6), code = e2m1(x / s), nearest, ties to even
+ *   DG_W4_U4:   lo = min(x, 0), hi = max(x, 0), s = bf16(max(hi - lo, 1e-4) / 15),
+ *               z = min(rint(-lo / s), 15), code = clamp(rint(x / s) + z, 0, 15)
+ * in fp32 with correctly rounded divisions, against the scale as stored.
+ */
+int dg_quantize_b_w4(const void* x, int x_bf16, uint8_t* codes, uint16_t* scales, uint8_t* zeros, int n, int k,
+                     int group, int format, dg_stream_t stream);
+
+/* w[n][k] = bf16(s * (c - z)): the bf16 weights that codes stand for. */
+int dg_dequantize_b_w4(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, uint16_t* w, int n, int k,
+                       int group, int format, dg_stream_t stream);
+
+/*
+ * ---- An 8-bit key/value cache and the attention over it
+ *
+ * A pool of num_blocks blocks of `block` tokens (16, 32, 64 or 128) of h_kv
+ * heads of d values (64, 128 or 256), in e4m3 codes with one fp32 scale for
+ * each block and head, keys and values apart:
+ *
+ *   k_codes [num_blocks][h_kv][block][d]    k_scales [num_blocks][h_kv]
+ *   v_codes [num_blocks][h_kv][d][block]    v_scales [num_blocks][h_kv]
+ *
+ * (values lie dimension by dimension).  block_table [batch][max_blocks] int32
+ * names the block that holds tokens j * block .. j * block + block - 1 of each
+ * sequence.  Entries that no token in question falls into are not read; tokens
+ * whose entry lies outside [0, num_blocks), or past max_blocks, are neither
+ * written nor seen.  Code arrays may pass 4 GiB.
+ *
+ * Packed tokens: q, k, v hold the rows of all sequences one after the other,
+ * [total][heads][d] bf16 with *_stride elements (a multiple of 8) from token to
+ * token, so slices of one projection's output serve as they are; cu [batch+1]
+ * int32 holds the running sums of the sequences' rows, cu[0] = 0.  Lengths and
+ * running sums live on the device and are read there only; rows outside
+ * [0, total) and rows past the given longest sequence are ignored.
+ *
+ * dg_kv8_append puts k and v of the new tokens of every sequence behind the
+ * ctx_lens[i] tokens that it has in the cache (max_new: the most new tokens of
+ * one sequence).  Per block and head, over the new values that fall into it:
+ *
+ *   s' = max(s, smallest power of two p with amax <= 448 p)   amax floored at 1e-4
+ *   code = e4m3(x / s'), nearest even
+ *
+ * with s the block's scale, or 0 if it held no token; if s' > s the block's
+ * older codes become e4m3(c * s / s').  Powers of two lose nothing in either
+ * step but below the smallest normal code.  amax counts finite values;
+ * infinities saturate, NaN is stored as NaN.  A block that gets tokens must
+ * belong to one sequence.  Bytes past a sequence's last token keep what they
+ * held.  Nothing is allocated.
+ */
+int dg_kv8_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint8_t* k_codes,
+                  uint8_t* v_codes, float* k_scales, float* v_scales, const int32_t* block_table,
+                  const int32_t* ctx_lens, const int32_t* cu_new, int batch, int total, int max_new, int h_kv, int d,
+                  int block, int num_blocks, int max_blocks, dg_stream_t stream);
+
+/*
+ * Attention of the packed queries over the cache: for query i of the n_i of
+ * sequence s, standing at position kv_lens[s] - n_i + i (its own key is in the
+ * cache already, so one call serves single tokens, several tokens and prompts
+ * behind a cached prefix), and head h reading key/value head h / (h_q / h_kv):
+ *
+ *   x[j] = scale * (q . k[j]),  out = sum_j softmax(x)[j] v[j],  lse = log sum_j e^x[j]
+ *
+ * over the tokens j it sees: those up to its own position if causal, all
+ * kv_lens[s] otherwise, and of these the last `window` if window > 0 (causal
+ * only).  A row that sees no token gets out = 0 and lse = -inf.  A NaN in a
+ * key or value reaches the rows that see it and no others; what the cache
+ * holds past kv_lens[s] reaches none.  Scales must be positive (a value scale
+ * below 2^-64 counts as 2^-64).
+ * out is bf16 [total][h_q][d], lse fp32 [total][h_q] or NULL.  max_q is the
+ * most queries of one sequence.  Scores, the softmax's running maximum and
+ * sums and the output's accumulator are fp32; probabilities are rounded to
+ * fp16 for the second product.  Results do not depend on anything but the
+ * arguments: the same call gives the same bits.
+ * Needs dg_kv8_attention_workspace_size bytes of the stream's workspace (see
+ * the workspace rule above: reserve it before capturing).  The work is shared
+ * out on the device from the lengths it finds there, so a captured call stays
+ * right, and balanced, as sequences grow.
+ */
+int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes, const uint8_t* v_codes,
+                     const float* k_scales, const float* v_scales, const int32_t* block_table,
+                     const int32_t* kv_lens, const int32_t* cu_q, uint16_t* out, float* lse, float scale, int causal,
+                     int window, int batch, int total, int max_q, int h_q, int h_kv, int d, int block, int num_blocks,
+                     int max_blocks, dg_stream_t stream);
+
+/* Bytes of the stream's workspace that dg_kv8_attention takes on the current device. */
+int dg_kv8_attention_workspace_size(int d, size_t* bytes);
+
+/*
  * Size the split-K workspace of `stream` on the current device to hold at
  * least `bytes` of partial tiles (dg_dense_workspace_size gives a call's
  * need), so that later calls on that stream that fit allocate nothing and

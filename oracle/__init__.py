@@ -28,6 +28,8 @@ e2m1   the FP4 codec (16 codes) and its two-per-byte packing
 quant  1x128 (activation) and 128x128 (weight) quantisers, FP8 and FP4
 gemm   dense, contiguous-grouped, masked-grouped and K-grouped reference GEMMs in fp64,
        the BF16 and FP4 NT GEMMs; FC1 + SwiGLU on the masked and contiguous layouts
+w4     4-bit weights with group scales: quantiser, inverse, product
+kv8    the paged 8-bit key/value cache: append and attention
 check  the element-wise acceptance rule
 """
 
@@ -51,3 +53,5 @@ from .gemm import (  # noqa: F401
     silu,
 )
 from .check import tolerance_check, bf16_bits_to_float, bf16_round  # noqa: F401
+from .w4 import dequantize_w4, quantize_w4, w4_gemm_ref  # noqa: F401
+from . import kv8  # noqa: F401
