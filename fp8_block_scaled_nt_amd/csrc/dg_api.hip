@@ -236,6 +236,10 @@ const SkinnyConfig* find_skinny(const char* name) {
   return nullptr;
 }
 
+// the two ways of an attention call over the 8-bit cache
+constexpr const char* kKv8Split = "kv8_split";
+constexpr const char* kKv8Prompt = "kv8_prompt";
+
 // DG_FORCE_CONFIG=<name> pins the configuration of the variant it names (for
 // tuning sweeps); an unknown name is an error rather than silently ignored.
 int forced_config(int variant, const Config** out, int dtype = dg::kFp8, int epi = dg::kEpiBf16) {
@@ -246,7 +250,7 @@ int forced_config(int variant, const Config** out, int dtype = dg::kFp8, int epi
   const Config* t = configs(&cnt);
   bool known = false;
   for (int i = 0; i < cnt; ++i) known = known || strcmp(t[i].name, e) == 0;
-  known = known || find_skinny(e) != nullptr;
+  known = known || find_skinny(e) != nullptr || strcmp(e, kKv8Split) == 0 || strcmp(e, kKv8Prompt) == 0;
   if (!known) return fail(DG_ERR_INVALID_ARGUMENT, "DG_FORCE_CONFIG names no configuration: %s", e);
   *out = find_config(e, variant, dtype, epi);
   return DG_OK;
@@ -1455,6 +1459,8 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   if (int s = check_batch(batch, total, max_q)) return s;
   if (h_q < 1 || h_q % h_kv != 0)
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "h_q must be a positive multiple of h_kv = %d (got %d)", h_kv, h_q);
+  if (!(scale >= 0.f && scale <= 3.4e38f))
+    return fail(DG_ERR_INVALID_ARGUMENT, "scale must be finite and >= 0 (got %g)", (double)scale);
   if (window < 0) return fail(DG_ERR_INVALID_ARGUMENT, "window must be >= 0 (got %d)", window);
   if (window > 0 && !causal) return fail(DG_ERR_INVALID_ARGUMENT, "a window goes with causal attention only");
   if (int s = check_packed(q, q_stride, h_q, d, "q")) return s;
@@ -1482,6 +1488,22 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   p.total = total;
   p.h_q = h_q;
   p.group = h_q / h_kv;
+  if (num_blocks == 0) p.c.max_blocks = 0;  // no blocks: no tokens, whatever the lengths say
+  void* args[] = {&p};
+  // Prompts: rows in workgroups of 128 (64 for d = 256) that walk all their
+  // keys, as long as there are enough of them to fill the GPU.
+  const int prompt_rows = d == 256 ? 64 : 128;
+  const long long rows = (long long)p.most * p.group;
+  const long long prompt_tiles = (rows + prompt_rows - 1) / prompt_rows;
+  bool prompt = rows >= 64 && prompt_tiles * h_kv * batch >= info->cus;
+  if (const char* e = getenv("DG_FORCE_CONFIG"))
+    prompt = strcmp(e, kKv8Prompt) == 0 || (prompt && strcmp(e, kKv8Split) != 0);
+  if (prompt && prompt_tiles <= 65535) {
+    const void* fn = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<64, 2>)
+                     : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<128, 2>)
+                                : reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<256, 1>);
+    return launch_plain("kv8_prompt", fn, dim3(h_kv, batch, (unsigned)prompt_tiles), 256, args, stream);
+  }
   p.workers = kv8_workers(info);
   char* base = nullptr;
   if (int s = ensure_workspace(dev, (hipStream_t)stream, kv8_part_floats(p.workers, d) * sizeof(float), &base)) return s;
@@ -1493,7 +1515,6 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   const void* join = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_join_kernel<64>)
                      : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_join_kernel<128>)
                                 : reinterpret_cast<const void*>(&dg::kv8_join_kernel<256>);
-  void* args[] = {&p};
   if (int s = launch_plain("kv8_attn", fn, dim3(p.workers), 256, args, stream)) return s;
   return launch_plain("kv8_join", join, dim3((unsigned)tiles, h_kv, batch), 256, args, stream);
 }

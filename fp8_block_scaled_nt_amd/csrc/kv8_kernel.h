@@ -38,12 +38,12 @@ struct Kv8Cache {
 
 // The block of sequence `seq` that holds token `token`, or -1 where the table
 // has none (past its width, or an entry outside the pool): such tokens are
-// neither read nor written.
+// neither read nor written.  max_blocks is at least 1.
 __device__ __forceinline__ int kv8_page(const Kv8Cache& c, int seq, int token) {
   const int j = token >> c.block_log2;
-  if (j < 0 || j >= c.max_blocks) return -1;
-  const int page = c.table[(size_t)seq * c.max_blocks + j];
-  return page >= 0 && page < c.num_blocks ? page : -1;
+  const int page = c.table[(size_t)seq * c.max_blocks + min(max(j, 0), c.max_blocks - 1)];
+  // one select, no branches around the load: it is to be in flight early
+  return ((unsigned)j < (unsigned)c.max_blocks) & ((unsigned)page < (unsigned)c.num_blocks) ? page : -1;
 }
 
 // New rows of sequence `seq`: [first, first + count) of the packed tokens.
@@ -388,175 +388,255 @@ __device__ __forceinline__ uint32_t kv8_nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u;
 }
 
-// A wave's running state for its 16 rows: lane l holds row l % 16, dimensions
-// 16 i + 4 (l / 16) + e of u in u[i][e], and its own lane group's part of l.
-template <int D>
+// A wave's running state for 16 MT rows: lane l holds, for each tile of 16,
+// row l % 16, dimensions 16 i + 4 (l / 16) + e of u in u[i][e], and its own
+// lane group's part of l.
+template <int D, int MT>
 struct Kv8State {
-  v4f u[D / 16];
-  float m, l;
+  v4f u[MT][D / 16];
+  float m[MT], l[MT];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) u[t][i] = v4f{0.f, 0.f, 0.f, 0.f};
+      m[t] = -__builtin_huge_valf();
+      l[t] = 0.f;
+    }
+  }
 };
 
-// One step: 64 keys from token `base` on.
-template <int D>
-__device__ __forceinline__ void kv8_step(const Kv8AttnParams& p, int seq, int head, const Kv8Seq& sq, int base,
-                                         int row_lo, int row_hi, bool masked, const v8bf (&qf)[D / 32],
-                                         Kv8State<D>& st) {
-  const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
-  const Kv8Cache& c = p.c;
-  // this lane's 16-key run: as a row of K in the first product, and as the
-  // keys of its lane group in p and V^T
-  const int run_k = base + (a >> 2) * 16, run_v = base + g * 16;
-  const int page_k = run_k < sq.kv ? kv8_page(c, seq, run_k) : -1;
-  const int page_v = run_v < sq.kv ? kv8_page(c, seq, run_v) : -1;
-  const int inside = c.block - 1;
-  v4u kw[4][D / 64];
-  {
-    const uint8_t* src = c.k_codes + ((size_t)max(page_k, 0) * c.h_kv + head) * (size_t)c.block * D +
-                         (size_t)((run_k & inside) + (a & 3)) * D + g * 16;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        kw[j][h] = v4u{0, 0, 0, 0};
-        if (page_k >= 0) kw[j][h] = *(const v4u*)(src + j * 4 * D + h * 64);
-      }
-  }
-  v4u vw[D / 16];
-  {
-    const uint8_t* src = c.v_codes + ((size_t)max(page_v, 0) * c.h_kv + head) * (size_t)c.block * D +
-                         (size_t)a * c.block + (run_v & inside);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      vw[i] = v4u{0, 0, 0, 0};
-      if (page_v >= 0) vw[i] = *(const v4u*)(src + (size_t)i * 16 * c.block);
-    }
-  }
-  float ks = 0.f, vs = 1.f;
-  if (page_v >= 0) {
-    ks = c.k_scales[(size_t)page_v * c.h_kv + head];
-    vs = c.v_scales[(size_t)page_v * c.h_kv + head];
-  }
-  ks *= p.scale_log2;
-  vs = fmaxf(vs, kKv8MinVs);
-  const float lv = __builtin_amdgcn_logf(vs), inv_vs = __builtin_amdgcn_rcpf(vs);
+// Where a lane's rows stand: keys [lo, hi) that its row of each tile sees.
+template <int MT>
+struct Kv8Rows {
+  int lo[MT], hi[MT];
+};
 
-  // t[4 j + e]: key run_v + 4 j + e of row a
-  float t[16];
+// The block that holds the 16 keys of this lane group's run, and its scales.
+struct Kv8Run {
+  int page;
+  float ks, vs;
+};
+
+__device__ __forceinline__ Kv8Run kv8_run(const Kv8Cache& c, int head, int page) {
+  const size_t at = (size_t)max(page, 0) * c.h_kv + head;
+  return Kv8Run{page, c.k_scales[at], c.v_scales[at]};
+}
+
+// One step: 64 keys from token `base` on, against 16 MT rows.  load_k(j, h)
+// gives the lane's 16 bytes h * 64 + 16 g .. of key (a / 4) * 16 + 4 j + a % 4,
+// load_v(i) those of dimension 16 i + a at keys 16 g .. (a = lane % 16, g =
+// lane / 16).  `masked`: some row does not see some of the keys, or the
+// sequence ends or the table lacks a block inside the step.
+template <int D, int MT, class LoadK, class LoadV>
+__device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Run& run, float scale_log2, bool masked,
+                                         const Kv8Rows<MT>& rows, const v8bf (&qf)[MT][D / 32],
+                                         Kv8State<D, MT>& st, LoadK load_k, LoadV load_v) {
+  const int run_v = base + ((threadIdx.x & 63) >> 4) * 16;
+  const bool there = run.page >= 0;
+  const float vs = there ? fmaxf(run.vs, kKv8MinVs) : 1.f;
+  const float inv_vs = __builtin_amdgcn_rcpf(vs);
+  float ks = run.ks * scale_log2, lv = __builtin_amdgcn_logf(vs);
+
+  // s[4 j + e]: raw product with key run_v + 4 j + e; t = s ks + lv
+  float s[MT][16];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    v4f s = {0.f, 0.f, 0.f, 0.f};
+    v4f acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
-      s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_to_bf16(kw[j][h][0], kw[j][h][1]), qf[2 * h], s, 0, 0, 0);
-      s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3_to_bf16(kw[j][h][2], kw[j][h][3]), qf[2 * h + 1], s, 0, 0, 0);
+      const v4u w = load_k(j, h);
+      const v8bf k0 = e4m3_to_bf16(w[0], w[1]), k1 = e4m3_to_bf16(w[2], w[3]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[t][2 * h], acc[t], 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[t][2 * h + 1], acc[t], 0, 0, 0);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t[4 * j + e] = s[e] * ks + lv;
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][4 * j + e] = acc[t][e];
   }
-  uint32_t seen = 0xFFFFu;  // bit i: this row sees key run_v + i
+  uint32_t seen[MT];  // bit i: the row sees key run_v + i
   if (masked) {
-    seen = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const bool in = page_v >= 0 && run_v + i >= row_lo && run_v + i < row_hi;
-      seen |= (in ? 1u : 0u) << i;
-      t[i] = in ? t[i] : -__builtin_huge_valf();
+    for (int t = 0; t < MT; ++t) {
+      seen[t] = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool in = there && run_v + i >= rows.lo[t] && run_v + i < rows.hi[t];
+        seen[t] |= (in ? 1u : 0u) << i;
+        s[t][i] = in ? s[t][i] * ks + lv : -__builtin_huge_valf();
+      }
     }
+    ks = 1.f;
+    lv = 0.f;
   }
-  float m = t[0];
+  v4u pw[MT][2], rest[MT][2];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) m = fmaxf(m, t[i]);
-  m = fmaxf(m, __shfl_xor(m, 16, 64));
-  m = fmaxf(m, __shfl_xor(m, 32, 64));
-  m = fmaxf(m, st.m);
-  const float ref = m == -__builtin_huge_valf() ? 0.f : m;  // nothing seen yet: any finite reference
-  if (__any(m > st.m)) {
-    const float shrink = __builtin_amdgcn_exp2f(st.m - ref);
-    st.l *= shrink;
+  for (int t = 0; t < MT; ++t) {
+    float m = s[t][0];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) st.u[i] *= shrink;
-    st.m = m;
-  }
-  float sum = 0.f;
-  v4u pw[2], rest[2];
+    for (int i = 1; i < 16; ++i) m = fmaxf(m, s[t][i]);
+    m = m * ks + lv;
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    m = fmaxf(m, st.m[t]);
+    const float ref = m == -__builtin_huge_valf() ? 0.f : m;  // nothing seen yet: any finite reference
+    if (__any(m > st.m[t])) {
+      const float shrink = __builtin_amdgcn_exp2f(st.m[t] - ref);
+      st.l[t] *= shrink;
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const float p0 = __builtin_amdgcn_exp2f(t[i] - ref), p1 = __builtin_amdgcn_exp2f(t[i + 1] - ref);
-    sum += p0 + p1;
-    pw[i / 8][(i / 2) & 3] = pack2_f16(p0, p1);
-  }
-  st.l += sum * inv_vs;
-  if (masked) {
-    // Bytes past the sequence's end hold anything: zero them.  A NaN code of
-    // a token that some rows see and others do not must reach the former
-    // only, and 0 * NaN would reach both: such codes are zeroed, and a second
-    // product counts, per row and dimension, the NaN that the row sees.
-    v4u keep;
-    uint32_t bad = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = min(max(sq.kv - (run_v + 4 * i), 0), 4);
-      keep[i] = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+      for (int i = 0; i < D / 16; ++i) st.u[t][i] *= shrink;
+      st.m[t] = m;
     }
+    const float off = lv - ref;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float p0 = __builtin_amdgcn_exp2f(s[t][i] * ks + off), p1 = __builtin_amdgcn_exp2f(s[t][i + 1] * ks + off);
+      sum[(i / 2) & 3] += p0 + p1;
+      const uint32_t both = pack2_f16(p0, p1);
+      pw[t][i / 8][(i / 2) & 3] = both;
+      if (masked) {
+        // What fp16 left of p, as a second fp16: rows that see few keys (all
+        // of them in a masked step) have large outputs that no averaging of
+        // the rounding errors helps; with one piece 5 of 493568 outputs of
+        // prompts of up to 150 tokens were off by more than 70% of 8e-3 |r| +
+        // 1e-3 rms, the worst by 129%, with two in these steps none, the
+        // worst 49% (bf16's own rounding).
+        const v2h hi = __builtin_bit_cast(v2h, both);
+        rest[t][i / 8][(i / 2) & 3] = pack2_f16(p0 - (float)hi[0], p1 - (float)hi[1]);
+      }
+    }
+    st.l[t] += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * inv_vs;
+  }
+  if (!masked) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      vw[i] &= keep;
+      const v4u w = load_v(i);
+      const v8h v0 = e4m3_to_f16(w[0], w[1]), v1 = e4m3_to_f16(w[2], w[3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) bad |= kv8_nan_bytes(vw[i][e]);
+      for (int t = 0; t < MT; ++t)
+        st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, __builtin_bit_cast(v8h, pw[t][0]), st.u[t][i], 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, __builtin_bit_cast(v8h, pw[t][1]), st.u[t][i], 0, 0, 0);
     }
+    return;
+  }
+  // Bytes past the sequence's end, or of a block that is not there, hold
+  // anything: zero them.  A NaN code of a token that some rows see and others
+  // do not must reach the former only, and 0 * NaN would reach both: such
+  // codes are zeroed, and a second product counts, per row and dimension, the
+  // NaN that the row sees.
+  v4u keep;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = there ? min(max(kv - (run_v + 4 * i), 0), 4) : 0;
+    keep[i] = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+  }
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    v4u w = load_v(i) & keep;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad |= kv8_nan_bytes(w[e]);
     if (__any(bad != 0)) {
-      v4u sw[2];
+      v4u ind[2];
 #pragma unroll
-      for (int i = 0; i < 16; i += 2)
-        sw[i / 8][(i / 2) & 3] = (seen >> i & 1 ? 0x3C00u : 0u) | (seen >> i & 2 ? 0x3C000000u : 0u);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t b = kv8_nan_bytes(w[e]);
+        w[e] &= ~(b * 255u);
+        ind[e / 2][2 * (e & 1)] = (b & 1u) * 0x3C00u | (b >> 8 & 1u) * 0x3C000000u;
+        ind[e / 2][2 * (e & 1) + 1] = (b >> 16 & 1u) * 0x3C00u | (b >> 24 & 1u) * 0x3C000000u;
+      }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
+      for (int t = 0; t < MT; ++t) {
         v4f cnt = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          v4u ind;
+          v4u sw;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t b = kv8_nan_bytes(vw[i][2 * h + e]);
-            vw[i][2 * h + e] &= ~(b * 255u);
-            ind[2 * e] = (b & 1u) * 0x3C00u | (b >> 8 & 1u) * 0x3C000000u;
-            ind[2 * e + 1] = (b >> 16 & 1u) * 0x3C00u | (b >> 24 & 1u) * 0x3C000000u;
-          }
-          cnt = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, ind), __builtin_bit_cast(v8h, sw[h]),
+          for (int e = 0; e < 4; ++e)
+            sw[e] = (seen[t] >> (8 * h + 2 * e) & 1u) * 0x3C00u | (seen[t] >> (8 * h + 2 * e + 1) & 1u) * 0x3C000000u;
+          cnt = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, ind[h]), __builtin_bit_cast(v8h, sw),
                                                        cnt, 0, 0, 0);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (cnt[e] > 0.f) st.u[i][e] = __builtin_nanf("");
+          if (cnt[e] > 0.f) st.u[t][i][e] = __builtin_nanf("");
       }
     }
-    // What fp16 left of p, as a second fp16: rows that see few keys (all of
-    // them in a masked step) have large outputs that no averaging of the
-    // rounding errors helps; with one piece 5 of 493568 outputs of prompts of
-    // up to 150 tokens were off by more than 70% of 8e-3 |r| + 1e-3 rms, the
-    // worst by 129%, with two in these steps none, the worst 49% (bf16's own
-    // rounding).
+    const v8h v0 = e4m3_to_f16(w[0], w[1]), v1 = e4m3_to_f16(w[2], w[3]);
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const uint32_t both = pw[i / 8][(i / 2) & 3];
-      const v2h hi = __builtin_bit_cast(v2h, both);
-      rest[i / 8][(i / 2) & 3] = pack2_f16(__builtin_amdgcn_exp2f(t[i] - ref) - (float)hi[0],
-                                           __builtin_amdgcn_exp2f(t[i + 1] - ref) - (float)hi[1]);
+    for (int t = 0; t < MT; ++t) {
+      v4f u = st.u[t][i];
+      u = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, __builtin_bit_cast(v8h, rest[t][0]), u, 0, 0, 0);
+      u = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, __builtin_bit_cast(v8h, rest[t][1]), u, 0, 0, 0);
+      u = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, __builtin_bit_cast(v8h, pw[t][0]), u, 0, 0, 0);
+      st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, __builtin_bit_cast(v8h, pw[t][1]), u, 0, 0, 0);
     }
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        st.u[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e4m3_to_f16(vw[i][2 * h], vw[i][2 * h + 1]),
-                                                         __builtin_bit_cast(v8h, rest[h]), st.u[i], 0, 0, 0);
   }
+}
+
+// The B fragments of one row of q.
+template <int D>
+__device__ __forceinline__ void kv8_load_q(const Kv8AttnParams& p, const Kv8Seq& sq, int head, int row, v8bf (&qf)[D / 32]) {
+  const int g = (threadIdx.x & 63) >> 4;
+  const uint16_t* src = p.q + (long long)(sq.first + row / p.group) * p.q_stride +
+                        (long long)(head * p.group + row % p.group) * D + g * 16;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      st.u[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e4m3_to_f16(vw[i][2 * h], vw[i][2 * h + 1]),
-                                                       __builtin_bit_cast(v8h, pw[h]), st.u[i], 0, 0, 0);
+  for (int h = 0; h < D / 64; ++h) {
+    qf[2 * h] = __builtin_bit_cast(v8bf, *(const v4u*)(src + h * 64));
+    qf[2 * h + 1] = __builtin_bit_cast(v8bf, *(const v4u*)(src + h * 64 + 8));
   }
+}
+
+// Whether a step from token `base` on needs masks, given the keys [all_lo,
+// all_hi) that every row sees (all_hi is at most kv).
+__device__ __forceinline__ bool kv8_masked(int base, int all_lo, int all_hi, int page) {
+  return base < all_lo || base + kKv8Step > all_hi || __any(page < 0);
+}
+
+// A wave's loads of one step straight from the cache into registers.
+template <int D>
+struct Kv8Regs {
+  v4u k[4][D / 64], v[D / 16];
+
+  __device__ __forceinline__ void load_k(const Kv8Cache& c, int head, int base, int page) {
+    const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+    const int run = base + (a >> 2) * 16;
+    const uint8_t* src = c.k_codes + ((size_t)max(page, 0) * c.h_kv + head) * (size_t)(c.block * D) +
+                         (((run & (c.block - 1)) + (a & 3)) * D + g * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) k[j][h] = *(const v4u*)(src + j * 4 * D + h * 64);
+  }
+  __device__ __forceinline__ void load_v(const Kv8Cache& c, int head, int base, int page) {
+    const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+    const int run = base + g * 16;
+    const uint8_t* src = c.v_codes + ((size_t)max(page, 0) * c.h_kv + head) * (size_t)(c.block * D) +
+                         (a * c.block + (run & (c.block - 1)));
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) v[i] = *(const v4u*)(src + i * 16 * c.block);
+  }
+};
+
+// The blocks of this lane's runs in a step: of its row of K (keys (a / 4) * 16
+// of the step on) and of its lane group (keys 16 g on).
+__device__ __forceinline__ void kv8_pages(const Kv8Cache& c, int seq, int kv, int base, int* page_k, int* page_v) {
+  const int lane = threadIdx.x & 63;
+  const int run_k = base + ((lane & 15) >> 2) * 16, run_v = base + (lane >> 4) * 16;
+  const int pk = kv8_page(c, seq, run_k), pv = kv8_page(c, seq, run_v);
+  *page_k = run_k < kv ? pk : -1;
+  *page_v = run_v < kv ? pv : -1;
 }
 
 // Rows are written by 16 threads each: thread part of a row holds D / 16 of
@@ -613,46 +693,66 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
     const int t0 = (int)(rel - (long long)tile_no * sq.steps);
     const int t1 = (int)min((long long)sq.steps, t0 + (end - at));
 
-    // this lane's row: its query as B fragments, and the keys it sees
-    const int row = tile * 16 + a, rows = sq.count * p.group;
-    const int safe = min(row, rows - 1);
-    const int qi = safe / p.group;
-    const uint16_t* src = p.q + (long long)(sq.first + qi) * p.q_stride + (long long)(head * p.group + safe % p.group) * D;
-    v8bf qf[D / 32];
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      qf[2 * h] = __builtin_bit_cast(v8bf, *(const v4u*)(src + h * 64 + g * 16));
-      qf[2 * h + 1] = __builtin_bit_cast(v8bf, *(const v4u*)(src + h * 64 + g * 16 + 8));
-    }
-    int row_lo, row_hi;
-    kv8_sees(p, sq, qi, &row_lo, &row_hi);
+    // this lane's row: its query, and the keys it sees
+    const int rows = sq.count * p.group, row = min(tile * 16 + a, rows - 1);
+    v8bf qf[1][D / 32];
+    kv8_load_q<D>(p, sq, head, row, qf[0]);
+    Kv8Rows<1> see;
+    kv8_sees(p, sq, row / p.group, &see.lo[0], &see.hi[0]);
     // keys that every row of the tile sees, and that any row sees
     int all_lo, all_hi, any_lo, any_hi;
     kv8_sees(p, sq, min(tile * 16 + 15, rows - 1) / p.group, &all_lo, &any_hi);
     kv8_sees(p, sq, tile * 16 / p.group, &any_lo, &all_hi);
-    Kv8State<D> st;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) st.u[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    st.m = -__builtin_huge_valf();
-    st.l = 0.f;
-    for (int t = t0 + wave; t < t1; t += 4) {
-      const int base = (sq.step0 + t) * kKv8Step;
-      if (base >= any_hi || base + kKv8Step <= any_lo) continue;  // no row sees any of it
-      // a step needs masks unless every row sees all of it and the table has all of it
-      bool masked = base < all_lo || base + kKv8Step > all_hi;
-      if (!masked) masked = __any(kv8_page(p.c, seq, base + g * 16) < 0);
-      kv8_step<D>(p, seq, head, sq, base, row_lo, row_hi, masked, qf, st);
+    Kv8State<D, 1> st;
+    st.clear();
+    // Steps that any row sees.  K of the next step is loaded as soon as this
+    // step's product has freed its registers, and so is V: each is in flight
+    // while the rest of the step computes.
+    const int first = max(t0, any_lo / kKv8Step - sq.step0) + wave;
+    const int last = min(t1, (any_hi + kKv8Step - 1) / kKv8Step - sq.step0);
+    if (first < last) {
+      Kv8Regs<D> regs;
+      int base = (sq.step0 + first) * kKv8Step, pk, pv, next_pk, next_pv;
+      kv8_pages(p.c, seq, sq.kv, base, &pk, &pv);
+      kv8_pages(p.c, seq, sq.kv, base + 4 * kKv8Step, &next_pk, &next_pv);
+      regs.load_k(p.c, head, base, pk);
+      Kv8Run run = kv8_run(p.c, head, pv);
+      regs.load_v(p.c, head, base, pv);
+      for (int t = first; t < last; t += 4) {
+        const bool more = t + 4 < last;
+        const bool masked = kv8_masked(base, all_lo, all_hi, pv);
+        const Kv8Run now = run;
+        const int here = base;
+        base += 4 * kKv8Step;
+        pk = next_pk;
+        pv = next_pv;
+        kv8_pages(p.c, seq, sq.kv, base + 4 * kKv8Step, &next_pk, &next_pv);
+        kv8_step<D, 1>(sq.kv, here, now, p.scale_log2, masked, see, qf, st,
+                       [&](int j, int h) {
+                         const v4u w = regs.k[j][h];
+                         return w;
+                       },
+                       [&](int i) {
+                         if (i == 0 && more) {
+                           regs.load_k(p.c, head, base, pk);
+                           run = kv8_run(p.c, head, pv);
+                         }
+                         const v4u w = regs.v[i];
+                         return w;
+                       });
+        if (more) regs.load_v(p.c, head, base, pv);
+      }
     }
     // the waves' states, merged in LDS
-    st.l += __shfl_xor(st.l, 16, 64);
-    st.l += __shfl_xor(st.l, 32, 64);
+    st.l[0] += __shfl_xor(st.l[0], 16, 64);
+    st.l[0] += __shfl_xor(st.l[0], 32, 64);
     __syncthreads();
     if (g == 0) {
-      s_m[wave][a] = st.m;
-      s_l[wave][a] = st.l;
+      s_m[wave][a] = st.m[0];
+      s_l[wave][a] = st.l[0];
     }
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) *(v4f*)&s_u[wave][a][i * 16 + g * 4] = st.u[i];
+    for (int i = 0; i < D / 16; ++i) *(v4f*)&s_u[wave][a][i * 16 + g * 4] = st.u[0][i];
     __syncthreads();
     {
       const int r = tid >> 4, part = tid & 15;
@@ -717,6 +817,129 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttnParams p) {
     }
   }
   kv8_write<D>(p, sq, head, tile * 16 + r, part, u, m, l);
+}
+
+// Where the 16-byte piece `part` of row `row` lies in an LDS tile of rows of
+// `kParts` pieces: the 16 lanes that read one piece each of rows 0..15 of a
+// tile then fall on all 64 banks once.
+template <int kParts>
+__device__ __forceinline__ int kv8_slot(int row, int part) {
+  constexpr int kShift = kParts == 4 ? 2 : kParts == 8 ? 1 : 0;
+  return row * kParts + (part ^ ((row >> kShift) & (kParts - 1)));
+}
+
+// Prompts: one workgroup takes 64 MT rows of one key/value head, 16 MT of them
+// a wave, and walks all keys that they see.  Each step's codes go to LDS once
+// for the four waves, in two buffers: while one is worked on, the next step's
+// pieces are on their way to registers, and from there to the other.
+template <int D, int MT>
+__global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
+  constexpr int kRows = 64 * MT, kParts = D / 16, kPer = D / 64;
+  __shared__ v4u s_k[2][64 * kParts], s_v[2][D * 4];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, a = lane & 15, g = lane >> 4;
+  const int head = blockIdx.x, seq = blockIdx.y;
+  const int tile = gridDim.z - 1 - blockIdx.z;  // rows that see the most keys start first
+  const Kv8Seq sq = kv8_seq(p, seq);
+  const int rows = sq.count * p.group, row0 = tile * kRows;
+  if (row0 >= rows) return;
+  const Kv8Cache& c = p.c;
+
+  // keys that any row of the workgroup sees, and this wave's rows
+  int any_lo, any_hi, unused;
+  kv8_sees(p, sq, row0 / p.group, &any_lo, &unused);
+  kv8_sees(p, sq, (min(row0 + kRows, rows) - 1) / p.group, &unused, &any_hi);
+  const int wave0 = row0 + wave * 16 * MT, wave1 = min(wave0 + 16 * MT, rows) - 1;  // none if wave0 > wave1
+  int all_lo = 0, all_hi = 0, wave_lo = 0, wave_hi = 0;
+  if (wave0 <= wave1) {
+    kv8_sees(p, sq, wave1 / p.group, &all_lo, &wave_hi);
+    kv8_sees(p, sq, wave0 / p.group, &wave_lo, &all_hi);
+  }
+  v8bf qf[MT][D / 32];
+  Kv8Rows<MT> see;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int row = min(wave0 + t * 16 + a, rows - 1);
+    kv8_load_q<D>(p, sq, head, row, qf[t]);
+    kv8_sees(p, sq, row / p.group, &see.lo[t], &see.hi[t]);
+  }
+  Kv8State<D, MT> st;
+  st.clear();
+
+  // this thread's pieces of a step: kPer of K, kPer of V
+  int page_k[kPer], page_v, page_run;
+  v4u held_k[kPer], held_v[kPer];
+  auto look = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int run = base + (((tid + 256 * i) / kParts) & ~15);
+      page_k[i] = max(kv8_page(c, seq, run), 0);
+    }
+    page_v = max(kv8_page(c, seq, base + (tid & 3) * 16), 0);
+    const int run = base + g * 16, page = kv8_page(c, seq, run);
+    page_run = run < sq.kv ? page : -1;
+  };
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int key = (tid + 256 * i) / kParts, part = (tid + 256 * i) % kParts;
+      held_k[i] = *(const v4u*)(c.k_codes + ((size_t)page_k[i] * c.h_kv + head) * (size_t)(c.block * D) +
+                                (((base + key) & (c.block - 1)) * D + part * 16));
+      const int d = (tid + 256 * i) >> 2;
+      held_v[i] = *(const v4u*)(c.v_codes + ((size_t)page_v * c.h_kv + head) * (size_t)(c.block * D) +
+                                (d * c.block + ((base + (tid & 3) * 16) & (c.block - 1))));
+    }
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int key = (tid + 256 * i) / kParts, part = (tid + 256 * i) % kParts;
+      // row 16 j + a of the tile is the key that lane a takes in product j
+      const int row = ((key >> 2) & 3) * 16 + (key >> 4) * 4 + (key & 3);
+      s_k[buf][kv8_slot<kParts>(row, part)] = held_k[i];
+      s_v[buf][kv8_slot<4>((tid + 256 * i) >> 2, tid & 3)] = held_v[i];
+    }
+  };
+  const int first = any_lo / kKv8Step, last = (any_hi + kKv8Step - 1) / kKv8Step;
+  if (first < last) {
+    look(first * kKv8Step);
+    fetch(first * kKv8Step);
+    Kv8Run run = kv8_run(c, head, page_run);
+    look((first + 1) * kKv8Step);
+    put(0);
+    __syncthreads();
+    for (int s = first; s < last; ++s) {
+      const int base = s * kKv8Step, buf = (s - first) & 1;
+      const Kv8Run now = run;
+      if (s + 1 < last) {
+        fetch(base + kKv8Step);
+        run = kv8_run(c, head, page_run);
+        look(base + 2 * kKv8Step);
+      }
+      if (base < wave_hi && base + kKv8Step > wave_lo) {
+        const bool masked = kv8_masked(base, all_lo, all_hi, now.page);
+        kv8_step<D, MT>(sq.kv, base, now, p.scale_log2, masked, see, qf, st,
+                        [&](int j, int h) { return s_k[buf][kv8_slot<kParts>(j * 16 + a, h * 4 + g)]; },
+                        [&](int i) { return s_v[buf][kv8_slot<4>(i * 16 + a, g)]; });
+      }
+      if (s + 1 < last) put(buf ^ 1);
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    float l = st.l[t];
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    const int row = wave0 + t * 16 + a;
+    if (row >= rows) continue;
+    const size_t at = (size_t)(sq.first + row / p.group) * p.h_q + head * p.group + row % p.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // l == 0: the row sees no key
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      *(v2u*)(p.out + at * D + i * 16 + g * 4) = v2u{pack2_bf16(st.u[t][i][0] * inv, st.u[t][i][1] * inv),
+                                                     pack2_bf16(st.u[t][i][2] * inv, st.u[t][i][3] * inv)};
+    if (p.lse && g == 0) p.lse[at] = (st.m[t] + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+  }
 }
 
 }  // namespace dg

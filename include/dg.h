@@ -405,7 +405,7 @@ int dg_kv8_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_
  *
  *   x[j] = scale * (q . k[j]),  out = sum_j softmax(x)[j] v[j],  lse = log sum_j e^x[j]
  *
- * over the tokens j it sees: those up to its own position if causal, all
+ * with scale >= 0, over the tokens j it sees: those up to its own position if causal, all
  * kv_lens[s] otherwise, and of these the last `window` if window > 0 (causal
  * only).  A row that sees no token gets out = 0 and lse = -inf.  A NaN in a
  * key or value reaches the rows that see it and no others; what the cache

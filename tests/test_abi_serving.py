@@ -73,7 +73,8 @@ def test_append(lib, changed, status):
 
 
 @pytest.mark.parametrize("changed,status", BOTH + [
-    (dict(q=None), 1), (dict(out=None), 1), (dict(lens=None), 1), (dict(window=-1), 1), (dict(window=5, causal=0), 1),
+    (dict(q=None), 1), (dict(out=None), 1), (dict(lens=None), 1), (dict(window=-1), 1), (dict(scale=-0.5), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(window=5, causal=0), 1),
     (dict(h_q=7), 2), (dict(h_q=0), 2), (dict(q_stride=1020), 2), (dict(q_stride=0), 2), (dict(total=1 << 30, most=1 << 30, h_q=64, q_stride=8192), 2),
     (dict(q=ODD), 3), (dict(out=ODD), 3), (dict(lse=OFF4), 3), (dict(total=0, q=None, out=None), 0),
 ])

@@ -202,8 +202,16 @@ ATTN = [
 ]
 
 
+@pytest.fixture(params=["", "kv8_split", "kv8_prompt"])
+def way(request, monkeypatch):
+    """The library's own choice between its two ways of a call, and each of them."""
+    if request.param:
+        monkeypatch.setenv("DG_FORCE_CONFIG", request.param)
+    return request.param
+
+
 @pytest.mark.parametrize("block,hq,h,d,new,kv,window", ATTN)
-def test_attention(gpu, block, hq, h, d, new, kv, window):
+def test_attention(way, gpu, block, hq, h, d, new, kv, window):
     print(f"[case] attention block {block} heads {hq}/{h} d {d} {new} {kv} window {window}", flush=True)
     rng = np.random.default_rng(block + hq + d + len(kv))
     cache, table = make_cache(rng, kv, block, h, d)
@@ -217,7 +225,7 @@ def test_attention(gpu, block, hq, h, d, new, kv, window):
 
 
 @pytest.mark.parametrize("new,kv,hq", [([1, 1], [100, 3], 4), ([20, 7], [200, 7], 8)])
-def test_attention_not_causal_and_without_lse(gpu, new, kv, hq):
+def test_attention_not_causal_and_without_lse(way, gpu, new, kv, hq):
     rng = np.random.default_rng(21)
     cache, table = make_cache(rng, kv, 32, 2, 64)
     cu = running(new)
@@ -228,7 +236,7 @@ def test_attention_not_causal_and_without_lse(gpu, new, kv, hq):
     assert oracle.tolerance_check(out, kv8.attention_ref(q, cache, table, kv, cu, 0.125)[0])["ok"]
 
 
-def test_attention_large_scores_and_far_scales(gpu):
+def test_attention_large_scores_and_far_scales(way, gpu):
     # scores of +-200 (a one-hot softmax), value scales 2^40 apart, some blocks' values zero
     rng = np.random.default_rng(22)
     cache, table = make_cache(rng, [300], 64, 1, 64)
@@ -275,11 +283,11 @@ def nan_case(gpu, new, kv, hq, where, in_values, window=0):
 @pytest.mark.parametrize("in_values", [False, True])
 @pytest.mark.parametrize("new,kv,hq,where,window", [(1, 100, 4, 50, 0), (10, 100, 4, 95, 0), (40, 100, 2, 70, 0), (150, 200, 4, 100, 0),
                                                     (1, 100, 4, 20, 30), (40, 100, 2, 40, 30), (150, 200, 4, 60, 20)])
-def test_attention_nan(gpu, new, kv, hq, where, window, in_values):
+def test_attention_nan(way, gpu, new, kv, hq, where, window, in_values):
     nan_case(gpu, new, kv, hq, where, in_values, window)
 
 
-def test_attention_skips_tokens_that_the_table_does_not_have(gpu):
+def test_attention_skips_tokens_that_the_table_does_not_have(way, gpu):
     rng = np.random.default_rng(24)
     cache, table = make_cache(rng, [200, 100], 32, 2, 64)
     table[0, 2], table[1, 0] = -1, 2 ** 30
@@ -294,7 +302,7 @@ def test_attention_skips_tokens_that_the_table_does_not_have(gpu):
     hold([x[10:] for x in got], [x[10:] for x in want])
 
 
-def test_attention_strided_queries_and_other_stream(gpu):
+def test_attention_strided_queries_and_other_stream(way, gpu):
     rng = np.random.default_rng(25)
     cache, table = make_cache(rng, [150, 40], 64, 2, 128)
     wide = bf16(rng.standard_normal((6, 8 + 5, 128)))
@@ -311,6 +319,18 @@ def test_attention_strided_queries_and_other_stream(gpu):
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     hold((H.d_float(out), lse.cpu().numpy().astype(np.float64)), want)
+
+
+def test_attention_many_prompts(gpu):
+    # enough rows for the way of prompts to be chosen, lengths of all kinds
+    rng = np.random.default_rng(29)
+    new = [int(x) for x in rng.integers(0, 40, 64)]
+    new[5] = 48
+    kv = [n + int(x) for n, x in zip(new, rng.integers(0, 90, 64))]
+    cache, table = make_cache(rng, kv, 32, 4, 64)
+    cu = running(new)
+    q = bf16(rng.standard_normal((cu[-1], 8, 64)))
+    hold(attend(gpu, q, cache, table, kv, cu), kv8.attention_ref(q, cache, table, kv, cu, 0.125))
 
 
 def test_attention_many_sequences(gpu):
