@@ -40,7 +40,7 @@ __all__ = [
     "k_grouped_fp8_gemm_nt", "bf16_gemm_nt", "fp4_gemm_nt", "quantize_a_1x128_fp4", "quantize_b_128x128_fp4", "get_m_alignment_for_contiguous_layout", "get_sfa_ld", "empty_sfa",
     "profile_next_launch",
     "reserve_workspace", "dense_workspace_size",
-    "bf16_w4_gemm_nt", "quantize_b_w4", "dequantize_b_w4",
+    "bf16_w4_gemm_nt", "bf16_w4_workspace_size", "quantize_b_w4", "dequantize_b_w4",
     "empty_kv8_cache", "kv8_append", "kv8_attention", "kv8_attention_workspace_size",
 ]
 
@@ -78,6 +78,7 @@ _SIGNATURES = {
     "dg_reserve_workspace": [ctypes.c_size_t, _vp],
     "dg_dense_workspace_size": [_ci, _ci, _ci, _ci, ctypes.POINTER(ctypes.c_size_t)],
     "dg_bf16_w4_gemm_nt": [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _vp],
+    "dg_bf16_w4_workspace_size": [_ci, _ci, _ci, _ci, _ci, ctypes.POINTER(ctypes.c_size_t)],
     "dg_quantize_b_w4": [_vp, _ci, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _vp],
     "dg_dequantize_b_w4": [_vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _vp],
     "dg_kv8_append": [_vp, _cl, _vp, _cl] + [_vp] * 7 + [_ci] * 8 + [_vp],
@@ -110,7 +111,8 @@ def _check(status):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """Handle of the current stream (as torch.cuda.current_stream().cuda_stream, 3.0 us, in 0.3 us)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t):
@@ -461,8 +463,8 @@ def _w4_shape(b_triple):
     _need(codes, "codes", (torch.uint8,), 2)
     _need(scales, "scales", (torch.bfloat16,), 2)
     n, kh = codes.shape
-    groups = scales.shape[1]
-    if groups < 1 or scales.shape[0] != n or 2 * kh % groups:
+    rows, groups = scales.shape
+    if groups < 1 or rows != n or 2 * kh % groups:
         raise ValueError(f"scales {tuple(scales.shape)} do not fit codes {tuple(codes.shape)}")
     if zeros is not None:
         _need(zeros, "zeros", (torch.uint8,), 2)
@@ -477,13 +479,23 @@ def bf16_w4_gemm_nt(a, b_triple, d):
     _need(a, "a", (torch.bfloat16,), 2)
     _need(d, "d", (torch.bfloat16,), 2)
     codes, scales, zeros, n, k, group, fmt = _w4_shape(b_triple)
-    m = a.shape[0]
-    if a.shape[1] != k or d.shape[0] != m or d.shape[1] != n:
+    m, ka = a.shape
+    if ka != k or d.shape != (m, n):
         raise ValueError(f"shape mismatch a{tuple(a.shape)} w({n}, {k}) d{tuple(d.shape)}")
     _check(lib().dg_bf16_w4_gemm_nt(a.data_ptr(), codes.data_ptr(), scales.data_ptr(),
                                     None if zeros is None else zeros.data_ptr(), d.data_ptr(), m, n, k, group, fmt,
                                     _stream()))
     return d
+
+
+def bf16_w4_workspace_size(m, n, k, group=128, fmt="e2m1"):
+    """Bytes of a stream's workspace that bf16_w4_gemm_nt takes for a shape;
+    give it to reserve_workspace before capturing such calls."""
+    if fmt not in _W4_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(_W4_FORMATS)}")
+    size = ctypes.c_size_t(0)
+    _check(lib().dg_bf16_w4_workspace_size(int(m), int(n), int(k), int(group), _W4_FORMATS[fmt], ctypes.byref(size)))
+    return size.value
 
 
 def quantize_b_w4(x, fmt="e2m1", group=128):
@@ -533,8 +545,8 @@ def _kv8_shape(cache, block_table, lens, cu):
     _need(lens, "lens", (torch.int32,), 1)
     _need(cu, "cu", (torch.int32,), 1)
     num_blocks, h_kv, block, d = k_codes.shape
-    if (tuple(v_codes.shape) != (num_blocks, h_kv, d, block) or tuple(k_scales.shape) != (num_blocks, h_kv)
-            or tuple(v_scales.shape) != (num_blocks, h_kv)):
+    per_head = (num_blocks, h_kv)
+    if v_codes.shape != (num_blocks, h_kv, d, block) or k_scales.shape != per_head or v_scales.shape != per_head:
         raise ValueError("cache shape mismatch")
     batch, max_blocks = block_table.shape
     if lens.shape[0] != batch or cu.shape[0] != batch + 1:
@@ -583,11 +595,11 @@ def kv8_attention(q, cache, block_table, kv_lens, cu_q, max_q, out, lse=None, sc
     _need(out, "out", (torch.bfloat16,), 3)
     h_q = out.shape[1]
     total, stride = _packed(q, "q", h_q, d)
-    if out.shape[0] != total or out.shape[2] != d:
+    if out.shape != (total, h_q, d):
         raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
     if lse is not None:
         _need(lse, "lse", (torch.float32,), 2)
-        if lse.shape[0] != total or lse.shape[1] != h_q:
+        if lse.shape != (total, h_q):
             raise ValueError(f"lse must be {(total, h_q)}, got {tuple(lse.shape)}")
     k_codes, v_codes, k_scales, v_scales = cache
     _check(lib().dg_kv8_attention(q.data_ptr(), stride, k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),

@@ -862,28 +862,71 @@ int check_w4(int n, int k, int group, int format, const void* zeros) {
   if (n < 1) return fail(DG_ERR_INVALID_ARGUMENT, "n must be >= 1 (got %d)", n);
   if (group != 32 && group != 64 && group != 128)
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "group must be 32, 64 or 128 (got %d)", group);
+  if (k > (1 << 23)) return fail(DG_ERR_UNSUPPORTED_SHAPE, "k must be at most 2^23 (got %d)", k);  // 32-bit offsets
   if (k < group || k % group != 0)
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "k must be a positive multiple of the group of %d (got %d)", group, k);
   return DG_OK;
 }
 
-struct W4Kernel {
+// How a product is launched: up to 16 rows of a, workgroups of 16 weight rows
+// whose waves split K; more, tiles of 128 weight rows by 32 or 64 rows of a
+// and K in splits.
+struct W4Plan {
   const void* fn;
-  int rows, cols, threads;  // of d, per workgroup; threads of it
+  dim3 grid;
+  int threads, smem;
+  size_t partial_bytes;  // split tiles, 0 if K is not split
+  int tiles;
 };
 
+template <int FMT, int GROUP, bool WHOLE>
+W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
+  const int units = (k + 127) / 128;
+  if (m <= 16) {
+    // about 16 waves per CU, and a unit or more for each of them
+    const dim3 grid((n + 15) / 16);
+    const long long want = 16LL * info->cus / grid.x;
+    int waves = want > 8 && units >= 16 ? 16 : want > 4 && units >= 8 ? 8 : 4;
+    if (m <= 4)
+      return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 2, 4, WHOLE>), grid, waves * 64,
+              dg::w4_rows_smem<FMT, GROUP, 2, 4, WHOLE>(waves), 0, 0};
+    if (m <= 8)
+      return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 8, WHOLE>), grid, waves * 64,
+              dg::w4_rows_smem<FMT, GROUP, 1, 8, WHOLE>(waves), 0, 0};
+    if (waves > 8) waves = 8;  // 64 KB of LDS
+    return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 16, WHOLE>), grid, waves * 64,
+            dg::w4_rows_smem<FMT, GROUP, 1, 16, WHOLE>(waves), 0, 0};
+  }
+  const int rows = m <= 32 ? 32 : 64;
+  const int tiles_n = (n + 127) / 128, tiles_m = (m + rows - 1) / rows;
+  const long long tiles = (long long)tiles_n * tiles_m;
+  // two workgroups per CU, at least four units a split
+  long long splits = 2LL * info->cus / tiles;
+  if (splits > units / 4) splits = units / 4;
+  if (splits > 16) splits = 16;
+  if (const char* e = getenv("DG_SPLIT_K")) splits = atoi(e) < units ? atoi(e) : units;
+  if (splits < 1 || tiles > (long long)kCounterInts) splits = 1;
+  return {rows == 32 ? reinterpret_cast<const void*>(&dg::w4_tile_kernel<FMT, GROUP, 2, WHOLE>)
+                     : reinterpret_cast<const void*>(&dg::w4_tile_kernel<FMT, GROUP, 4, WHOLE>),
+          dim3(tiles_n, (unsigned)splits, tiles_m), 256, 0,
+          splits > 1 ? (size_t)tiles * splits * rows * 128 * sizeof(float) : 0, (int)tiles};
+}
+
 template <int FMT, int GROUP>
-W4Kernel w4_pick(int m) {
-  if (m <= 16)
-    return {reinterpret_cast<const void*>(&dg::w4_gemm_kernel<FMT, GROUP, 1, 1, 8, 2>), 16, 16, 512};
-  if (m <= 32)
-    return {reinterpret_cast<const void*>(&dg::w4_gemm_kernel<FMT, GROUP, 2, 2, 8, 1>), 32, 32, 512};
-  return {reinterpret_cast<const void*>(&dg::w4_gemm_kernel<FMT, GROUP, 4, 2, 8, 1>), 64, 32, 512};
+W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
+  if constexpr (GROUP == 128) return w4_plan<FMT, GROUP, true>(m, n, k, info);
+  return k % 128 == 0 ? w4_plan<FMT, GROUP, true>(m, n, k, info) : w4_plan<FMT, GROUP, false>(m, n, k, info);
 }
 
 template <int FMT>
-W4Kernel w4_pick(int m, int group) {
-  return group == 32 ? w4_pick<FMT, 32>(m) : group == 64 ? w4_pick<FMT, 64>(m) : w4_pick<FMT, 128>(m);
+W4Plan w4_plan(int m, int n, int k, int group, const DeviceInfo* info) {
+  return group == 32   ? w4_plan<FMT, 32>(m, n, k, info)
+         : group == 64 ? w4_plan<FMT, 64>(m, n, k, info)
+                       : w4_plan<FMT, 128>(m, n, k, info);
+}
+
+W4Plan w4_plan(int m, int n, int k, int group, int format, const DeviceInfo* info) {
+  return format == DG_W4_E2M1 ? w4_plan<dg::kW4E2m1>(m, n, k, group, info) : w4_plan<dg::kW4U4>(m, n, k, group, info);
 }
 
 template <int FMT, bool BF16>
@@ -900,10 +943,10 @@ const void* w4_dequant_fn(int group) {
                        : reinterpret_cast<const void*>(&dg::w4_dequant_kernel<FMT, 128>);
 }
 
-int launch_plain(const char* what, const void* fn, dim3 grid, int threads, void** args, dg_stream_t stream) {
+int launch_plain(const char* what, const void* fn, dim3 grid, int threads, void** args, dg_stream_t stream, int smem = 0) {
   if (log_enabled())
     fprintf(stderr, "[dg] %s grid=%ux%ux%u threads=%d\n", what, grid.x, grid.y, grid.z, threads);
-  hipError_t e = hipLaunchKernel(fn, grid, dim3(threads), args, 0, (hipStream_t)stream);
+  hipError_t e = hipLaunchKernel(fn, grid, dim3(threads), args, smem, (hipStream_t)stream);
   if (e != hipSuccess) return fail(DG_ERR_HIP, "launch of %s failed: %s", what, hipGetErrorString(e));
   return ok();
 }
@@ -1357,11 +1400,31 @@ int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* 
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
-  const W4Kernel w = format == DG_W4_E2M1 ? w4_pick<dg::kW4E2m1>(m, group) : w4_pick<dg::kW4U4>(m, group);
-  if ((m + w.rows - 1) / w.rows > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m too large (%d)", m);
-  dg::W4Params p{a, codes, scales, zeros, d, m, n, k};
+  const W4Plan w = w4_plan(m, n, k, group, format, info);
+  if (w.grid.z > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m too large (%d)", m);
+  dg::W4Params p{a, codes, scales, zeros, d, m, n, k, nullptr, nullptr};
+  if (w.partial_bytes) {
+    char* base = nullptr;
+    if (int s = ensure_workspace(dev, (hipStream_t)stream, w.partial_bytes, &base)) return s;
+    p.count = (int*)base;
+    p.partial = (float*)(base + kWsHeader);
+  }
   void* args[] = {&p};
-  return launch_plain("w4_gemm", w.fn, dim3((n + w.cols - 1) / w.cols, (m + w.rows - 1) / w.rows), w.threads, args, stream);
+  return launch_plain("w4_gemm", w.fn, w.grid, w.threads, args, stream, w.smem);
+}
+
+int dg_bf16_w4_workspace_size(int m, int n, int k, int group, int format, size_t* bytes) {
+  if (!bytes) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  *bytes = 0;
+  if (m < 0) return fail(DG_ERR_INVALID_ARGUMENT, "m must be >= 0 (got %d)", m);
+  const uint8_t any = 0;
+  if (int s = check_w4(n, k, group, format, format == DG_W4_U4 ? &any : nullptr)) return s;
+  if (m == 0) return ok();
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  *bytes = w4_plan(m, n, k, group, format, info).partial_bytes;
+  return ok();
 }
 
 int dg_quantize_b_w4(const void* x, int x_bf16, uint8_t* codes, uint16_t* scales, uint8_t* zeros, int n, int k,

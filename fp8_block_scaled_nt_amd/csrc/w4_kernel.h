@@ -64,8 +64,12 @@ __device__ __forceinline__ v8bf w4_widen(uint32_t w) {
     r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
     r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
   } else {
+    // in registers, so that mask and bias are one v_and_or_b32
+    uint32_t mask = 0x000F000Fu, bias = 0x43004300u;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(bias));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    for (int i = 0; i < 4; ++i) r[i] = ((w >> (4 * i)) & mask) | bias;
   }
   return __builtin_bit_cast(v8bf, r);
 }
@@ -106,81 +110,126 @@ struct W4Params {
   const uint8_t* zeros;    // [n][k/group], u4 only
   uint16_t* d;             // [m][n] bf16
   int m, n, k;
+  float* partial;  // w4_tile_kernel with splits: [tiles][splits] partial tiles
+  int* count;      // and their arrival counters, zero between calls
 };
 
-// One unit (128 of K) of a wave's operands, as loaded.
-template <int GROUP, int MT, int NT>
-struct W4Unit {
-  static constexpr int kGroups = 128 / GROUP;
-  v4u w[NT];
-  v4u a[MT][4];
-  uint16_t s[NT][kGroups];
-  uint8_t z[NT][kGroups];
-};
-
-template <int FMT, int GROUP, int MT, int NT>
-__device__ __forceinline__ void w4_load(const W4Params& p, int n0, int m0, int u, W4Unit<GROUP, MT, NT>& t) {
-  constexpr int kG = W4Unit<GROUP, MT, NT>::kGroups;
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int k0 = u * 128;
-  // quarters of the unit inside K (always four when groups are 128 wide)
-  const int quarters = GROUP == 128 ? 4 : min(4, (p.k - k0) / 32);
-  const int groups = quarters * 32 / GROUP;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const size_t row = (size_t)min(n0 + i * 16 + r, p.n - 1);
-    t.w[i] = v4u{0, 0, 0, 0};
-    if (q < quarters) t.w[i] = *(const v4u*)(p.codes + row * (size_t)(p.k / 2) + k0 / 2 + q * 16);
-    const size_t g0 = row * (size_t)(p.k / GROUP) + (size_t)u * kG;
-#pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      const int gg = min(g, groups - 1);
-      t.s[i][g] = p.scales[g0 + gg];
-      if constexpr (FMT == kW4U4) t.z[i][g] = p.zeros[g0 + gg];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const uint16_t* row = p.a + (size_t)min(m0 + i * 16 + r, p.m - 1) * p.k + k0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int jj = min(j, quarters - 1);
-      t.a[i][j] = *(const v4u*)(row + (GROUP == 128 ? q * 32 + j * 8 : jj * 32 + q * 8));
-    }
-  }
+// Quarters (32 of K) of unit u that lie inside K; K is a multiple of 32, and
+// WHOLE says of 128.
+template <bool WHOLE>
+__device__ __forceinline__ int w4_quarters(int k, int u) {
+  return WHOLE ? 4 : max(0, min(4, (k - u * 128) / 32));
 }
 
-template <int FMT, int GROUP, int MT, int NT>
-__device__ __forceinline__ void w4_accumulate(const W4Params& p, int u, W4Unit<GROUP, MT, NT>& t,
-                                              v4f (&acc)[MT][NT]) {
-  constexpr int kG = W4Unit<GROUP, MT, NT>::kGroups;
-  constexpr int kPer = 4 / kG;  // quarters of a group
-  const int groups = GROUP == 128 ? 1 : min(4, (p.k - u * 128) / 32) / kPer;
+constexpr uint32_t kW4Nowhere = 0x80000000u;  // a byte offset past every buffer here (k is at most 2^23)
+
+// 16 weight rows of a wave, and the way of their codes and scales from memory
+// to the lanes that use them.
+//
+// The matrix instruction wants row l % 16 in lane l.  Loaded that way, no two
+// neighbouring lanes read the same cache line, and a load of 1 KB takes the
+// CU's vector memory pipe 64 cycles, one for every lane (so did one of 64
+// scales: 23 us for 1 x 7168 x 16384, whether it came from HBM or L2, and as
+// much per unit with 4 workgroups on the GPU as with 448).  So lane l loads
+// piece l % 4 of row l / 4, four lanes a line, and the codes change lanes in
+// LDS of the wave's own (no barrier: a wave's LDS instructions are in order).
+// Scales come 64 at a time: four a row, which is 4 / (128 / GROUP) units.
+//
+// Loads are never under a branch, where the compiler could not count them and
+// would wait for all that are in flight: past the last unit, or outside the
+// matrix, they go to an offset past the buffer's end, which gives zeros and no
+// memory traffic.
+template <int FMT, int GROUP, bool WHOLE>
+struct W4Rows {
+  static constexpr int kG = 128 / GROUP;  // groups of a unit
+  static constexpr int kSU = 4 / kG;      // units of a load of scales
+  static constexpr int kLds = 64 * 16 + 2 * 64 * 4;
+
+  __amdgpu_buffer_rsrc_t codes, scales, zeros;
+  uint32_t at_codes, at_group;  // of this lane's row, in bytes and in groups
+  int groups, k;
+
+  __device__ __forceinline__ W4Rows(const W4Params& p, int n0) {
+    k = p.k;
+    groups = p.k / GROUP;
+    const int base = min(n0, p.n - 1), rows = n0 < p.n ? min(p.n - n0, 16) : 0, r = (threadIdx.x & 63) >> 2;
+    codes = __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + (size_t)base * (k / 2)), 0, rows * (k / 2), kBufferRsrcWord3);
+    scales = __builtin_amdgcn_make_buffer_rsrc((void*)(p.scales + (size_t)base * groups), 0, rows * groups * 2, kBufferRsrcWord3);
+    zeros = scales;
+    if constexpr (FMT == kW4U4)
+      zeros = __builtin_amdgcn_make_buffer_rsrc((void*)(p.zeros + (size_t)base * groups), 0, rows * groups, kBufferRsrcWord3);
+    at_codes = (uint32_t)r * (uint32_t)(k / 2) + (threadIdx.x & 3) * 16;
+    at_group = (uint32_t)r * (uint32_t)groups;
+  }
+
+  // This lane's piece of unit u of `units`.
+  __device__ __forceinline__ v4u load(int u, int units) const {
+    const bool in = u < units && (WHOLE || (int)(threadIdx.x & 3) < w4_quarters<WHOLE>(k, u));
+    const auto w = __builtin_amdgcn_raw_buffer_load_b128(codes, in ? at_codes + u * 64 : kW4Nowhere, 0, 0);
+    return __builtin_bit_cast(v4u, w);
+  }
+  // This lane's scale and zero of units u, u + step, ..
+  __device__ __forceinline__ void load_scales(int u, int step, uint32_t& s, uint32_t& z) const {
+    const int part = threadIdx.x & 3, g = (u + part / kG * step) * kG + part % kG;
+    const uint32_t at = g < groups ? at_group + g : kW4Nowhere / 2;
+    s = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales, at * 2, 0, 0);
+    if constexpr (FMT == kW4U4) z = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zeros, at, 0, 0);
+  }
+  // Into the wave's LDS, and out of it for row l % 16: quarter l / 16 of the
+  // codes; the scales (and what zero points subtract: 128 + z).
+  static __device__ __forceinline__ void put(uint8_t* lds, v4u w) {
+    const int r = (threadIdx.x & 63) >> 2, part = threadIdx.x & 3;
+    ((v4u*)lds)[r * 4 + (part ^ ((r >> 2) & 3))] = w;
+  }
+  static __device__ __forceinline__ v4u get(const uint8_t* lds) {
+    const int r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+    return ((const v4u*)lds)[r * 4 + (q ^ ((r >> 2) & 3))];
+  }
+  static __device__ __forceinline__ void put_scales(uint8_t* lds, uint32_t s, uint32_t z) {
+    ((uint32_t*)(lds + 1024))[threadIdx.x & 63] = s << 16;
+    if constexpr (FMT == kW4U4) ((float*)(lds + 1280))[threadIdx.x & 63] = (float)(z + 128u);
+  }
+  static __device__ __forceinline__ void get_scales(const uint8_t* lds, v4f& s, v4f& z) {
+    s = ((const v4f*)(lds + 1024))[threadIdx.x & 15];
+    if constexpr (FMT == kW4U4) z = ((const v4f*)(lds + 1280))[threadIdx.x & 15];
+  }
+};
+
+// Adds a unit's products with MT tiles of 16 rows of A to acc (lane l: weight
+// row l % 16, row 4 (l / 16) + e of A for e < E).  w, s and z are the unit's
+// codes, scales and zeros as W4Rows gives them, `first` the unit's first scale
+// among the four.  load_a(t, j) gives tile t's fragment for quarter-wide
+// product j, in the order that w4_widen leaves K in.
+template <int FMT, int GROUP, int MT, int NT, int E, bool WHOLE, class LoadA>
+__device__ __forceinline__ void w4_accumulate(int k, int u, v4u (&w)[NT], const v4f (&s)[NT], const v4f (&z)[NT],
+                                              int first, float (&acc)[MT][NT][E], LoadA load_a) {
+  constexpr int kG = 128 / GROUP;
+  constexpr int kPer = 4 / kG;  // products of a group
+  const int groups = w4_quarters<WHOLE>(k, u) / kPer;
   if constexpr (GROUP < 128) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) w4_transpose(t.w[i]);
+    for (int i = 0; i < NT; ++i) w4_transpose(w[i]);
   }
   const v4u one4 = v4u{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   const v8bf ones = __builtin_bit_cast(v8bf, one4);
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
-    if (GROUP < 128 && g >= groups) break;
+    if (!WHOLE && g >= groups) break;
     v8bf b[NT][kPer];
-    float s[NT], z[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) b[i][j] = w4_widen<FMT>(t.w[i][g * kPer + j]);
-      s[i] = bf16_to_f32(t.s[i][g]);
-      z[i] = FMT == kW4U4 ? 128.f + (float)t.z[i][g] : 0.f;
-    }
+      for (int j = 0; j < kPer; ++j) {
+        const uint32_t eight = w[i][g * kPer + j];
+        b[i][j] = w4_widen<FMT>(eight);
+      }
 #pragma unroll
     for (int mi = 0; mi < MT; ++mi) {
       v8bf a[kPer];
       v4f sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        a[j] = w4_order_a<FMT>(t.a[mi][g * kPer + j]);
+        a[j] = load_a(mi, g * kPer + j);
         if constexpr (FMT == kW4U4) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], ones, sum, 0, 0, 0);
       }
 #pragma unroll
@@ -189,57 +238,272 @@ __device__ __forceinline__ void w4_accumulate(const W4Params& p, int u, W4Unit<G
 #pragma unroll
         for (int j = 0; j < kPer; ++j) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], b[i][j], part, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (FMT == kW4U4) part[e] -= z[i] * sum[e];
-          acc[mi][i][e] += s[i] * part[e];
+        for (int e = 0; e < E; ++e) {
+          if constexpr (FMT == kW4U4) part[e] -= z[i][first + g] * sum[e];
+          acc[mi][i][e] += s[i][first + g] * part[e];
         }
       }
     }
   }
 }
 
-template <int FMT, int GROUP, int MT, int NT, int WAVES, int DEPTH>
-__global__ __launch_bounds__(WAVES * 64) void w4_gemm_kernel(W4Params p) {
-  __shared__ v4f red[WAVES][MT * NT][64];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT;
+// Up to 16 rows of a: a workgroup takes 16 weight rows, and its waves (4 to
+// 16) every so many-th unit of K each.  A wave keeps kDepth units of weights
+// in flight and refills a unit's registers as soon as it is used.
+//
+// a is the same for all workgroups and comes from L2, but a fragment of it is
+// 16 rows wide whatever m is.  So each wave loads U units of at most kW4Rows(U)
+// rows densely, a chunk ahead, and turns them into fragments through its LDS.
+// Row i of a becomes row 4 (i % 4) + i / 4 of A: of the four sums that a lane
+// has of every product, only the first E are then of rows below m, and only
+// these are scaled.
+//
+// One copy of the four units' code, for every number of units: most waves pass
+// through once or twice, and what they do not find in the instruction cache
+// costs them more than a branch a unit (with separate code for the last units
+// 7.4 us for 5 x 1001 x 1056, without 4.2).
+constexpr int kW4Depth = 4;
+// rows of a that U units of it are staged for: 4 for U = 2, 8 or 16 for U = 1
+template <int FMT, int GROUP, int U, int ROWS, bool WHOLE>
+__global__ __launch_bounds__(1024) void w4_rows_kernel(W4Params p) {
+  using Rows = W4Rows<FMT, GROUP, WHOLE>;
+  constexpr int E = ROWS / 4, kLoads = U * ROWS / 4, kChunk = U * ROWS * 256;
+  extern __shared__ __align__(16) uint8_t lds[];  // of each wave: a chunk of a, then Rows::kLds; later the waves' sums
+  const int waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * 16;
   const int units = (p.k + 127) / 128;
-  const int u1 = (int)((long long)units * (wave + 1) / WAVES);
-  v4f acc[MT][NT];
+  const int count = (units - wave + waves - 1) / waves;  // this wave's units: wave, wave + waves, ..
+  v4u* mine = (v4u*)(lds + wave * (kChunk + Rows::kLds));
+  uint8_t* mine_w = (uint8_t*)mine + kChunk;
+  const Rows rows(p, n0);
+  const __amdgpu_buffer_rsrc_t src_a =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.a, 0, p.m * p.k * 2, kBufferRsrcWord3);
+
+  // chunk of a from the wave's unit number u on: load i brings piece `part` of
+  // unit number u + v of row row_of(i), and zeros for rows past m
+  v4u held[kLoads];
+  const int v = (lane >> 4) & (U - 1), part = lane & 15;
+  auto row_of = [&](int i) { return i * (4 / U) + lane / (16 * U); };
+  auto fetch = [&](int u, int i) {
+    const int unit = wave + (u + v) * waves;
+    const bool in = row_of(i) < p.m && unit < units && (WHOLE || part < 4 * w4_quarters<WHOLE>(p.k, unit));
+    const uint32_t at = (uint32_t)row_of(i) * (uint32_t)p.k + unit * 128 + part * 8;
+    const auto x = __builtin_amdgcn_raw_buffer_load_b128(src_a, in ? at * 2 : kW4Nowhere, 0, 0);
+    held[i] = __builtin_bit_cast(v4u, x);
+  };
+  auto put = [&](int i) {
+    mine[(row_of(i) * U + v) * 16 + (part ^ row_of(i))] = __builtin_bit_cast(v4u, w4_order_a<FMT>(held[i]));
+  };
+  const int row = (r >> 2) + 4 * (r & 3) & (ROWS - 1);
+  float acc[1][1][E];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int e = 0; e < E; ++e) acc[0][0][e] = 0.f;
+
+  v4u t[kW4Depth];
+  uint32_t s[kW4Depth / Rows::kSU], z[kW4Depth / Rows::kSU];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  int u = (int)((long long)units * wave / WAVES);
-  for (; u + DEPTH <= u1; u += DEPTH) {
-    W4Unit<GROUP, MT, NT> t[DEPTH];
-#pragma unroll
-    for (int i = 0; i < DEPTH; ++i) w4_load<FMT>(p, n0, m0, u + i, t[i]);
-#pragma unroll
-    for (int i = 0; i < DEPTH; ++i) w4_accumulate<FMT>(p, u + i, t[i], acc);
+  for (int i = 0; i < kW4Depth; ++i) {
+    t[i] = rows.load(wave + i * waves, units);
+    if (i % Rows::kSU == 0) rows.load_scales(wave + i * waves, waves, s[i / Rows::kSU], z[i / Rows::kSU]);
   }
-  for (; u < u1; ++u) {
-    W4Unit<GROUP, MT, NT> t;
-    w4_load<FMT>(p, n0, m0, u, t);
-    w4_accumulate<FMT>(p, u, t, acc);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) fetch(0, i);
+  v4f s4[1], z4[1];
+#pragma unroll 1
+  for (int u = 0; u < count; u += kW4Depth) {
+#pragma unroll
+    for (int i = 0; i < kW4Depth; ++i) {
+      const int next = wave + (u + i + kW4Depth) * waves;
+      Rows::put(mine_w, t[i]);
+      t[i] = rows.load(next, units);
+      if (i % Rows::kSU == 0) {
+        Rows::put_scales(mine_w, s[i / Rows::kSU], z[i / Rows::kSU]);
+        rows.load_scales(next, waves, s[i / Rows::kSU], z[i / Rows::kSU]);
+        Rows::get_scales(mine_w, s4[0], z4[0]);
+      }
+      if (i % U == 0) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          put(j);
+          fetch(u + i + U, j);
+        }
+      }
+      v4u w[1] = {Rows::get(mine_w)};
+      w4_accumulate<FMT, GROUP, 1, 1, E, WHOLE>(p.k, wave + (u + i) * waves, w, s4, z4, i % Rows::kSU * Rows::kG, acc,
+                                                [&](int, int j) {
+        const int piece = GROUP == 128 ? q * 4 + j : j * 4 + q;
+        return __builtin_bit_cast(v8bf, mine[(row * U + i % U) * 16 + (piece ^ row)]);
+      });
+      __builtin_amdgcn_sched_barrier(0);  // a unit at a time: mixing units only takes registers
+      if (u + i + 1 >= count) goto done;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) red[wave][i * NT + j][lane] = acc[i][j];
+done:
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * NT * 64; e += WAVES * 64) {
-    const int tile = e >> 6, l = e & 63;
-    v4f v = red[0][tile][l];
+  float* red = (float*)lds;  // [waves][E][64]
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) v += red[w][tile][l];
-    const int row = m0 + (tile / NT) * 16 + (l >> 4) * 4;
-    const int col = n0 + (tile % NT) * 16 + (l & 15);
-    if (col >= p.n) continue;
+  for (int e = 0; e < E; ++e) red[(wave * E + e) * 64 + lane] = acc[0][0][e];
+  __syncthreads();
+  const int e = threadIdx.x >> 6;  // a wave for each of the E rows of a lane group
+  if (e >= E) return;
+  float sum = red[e * 64 + lane];
+#pragma unroll 1
+  for (int w = 1; w < waves; ++w) sum += red[(w * E + e) * 64 + lane];
+  const int out = q + 4 * e, col = n0 + r;
+  if (out < p.m && col < p.n) p.d[(size_t)out * p.n + col] = f32_to_bf16(sum);
+}
+// LDS of a workgroup
+template <int FMT, int GROUP, int U, int ROWS, bool WHOLE>
+constexpr int w4_rows_smem(int waves) {
+  return waves * (U * ROWS * 256 + W4Rows<FMT, GROUP, WHOLE>::kLds);
+}
+
+// More than 16 rows of a: a workgroup of four waves takes 16 MT rows and 128
+// weight rows, 32 a wave, over one split of K.  The unit of a that all four
+// waves multiply with goes through LDS, in two buffers, fetched two units
+// ahead; each wave brings its own weights, kAhead units ahead.  Splits meet in
+// the stream's workspace: partial tiles are stored and loaded at agent scope
+// (SC1), each thread waits for its stores, a barrier and a relaxed counter
+// follow, and the last of a tile's workgroups adds all of them in split order.
+template <int FMT, int GROUP, int MT, bool WHOLE>
+__global__ __launch_bounds__(256, 2) void w4_tile_kernel(W4Params p) {
+  using Rows = W4Rows<FMT, GROUP, WHOLE>;
+  constexpr int NT = 2, kAhead = 4, kTile = MT * NT * 4 * 64 * 4;  // floats of a workgroup's tile
+  __shared__ v4u s_a[2][16 * MT * 16];
+  __shared__ __align__(16) uint8_t s_w[4][NT][Rows::kLds];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4;
+  const int n0 = blockIdx.x * 128 + wave * 32, m0 = blockIdx.z * 16 * MT;
+  const int units = (p.k + 127) / 128, splits = gridDim.y;
+  const int u0 = (int)((long long)units * blockIdx.y / splits), u1 = (int)((long long)units * (blockIdx.y + 1) / splits);
+  const Rows rows[NT] = {Rows(p, n0), Rows(p, n0 + 16)};
+
+  v4u held[2][MT];
+  auto fetch_a = [&](int u, int set) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (row + i < p.m) p.d[(size_t)(row + i) * p.n + col] = f32_to_bf16(v[i]);
+    for (int i = 0; i < MT; ++i) {
+      const int c = tid + 256 * i, row = min(m0 + c / 16, p.m - 1), part = c % 16;
+      const int inside = WHOLE ? part : min(part, 4 * w4_quarters<WHOLE>(p.k, u) - 1);
+      held[set][i] = *(const v4u*)(p.a + (size_t)row * p.k + (size_t)u * 128 + inside * 8);
+    }
+  };
+  auto put_a = [&](int buf, int set) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int c = tid + 256 * i, row = c / 16, part = c % 16;
+      s_a[buf][row * 16 + (part ^ (row & 15))] = __builtin_bit_cast(v4u, w4_order_a<FMT>(held[set][i]));
+    }
+  };
+  v4u t[kAhead][NT];
+  uint32_t s[kAhead / Rows::kSU][NT], z[kAhead / Rows::kSU][NT];
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+  // past the split's end its last unit of a is loaded again, and not used
+  fetch_a(u0, 0);
+  fetch_a(min(u0 + 1, u1 - 1), 1);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      t[i][j] = rows[j].load(u0 + i, u1);
+      if (i % Rows::kSU == 0) rows[j].load_scales(u0 + i, 1, s[i / Rows::kSU][j], z[i / Rows::kSU][j]);
+    }
+  put_a(0, 0);
+  fetch_a(min(u0 + 2, u1 - 1), 0);
+  __syncthreads();
+  v4f s4[NT], z4[NT];
+#pragma unroll 1
+  for (int u = u0; u < u1; u += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int buf = i & 1, next = u + i + kAhead;  // kAhead is even
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        Rows::put(s_w[wave][j], t[i][j]);
+        t[i][j] = rows[j].load(next, u1);
+        if (i % Rows::kSU == 0) {
+          Rows::put_scales(s_w[wave][j], s[i / Rows::kSU][j], z[i / Rows::kSU][j]);
+          rows[j].load_scales(next, 1, s[i / Rows::kSU][j], z[i / Rows::kSU][j]);
+          Rows::get_scales(s_w[wave][j], s4[j], z4[j]);
+        }
+      }
+      put_a(buf ^ 1, buf ^ 1);
+      fetch_a(min(u + i + 3, u1 - 1), buf ^ 1);
+      v4u w[NT] = {Rows::get(s_w[wave][0]), Rows::get(s_w[wave][1])};
+      w4_accumulate<FMT, GROUP, MT, NT, 4, WHOLE>(p.k, u + i, w, s4, z4, i % Rows::kSU * Rows::kG, acc, [&](int mi, int j) {
+        const int row = mi * 16 + (lane & 15), part = GROUP == 128 ? q * 4 + j : j * 4 + q;
+        return __builtin_bit_cast(v8bf, s_a[buf][row * 16 + (part ^ (row & 15))]);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+      __syncthreads();
+      if (u + i + 1 >= u1) goto done;
+    }
   }
+done:
+
+  if (splits > 1) {
+    const int tile = blockIdx.z * gridDim.x + blockIdx.x;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        p.partial + (size_t)tile * splits * kTile, 0, splits * kTile * 4, kBufferRsrcWord3);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v4f{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]}), rs,
+                                               (blockIdx.y * kTile + ((i * NT + j) * 256 + tid) * 4) * 4, 0, kCpolSc1);
+    wait_vmem_all();
+    __syncthreads();
+    if (tid == 0)
+      s_last = __hip_atomic_fetch_add(p.count + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == splits - 1;
+    __syncthreads();
+    if (!s_last) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+    for (int s0 = 0; s0 < splits; s0 += 2) {
+      v4f part[2][MT][NT];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            // past the last split the buffer's bounds give zero
+            const auto v = __builtin_amdgcn_raw_buffer_load_b128(
+                rs, ((s0 + s) * kTile + ((i * NT + j) * 256 + tid) * 4) * 4, 0, kCpolSc1);
+            part[s][i][j] = __builtin_bit_cast(v4f, v);
+          }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] += part[s][i][j][e];
+    }
+    if (tid == 0) __hip_atomic_store(p.count + tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int col = n0 + j * 16 + (lane & 15);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = m0 + i * 16 + q * 4 + e;
+        if (row < p.m && col < p.n) p.d[(size_t)row * p.n + col] = f32_to_bf16(acc[i][j][e]);
+      }
+    }
 }
 
 // ---- quantiser and its inverse: streaming passes, bound by HBM

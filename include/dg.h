@@ -332,13 +332,18 @@ typedef enum { DG_W4_E2M1 = 0, DG_W4_U4 = 1 } dg_w4_format;
  * for bf16 a [m][k]: the projections of a decode step, where a handful of
  * tokens meet weights that are read once.  Products and sums are fp32 (the
  * scale meets the fp32 sum of its group, so no weight is rounded after
- * scaling), one launch, no scratch memory, the same bits on every call.  Any
- * m >= 0 (0: a no-op) is computed; up to 64 rows share one read of the
- * weights, more rows read them again for every 64, so a long prompt is better
- * served by dg_dequantize_b_w4 and dg_bf16_gemm_nt.
+ * scaling), in one launch, with the same bits on every call.  Any m >= 0 (0: a
+ * no-op) is computed; up to 64 rows share one read of the weights, more rows
+ * read them again for every 64, so a long prompt is better served by
+ * dg_dequantize_b_w4 and dg_bf16_gemm_nt.  With m > 16, K may be split over
+ * workgroups: the call then needs dg_bf16_w4_workspace_size bytes of the
+ * stream's workspace (see the workspace rule above).
  */
 int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
                        uint16_t* d, int m, int n, int k, int group, int format, dg_stream_t stream);
+
+/* Bytes of the stream's workspace that dg_bf16_w4_gemm_nt takes for a shape on the current device (0 for m <= 16). */
+int dg_bf16_w4_workspace_size(int m, int n, int k, int group, int format, size_t* bytes);
 
 /*
  * Quantise a weight matrix x[n][k] (bf16 bits if x_bf16, else fp32) into that
