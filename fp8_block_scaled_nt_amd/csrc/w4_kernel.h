@@ -223,28 +223,54 @@ __device__ __forceinline__ void w4_accumulate(int k, int u, v4u (&w)[NT], const 
         const uint32_t eight = w[i][g * kPer + j];
         b[i][j] = w4_widen<FMT>(eight);
       }
+    // all tiles side by side, and two chains of products where there is but
+    // one: a product waits some 30 cycles for the one before it in its chain
+    constexpr int kChains = MT * NT == 1 && kPer > 1 ? 2 : 1;
+    v4f part[kChains][MT][NT], sum[kChains][MT];
 #pragma unroll
-    for (int mi = 0; mi < MT; ++mi) {
-      v8bf a[kPer];
-      v4f sum = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < kChains; ++c)
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        a[j] = load_a(mi, g * kPer + j);
-        if constexpr (FMT == kW4U4) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], ones, sum, 0, 0, 0);
+      for (int mi = 0; mi < MT; ++mi) {
+        sum[c][mi] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NT; ++i) part[c][mi][i] = v4f{0.f, 0.f, 0.f, 0.f};
       }
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        v4f part = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < kPer; ++j)
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], b[i][j], part, 0, 0, 0);
+      for (int mi = 0; mi < MT; ++mi) {
+        const int c = j % kChains;
+        const v8bf a = load_a(mi, g * kPer + j);
+        if constexpr (FMT == kW4U4) sum[c][mi] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, sum[c][mi], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          part[c][mi][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[i][j], part[c][mi][i], 0, 0, 0);
+      }
+#pragma unroll
+    for (int mi = 0; mi < MT; ++mi)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if constexpr (FMT == kW4U4) part[e] -= z[i][first + g] * sum[e];
-          acc[mi][i][e] += s[i][first + g] * part[e];
+          float x = part[0][mi][i][e], y = sum[0][mi][e];
+          if constexpr (kChains == 2) {
+            x += part[1][mi][i][e];
+            y += sum[1][mi][e];
+          }
+          if constexpr (FMT == kW4U4) x -= z[i][first + g] * y;
+          acc[mi][i][e] += s[i][first + g] * x;
         }
-      }
-    }
   }
+}
+
+// Where 16-byte piece `part` of a unit of row `row` of a lies in LDS: pieces in
+// the order in which products take them (product j takes piece 4 q + j in lane
+// group q where a group is the whole unit, else 4 j + q), and rows apart by an
+// exclusive or, so that the 16 rows that are read together, and the lane
+// groups, fall on different banks.
+template <int GROUP>
+__device__ __forceinline__ int w4_slot_a(int row, int part) {
+  return (GROUP == 128 ? (part & 3) * 4 + (part >> 2) : part) ^ (row & 15);
 }
 
 // Up to 16 rows of a: a workgroup takes 16 weight rows, and its waves (4 to
@@ -293,7 +319,7 @@ __global__ __launch_bounds__(1024) void w4_rows_kernel(W4Params p) {
     held[i] = __builtin_bit_cast(v4u, x);
   };
   auto put = [&](int i) {
-    mine[(row_of(i) * U + v) * 16 + (part ^ row_of(i))] = __builtin_bit_cast(v4u, w4_order_a<FMT>(held[i]));
+    mine[(row_of(i) * U + v) * 16 + w4_slot_a<GROUP>(row_of(i), part)] = __builtin_bit_cast(v4u, w4_order_a<FMT>(held[i]));
   };
   const int row = (r >> 2) + 4 * (r & 3) & (ROWS - 1);
   float acc[1][1][E];
@@ -332,8 +358,7 @@ __global__ __launch_bounds__(1024) void w4_rows_kernel(W4Params p) {
       v4u w[1] = {Rows::get(mine_w)};
       w4_accumulate<FMT, GROUP, 1, 1, E, WHOLE>(p.k, wave + (u + i) * waves, w, s4, z4, i % Rows::kSU * Rows::kG, acc,
                                                 [&](int, int j) {
-        const int piece = GROUP == 128 ? q * 4 + j : j * 4 + q;
-        return __builtin_bit_cast(v8bf, mine[(row * U + i % U) * 16 + (piece ^ row)]);
+        return __builtin_bit_cast(v8bf, mine[(row * U + i % U) * 16 + ((j * 4 + q) ^ row)]);
       });
       __builtin_amdgcn_sched_barrier(0);  // a unit at a time: mixing units only takes registers
       if (u + i + 1 >= count) goto done;
@@ -392,7 +417,7 @@ __global__ __launch_bounds__(256, 2) void w4_tile_kernel(W4Params p) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const int c = tid + 256 * i, row = c / 16, part = c % 16;
-      s_a[buf][row * 16 + (part ^ (row & 15))] = __builtin_bit_cast(v4u, w4_order_a<FMT>(held[set][i]));
+      s_a[buf][row * 16 + w4_slot_a<GROUP>(row, part)] = __builtin_bit_cast(v4u, w4_order_a<FMT>(held[set][i]));
     }
   };
   v4u t[kAhead][NT];
@@ -437,8 +462,7 @@ __global__ __launch_bounds__(256, 2) void w4_tile_kernel(W4Params p) {
       fetch_a(min(u + i + 3, u1 - 1), buf ^ 1);
       v4u w[NT] = {Rows::get(s_w[wave][0]), Rows::get(s_w[wave][1])};
       w4_accumulate<FMT, GROUP, MT, NT, 4, WHOLE>(p.k, u + i, w, s4, z4, i % Rows::kSU * Rows::kG, acc, [&](int mi, int j) {
-        const int row = mi * 16 + (lane & 15), part = GROUP == 128 ? q * 4 + j : j * 4 + q;
-        return __builtin_bit_cast(v8bf, s_a[buf][row * 16 + (part ^ (row & 15))]);
+        return __builtin_bit_cast(v8bf, s_a[buf][(mi * 16 + (lane & 15)) * 16 + ((j * 4 + q) ^ (lane & 15))]);
       });
       __builtin_amdgcn_sched_barrier(0);
       __syncthreads();
