@@ -221,7 +221,7 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendParams p) {
 // the queries of one key/value head: row r of a sequence is query r / g, head
 // r % g of the group of g = h_q / h_kv heads that share the keys.
 //
-// Per row the kernels carry the running maximum m of t[j] = log2(e) x[j] +
+// Per row the kernels carry a reference m close to the running maximum of t[j] = log2(e) x[j] +
 // log2(vs[j]), u = sum_j 2^(t[j] - m) vc[j] and l = sum_j 2^(t[j] - m) / vs[j],
 // all in fp32.  With the values' scale inside the exponent, p = 2^(t - m) is
 // what multiplies the codes, whichever block they are in: one accumulator
@@ -230,8 +230,9 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendParams p) {
 // Both products run on the matrix cores with the 16 (or 32) rows as columns:
 // x^T = K q^T in bf16 (e4m3 codes are exact in bf16, q is bf16 anyway) and
 // u^T = V^T p^T in fp16.  fp16 holds e4m3 codes exactly too and rounds p to
-// 11 bits where bf16 keeps 8; p is at most 2^kSlack and what falls below
-// 2^-24 of that adds nothing that bf16 output could show.
+// 11 bits where bf16 keeps 8; p is at most 2^8, and where it falls below 2^-14,
+// to fp16's steps of 2^-24, beside a p of 2^-8 or more in the same row, it adds
+// nothing that bf16 output could show.
 // The keys of a 64-key step are dealt to the rows of the A operand so that
 // lane group g (lanes 16 g ..) ends up with p for keys 16 g .. 16 g + 15,
 // which is how a lane of the second product's B operand wants them against
@@ -254,7 +255,8 @@ struct Kv8AttnParams {
   int workers;
 };
 
-constexpr int kKv8Step = 64;    // keys of one step of one wave
+constexpr int kKv8Step = 64;       // keys of one step of one wave
+constexpr float kKv8Slack = 8.f;  // log2 of how far p may pass 1 before its reference moves
 constexpr float kKv8MinVs = 5.421010862427522e-20f;  // 2^-64: scales below are taken as this
 
 // What a sequence asks for.
@@ -413,7 +415,8 @@ struct Kv8Rows {
   int lo[MT], hi[MT];
 };
 
-// The block that holds the 16 keys of this lane group's run, and its scales.
+// The block that holds the 16 keys of this lane group's run, and its scales as
+// they are in memory.
 struct Kv8Run {
   int page;
   float ks, vs;
@@ -424,55 +427,33 @@ __device__ __forceinline__ Kv8Run kv8_run(const Kv8Cache& c, int head, int page)
   return Kv8Run{page, c.k_scales[at], c.v_scales[at]};
 }
 
-// One step: 64 keys from token `base` on, against 16 MT rows.  load_k(j, h)
-// gives the lane's 16 bytes h * 64 + 16 g .. of key (a / 4) * 16 + 4 j + a % 4,
-// load_v(i) those of dimension 16 i + a at keys 16 g .. (a = lane % 16, g =
-// lane / 16).  `masked`: some row does not see some of the keys, or the
-// sequence ends or the table lacks a block inside the step.
-template <int D, int MT, class LoadK, class LoadV>
-__device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Run& run, float scale_log2, bool masked,
-                                         const Kv8Rows<MT>& rows, const v8bf (&qf)[MT][D / 32],
-                                         Kv8State<D, MT>& st, LoadK load_k, LoadV load_v) {
-  const int run_v = base + ((threadIdx.x & 63) >> 4) * 16;
+// What a step needs of them: t = s ks + lv; 1 / vs; whether the block is there.
+struct Kv8Scale {
+  float ks, lv, inv_vs;
+  int there;
+};
+
+__device__ __forceinline__ Kv8Scale kv8_scale_of(const Kv8Run& run, float scale_log2) {
   const bool there = run.page >= 0;
   const float vs = there ? fmaxf(run.vs, kKv8MinVs) : 1.f;
-  const float inv_vs = __builtin_amdgcn_rcpf(vs);
-  float ks = run.ks * scale_log2, lv = __builtin_amdgcn_logf(vs);
+  return Kv8Scale{run.ks * scale_log2, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs), there};
+}
 
-  // s[4 j + e]: raw product with key run_v + 4 j + e; t = s ks + lv
-  float s[MT][16];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v4f acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      const v4u w = load_k(j, h);
-      const v8bf k0 = e4m3_to_bf16(w[0], w[1]), k1 = e4m3_to_bf16(w[2], w[3]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[t][2 * h], acc[t], 0, 0, 0);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[t][2 * h + 1], acc[t], 0, 0, 0);
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][4 * j + e] = acc[t][e];
-  }
+// What remains of a step when its raw products s[4 j + e] with keys run_v + 4 j
+// + e are there: t = s ks + lv, the reference, p, and the second product.
+template <int D, int MT, bool MASKED, class LoadV>
+__device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Scale& sc, const Kv8Rows<MT>& rows,
+                                                 float (&s)[MT][16], Kv8State<D, MT>& st, LoadV load_v) {
+  float ks = sc.ks, lv = sc.lv;
   uint32_t seen[MT];  // bit i: the row sees key run_v + i
-  if (masked) {
+  if constexpr (MASKED) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      seen[t] = 0;
+      // keys [lo, hi) of the 16, none if the block is not there
+      const int lo = min(max(rows.lo[t] - run_v, 0), 16), hi = sc.there ? min(max(rows.hi[t] - run_v, 0), 16) : 0;
+      seen[t] = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool in = there && run_v + i >= rows.lo[t] && run_v + i < rows.hi[t];
-        seen[t] |= (in ? 1u : 0u) << i;
-        s[t][i] = in ? s[t][i] * ks + lv : -__builtin_huge_valf();
-      }
+      for (int i = 0; i < 16; ++i) s[t][i] = seen[t] >> i & 1u ? s[t][i] * ks + lv : -__builtin_huge_valf();
     }
     ks = 1.f;
     lv = 0.f;
@@ -486,24 +467,28 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Run& run, fl
     m = m * ks + lv;
     m = fmaxf(m, __shfl_xor(m, 16, 64));
     m = fmaxf(m, __shfl_xor(m, 32, 64));
-    m = fmaxf(m, st.m[t]);
-    const float ref = m == -__builtin_huge_valf() ? 0.f : m;  // nothing seen yet: any finite reference
-    if (__any(m > st.m[t])) {
-      const float shrink = __builtin_amdgcn_exp2f(st.m[t] - ref);
+    // The reference follows the maximum only when a row's has grown by more
+    // than kKv8Slack: p is then at most 2^kKv8Slack, and few steps pay for
+    // scaling u.
+    if (__any(m > st.m[t] + kKv8Slack)) {
+      m = fmaxf(m, st.m[t]);
+      const float shrink = __builtin_amdgcn_exp2f(st.m[t] - (m == -__builtin_huge_valf() ? 0.f : m));
       st.l[t] *= shrink;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) st.u[t][i] *= shrink;
       st.m[t] = m;
     }
+    const float ref = st.m[t] == -__builtin_huge_valf() ? 0.f : st.m[t];  // nothing seen yet: any finite reference
     const float off = lv - ref;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       const float p0 = __builtin_amdgcn_exp2f(s[t][i] * ks + off), p1 = __builtin_amdgcn_exp2f(s[t][i + 1] * ks + off);
-      sum[(i / 2) & 3] += p0 + p1;
+      sum[0] += p0;
+      sum[1] += p1;
       const uint32_t both = pack2_f16(p0, p1);
       pw[t][i / 8][(i / 2) & 3] = both;
-      if (masked) {
+      if constexpr (MASKED) {
         // What fp16 left of p, as a second fp16: rows that see few keys (all
         // of them in a masked step) have large outputs that no averaging of
         // the rounding errors helps; with one piece 5 of 493568 outputs of
@@ -514,11 +499,15 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Run& run, fl
         rest[t][i / 8][(i / 2) & 3] = pack2_f16(p0 - (float)hi[0], p1 - (float)hi[1]);
       }
     }
-    st.l[t] += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * inv_vs;
+    st.l[t] += (sum[0] + sum[1]) * sc.inv_vs;
   }
-  if (!masked) {
+  // Parts of a step stay apart: mixed, their operands do not fit the registers
+  // of two waves a SIMD (prompts of 2048: 499 us with spills, @@ without).
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (!MASKED) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
+      if (i % 2 == 0) __builtin_amdgcn_sched_barrier(0);
       const v4u w = load_v(i);
       const v8h v0 = e4m3_to_f16(w[0], w[1]), v1 = e4m3_to_f16(w[2], w[3]);
 #pragma unroll
@@ -538,11 +527,12 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Run& run, fl
   v4u keep;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int n = there ? min(max(kv - (run_v + 4 * i), 0), 4) : 0;
+    const int n = sc.there ? min(max(kv - (run_v + 4 * i), 0), 4) : 0;
     keep[i] = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
+    __builtin_amdgcn_sched_barrier(0);
     v4u w = load_v(i) & keep;
     uint32_t bad = 0;
 #pragma unroll
@@ -569,8 +559,7 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Run& run, fl
                                                        cnt, 0, 0, 0);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (cnt[e] > 0.f) st.u[t][i][e] = __builtin_nanf("");
+        for (int e = 0; e < 4; ++e) st.u[t][i][e] = cnt[e] > 0.f ? __builtin_nanf("") : st.u[t][i][e];
       }
     }
     const v8h v0 = e4m3_to_f16(w[0], w[1]), v1 = e4m3_to_f16(w[2], w[3]);
@@ -583,6 +572,51 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Run& run, fl
       st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, __builtin_bit_cast(v8h, pw[t][1]), u, 0, 0, 0);
     }
   }
+}
+
+// One step: 64 keys from token `base` on, against 16 MT rows.  load_k(j, h)
+// gives the lane's 16 bytes h * 64 + 16 g .. of key (a / 4) * 16 + 4 j + a % 4,
+// load_v(i) those of dimension 16 i + a at keys 16 g .. (a = lane % 16, g =
+// lane / 16).  `masked`: some row does not see some of the keys, or the
+// sequence ends or the table lacks a block inside the step.  load_q(t, i) gives
+// B fragment i of the lane's row of tile t.
+template <int D, int MT, class LoadQ, class LoadK, class LoadV>
+__device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, bool masked, const Kv8Rows<MT>& rows,
+                                         Kv8State<D, MT>& st, LoadQ load_q, LoadK load_k, LoadV load_v) {
+  float s[MT][16];
+  v8bf qf[MT][D / 32];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qf[t][i] = load_q(t, i);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+    v4f acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+      const v4u w = load_k(j, h);
+      const v8bf k0 = e4m3_to_bf16(w[0], w[1]), k1 = e4m3_to_bf16(w[2], w[3]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[t][2 * h], acc[t], 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[t][2 * h + 1], acc[t], 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][4 * j + e] = acc[t][e];
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  const int run_v = base + ((threadIdx.x & 63) >> 4) * 16;
+  if (masked)
+    kv8_rest_of_step<D, MT, true>(kv, run_v, sc, rows, s, st, load_v);
+  else
+    kv8_rest_of_step<D, MT, false>(kv, run_v, sc, rows, s, st, load_v);
 }
 
 // The B fragments of one row of q.
@@ -600,8 +634,8 @@ __device__ __forceinline__ void kv8_load_q(const Kv8AttnParams& p, const Kv8Seq&
 
 // Whether a step from token `base` on needs masks, given the keys [all_lo,
 // all_hi) that every row sees (all_hi is at most kv).
-__device__ __forceinline__ bool kv8_masked(int base, int all_lo, int all_hi, int page) {
-  return base < all_lo || base + kKv8Step > all_hi || __any(page < 0);
+__device__ __forceinline__ bool kv8_masked(int base, int all_lo, int all_hi, bool there) {
+  return base < all_lo || base + kKv8Step > all_hi || __any(!there);
 }
 
 // A wave's loads of one step straight from the cache into registers.
@@ -720,14 +754,14 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
       regs.load_v(p.c, head, base, pv);
       for (int t = first; t < last; t += 4) {
         const bool more = t + 4 < last;
-        const bool masked = kv8_masked(base, all_lo, all_hi, pv);
-        const Kv8Run now = run;
+        const bool masked = kv8_masked(base, all_lo, all_hi, pv >= 0);
+        const Kv8Scale now = kv8_scale_of(run, p.scale_log2);
         const int here = base;
         base += 4 * kKv8Step;
         pk = next_pk;
         pv = next_pv;
         kv8_pages(p.c, seq, sq.kv, base + 4 * kKv8Step, &next_pk, &next_pv);
-        kv8_step<D, 1>(sq.kv, here, now, p.scale_log2, masked, see, qf, st,
+        kv8_step<D, 1>(sq.kv, here, now, masked, see, st, [&](int t, int i) { return qf[t][i]; },
                        [&](int j, int h) {
                          const v4u w = regs.k[j][h];
                          return w;
@@ -831,17 +865,21 @@ __device__ __forceinline__ int kv8_slot(int row, int part) {
 // Prompts: one workgroup takes 64 MT rows of one key/value head, 16 MT of them
 // a wave, and walks all keys that they see.  Each step's codes go to LDS once
 // for the four waves, in two buffers: while one is worked on, the next step's
-// pieces are on their way to registers, and from there to the other.
+// pieces are on their way to registers, and from there to the other.  Wave w
+// brings keys 16 w .. 16 w + 15 of a step, K and V: they are of one block, so
+// its number, its scales and all addresses are uniform in the wave.
 template <int D, int MT>
 __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
   constexpr int kRows = 64 * MT, kParts = D / 16, kPer = D / 64;
   __shared__ v4u s_k[2][64 * kParts], s_v[2][D * 4];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, a = lane & 15, g = lane >> 4;
+  __shared__ Kv8Scale s_scale[2][4];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
   const int head = blockIdx.x, seq = blockIdx.y;
-  const int tile = gridDim.z - 1 - blockIdx.z;  // rows that see the most keys start first
   const Kv8Seq sq = kv8_seq(p, seq);
-  const int rows = sq.count * p.group, row0 = tile * kRows;
-  if (row0 >= rows) return;
+  const int rows = sq.count * p.group;
+  // every sequence's last tile, which sees the most keys, starts first
+  const int row0 = ((rows + kRows - 1) / kRows - 1 - (int)blockIdx.z) * kRows;
+  if (row0 < 0) return;
   const Kv8Cache& c = p.c;
 
   // keys that any row of the workgroup sees, and this wave's rows
@@ -854,74 +892,90 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
     kv8_sees(p, sq, wave1 / p.group, &all_lo, &wave_hi);
     kv8_sees(p, sq, wave0 / p.group, &wave_lo, &all_hi);
   }
-  v8bf qf[MT][D / 32];
+  // Where q's fragments stay between steps: registers, or, at d = 128, where
+  // these are all taken, LDS, fragment by fragment (of this wave: no barrier).
+  constexpr bool kQInLds = D == 128;
+  __shared__ v4u s_q[kQInLds ? kRows * (D / 8) : 1];
+  v8bf qf[MT][kQInLds ? 1 : D / 32];
   Kv8Rows<MT> see;
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int row = min(wave0 + t * 16 + a, rows - 1);
-    kv8_load_q<D>(p, sq, head, row, qf[t]);
+    if constexpr (kQInLds) {
+      v8bf once[D / 32];
+      kv8_load_q<D>(p, sq, head, row, once);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        s_q[((wave * MT + t) * (D / 32) + i) * 64 + lane] = __builtin_bit_cast(v4u, once[i]);
+    } else {
+      kv8_load_q<D>(p, sq, head, row, qf[t]);
+    }
     kv8_sees(p, sq, row / p.group, &see.lo[t], &see.hi[t]);
   }
   Kv8State<D, MT> st;
   st.clear();
 
-  // this thread's pieces of a step: kPer of K, kPer of V
-  int page_k[kPer], page_v, page_run;
+  // this wave's 16 keys of a step
+  int page;
+  Kv8Run run;
   v4u held_k[kPer], held_v[kPer];
   auto look = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int run = base + (((tid + 256 * i) / kParts) & ~15);
-      page_k[i] = max(kv8_page(c, seq, run), 0);
-    }
-    page_v = max(kv8_page(c, seq, base + (tid & 3) * 16), 0);
-    const int run = base + g * 16, page = kv8_page(c, seq, run);
-    page_run = run < sq.kv ? page : -1;
+    const int key = base + wave * 16;
+    const int found = kv8_page(c, seq, key);
+    page = __builtin_amdgcn_readfirstlane(key < sq.kv ? found : -1);
   };
   auto fetch = [&](int base) {
+    const int key = base + wave * 16;
+    const size_t tile = ((size_t)max(page, 0) * c.h_kv + head) * (size_t)(c.block * D);
+    const uint8_t* k = c.k_codes + tile + (key & (c.block - 1)) * D;
+    const uint8_t* v = c.v_codes + tile + (key & (c.block - 1));
+    run = kv8_run(c, head, page);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int key = (tid + 256 * i) / kParts, part = (tid + 256 * i) % kParts;
-      held_k[i] = *(const v4u*)(c.k_codes + ((size_t)page_k[i] * c.h_kv + head) * (size_t)(c.block * D) +
-                                (((base + key) & (c.block - 1)) * D + part * 16));
-      const int d = (tid + 256 * i) >> 2;
-      held_v[i] = *(const v4u*)(c.v_codes + ((size_t)page_v * c.h_kv + head) * (size_t)(c.block * D) +
-                                (d * c.block + ((base + (tid & 3) * 16) & (c.block - 1))));
+      held_k[i] = *(const v4u*)(k + (uint32_t)((lane + 64 * i) * 16));
+      held_v[i] = *(const v4u*)(v + (uint32_t)((lane + 64 * i) * c.block));
     }
   };
   auto put = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int key = (tid + 256 * i) / kParts, part = (tid + 256 * i) % kParts;
+      const int key = (lane + 64 * i) / kParts, part = (lane + 64 * i) % kParts;
       // row 16 j + a of the tile is the key that lane a takes in product j
-      const int row = ((key >> 2) & 3) * 16 + (key >> 4) * 4 + (key & 3);
+      const int row = (key >> 2) * 16 + wave * 4 + (key & 3);
       s_k[buf][kv8_slot<kParts>(row, part)] = held_k[i];
-      s_v[buf][kv8_slot<4>((tid + 256 * i) >> 2, tid & 3)] = held_v[i];
+      s_v[buf][kv8_slot<4>(lane + 64 * i, wave)] = held_v[i];
     }
+    if (lane == 0) s_scale[buf][wave] = kv8_scale_of(run, p.scale_log2);
   };
   const int first = any_lo / kKv8Step, last = (any_hi + kKv8Step - 1) / kKv8Step;
   if (first < last) {
     look(first * kKv8Step);
     fetch(first * kKv8Step);
-    Kv8Run run = kv8_run(c, head, page_run);
-    look((first + 1) * kKv8Step);
     put(0);
+    look((first + 1) * kKv8Step);
     __syncthreads();
+#pragma unroll 1
     for (int s = first; s < last; ++s) {
       const int base = s * kKv8Step, buf = (s - first) & 1;
-      const Kv8Run now = run;
-      if (s + 1 < last) {
-        fetch(base + kKv8Step);
-        run = kv8_run(c, head, page_run);
-        look(base + 2 * kKv8Step);
-      }
+      // past the last step: the table's last block, or block 0, into a buffer that nobody reads
+      fetch(base + kKv8Step);
+      look(base + 2 * kKv8Step);
       if (base < wave_hi && base + kKv8Step > wave_lo) {
-        const bool masked = kv8_masked(base, all_lo, all_hi, now.page);
-        kv8_step<D, MT>(sq.kv, base, now, p.scale_log2, masked, see, qf, st,
-                        [&](int j, int h) { return s_k[buf][kv8_slot<kParts>(j * 16 + a, h * 4 + g)]; },
-                        [&](int i) { return s_v[buf][kv8_slot<4>(i * 16 + a, g)]; });
+        const Kv8Scale now = s_scale[buf][g];
+        const bool masked = kv8_masked(base, all_lo, all_hi, now.there);
+        const v4u* k_at = s_k[buf];
+        const v4u* v_at = s_v[buf];
+        kv8_step<D, MT>(sq.kv, base, now, masked, see, st,
+                        [&](int t, int i) {
+                          if constexpr (kQInLds)
+                            return __builtin_bit_cast(v8bf, s_q[((wave * MT + t) * (D / 32) + i) * 64 + lane]);
+                          else
+                            return qf[t][i];
+                        },
+                        [&](int j, int h) { return k_at[kv8_slot<kParts>(j * 16 + a, h * 4 + g)]; },
+                        [&](int i) { return v_at[kv8_slot<4>(i * 16 + a, g)]; });
       }
-      if (s + 1 < last) put(buf ^ 1);
+      put(buf ^ 1);
       __syncthreads();
     }
   }
