@@ -577,11 +577,11 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
 // One step: 64 keys from token `base` on, against 16 MT rows.  load_k(j, h)
 // gives the lane's 16 bytes h * 64 + 16 g .. of key (a / 4) * 16 + 4 j + a % 4,
 // load_v(i) those of dimension 16 i + a at keys 16 g .. (a = lane % 16, g =
-// lane / 16).  `masked`: some row does not see some of the keys, or the
-// sequence ends or the table lacks a block inside the step.  load_q(t, i) gives
-// B fragment i of the lane's row of tile t.
-template <int D, int MT, class LoadQ, class LoadK, class LoadV>
-__device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, bool masked, const Kv8Rows<MT>& rows,
+// lane / 16), load_q(t, i) B fragment i of the lane's row of tile t.  MASKED:
+// some row may not see some of the keys, or the sequence end inside the step;
+// such steps are the first and last ones of a run and have loops of their own.
+template <int D, int MT, bool MASKED, class LoadQ, class LoadK, class LoadV>
+__device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, const Kv8Rows<MT>& rows,
                                          Kv8State<D, MT>& st, LoadQ load_q, LoadK load_k, LoadV load_v) {
   float s[MT][16];
   v8bf qf[MT][D / 32];
@@ -613,10 +613,7 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, b
   }
   __builtin_amdgcn_sched_barrier(0);
   const int run_v = base + ((threadIdx.x & 63) >> 4) * 16;
-  if (masked)
-    kv8_rest_of_step<D, MT, true>(kv, run_v, sc, rows, s, st, load_v);
-  else
-    kv8_rest_of_step<D, MT, false>(kv, run_v, sc, rows, s, st, load_v);
+  kv8_rest_of_step<D, MT, MASKED>(kv, run_v, sc, rows, s, st, load_v);
 }
 
 // The B fragments of one row of q.
@@ -761,7 +758,8 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
         pk = next_pk;
         pv = next_pv;
         kv8_pages(p.c, seq, sq.kv, base + 4 * kKv8Step, &next_pk, &next_pv);
-        kv8_step<D, 1>(sq.kv, here, now, masked, see, st, [&](int t, int i) { return qf[t][i]; },
+        auto step = [&](auto mask) {
+          kv8_step<D, 1, decltype(mask)::value>(sq.kv, here, now, see, st, [&](int t, int i) { return qf[t][i]; },
                        [&](int j, int h) {
                          const v4u w = regs.k[j][h];
                          return w;
@@ -774,6 +772,8 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
                          const v4u w = regs.v[i];
                          return w;
                        });
+        };
+        if (masked) step(std::true_type{}); else step(std::false_type{});
         if (more) regs.load_v(p.c, head, base, pv);
       }
     }
@@ -882,15 +882,14 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
   if (row0 < 0) return;
   const Kv8Cache& c = p.c;
 
-  // keys that any row of the workgroup sees, and this wave's rows
-  int any_lo, any_hi, unused;
-  kv8_sees(p, sq, row0 / p.group, &any_lo, &unused);
-  kv8_sees(p, sq, (min(row0 + kRows, rows) - 1) / p.group, &unused, &any_hi);
+  // keys that any row of the workgroup sees, that all see, and that any of this wave's rows sees
+  int any_lo, any_hi, all_lo, all_hi, wave_lo = 0, wave_hi = 0, unused;
+  kv8_sees(p, sq, row0 / p.group, &any_lo, &all_hi);
+  kv8_sees(p, sq, (min(row0 + kRows, rows) - 1) / p.group, &all_lo, &any_hi);
   const int wave0 = row0 + wave * 16 * MT, wave1 = min(wave0 + 16 * MT, rows) - 1;  // none if wave0 > wave1
-  int all_lo = 0, all_hi = 0, wave_lo = 0, wave_hi = 0;
   if (wave0 <= wave1) {
-    kv8_sees(p, sq, wave1 / p.group, &all_lo, &wave_hi);
-    kv8_sees(p, sq, wave0 / p.group, &wave_lo, &all_hi);
+    kv8_sees(p, sq, wave1 / p.group, &unused, &wave_hi);
+    kv8_sees(p, sq, wave0 / p.group, &wave_lo, &unused);
   }
   // Where q's fragments stay between steps: registers, or, at d = 128, where
   // these are all taken, LDS, fragment by fragment (of this wave: no barrier).
@@ -915,68 +914,87 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
   Kv8State<D, MT> st;
   st.clear();
 
-  // this wave's 16 keys of a step
-  int page;
+  // This wave's 16 keys of a step.  The table is read two steps ahead and the
+  // scales one, by vector loads although they are uniform: scalar loads share
+  // their counter with LDS, whose every wait would wait for them.
+  int zero = 0;
+  asm("" : "+v"(zero));
+  int found, page;
   Kv8Run run;
   v4u held_k[kPer], held_v[kPer];
   auto look = [&](int base) {
-    const int key = base + wave * 16;
-    const int found = kv8_page(c, seq, key);
-    page = __builtin_amdgcn_readfirstlane(key < sq.kv ? found : -1);
+    found = c.table[(size_t)seq * c.max_blocks + min((base + wave * 16) >> c.block_log2, c.max_blocks - 1) + zero];
   };
   auto fetch = [&](int base) {
     const int key = base + wave * 16;
-    const size_t tile = ((size_t)max(page, 0) * c.h_kv + head) * (size_t)(c.block * D);
-    const uint8_t* k = c.k_codes + tile + (key & (c.block - 1)) * D;
-    const uint8_t* v = c.v_codes + tile + (key & (c.block - 1));
-    run = kv8_run(c, head, page);
+    const int at = __builtin_amdgcn_readfirstlane(found);
+    page = (key < sq.kv) & ((unsigned)at < (unsigned)c.num_blocks) ? at : -1;
+    look(base + kKv8Step);
+    const size_t tile = (size_t)max(page, 0) * c.h_kv + head;
+    run = Kv8Run{page, c.k_scales[tile + zero], c.v_scales[tile + zero]};
+    const uint8_t* k = c.k_codes + tile * (size_t)(c.block * D) + (key & (c.block - 1)) * D;
+    const uint8_t* v = c.v_codes + tile * (size_t)(c.block * D) + (key & (c.block - 1));
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       held_k[i] = *(const v4u*)(k + (uint32_t)((lane + 64 * i) * 16));
       held_v[i] = *(const v4u*)(v + (uint32_t)((lane + 64 * i) * c.block));
     }
   };
+  // Keys of a block that the table does not have become zeros with lv = -inf:
+  // p = 0, without a mask.
   auto put = [&](int buf) {
+    const uint32_t keep = page < 0 ? 0u : 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int key = (lane + 64 * i) / kParts, part = (lane + 64 * i) % kParts;
       // row 16 j + a of the tile is the key that lane a takes in product j
       const int row = (key >> 2) * 16 + wave * 4 + (key & 3);
-      s_k[buf][kv8_slot<kParts>(row, part)] = held_k[i];
-      s_v[buf][kv8_slot<4>(lane + 64 * i, wave)] = held_v[i];
+      s_k[buf][kv8_slot<kParts>(row, part)] = held_k[i] & keep;
+      s_v[buf][kv8_slot<4>(lane + 64 * i, wave)] = held_v[i] & keep;
     }
-    if (lane == 0) s_scale[buf][wave] = kv8_scale_of(run, p.scale_log2);
+    if (lane == 0) {
+      Kv8Scale sc = kv8_scale_of(run, p.scale_log2);
+      if (page < 0) sc = Kv8Scale{0.f, -__builtin_huge_valf(), 1.f, 0};
+      s_scale[buf][wave] = sc;
+    }
   };
   const int first = any_lo / kKv8Step, last = (any_hi + kKv8Step - 1) / kKv8Step;
   if (first < last) {
     look(first * kKv8Step);
     fetch(first * kKv8Step);
     put(0);
-    look((first + 1) * kKv8Step);
     __syncthreads();
+    int s = first;
+    auto steps = [&](int until, auto mask) {
 #pragma unroll 1
-    for (int s = first; s < last; ++s) {
-      const int base = s * kKv8Step, buf = (s - first) & 1;
-      // past the last step: the table's last block, or block 0, into a buffer that nobody reads
-      fetch(base + kKv8Step);
-      look(base + 2 * kKv8Step);
-      if (base < wave_hi && base + kKv8Step > wave_lo) {
-        const Kv8Scale now = s_scale[buf][g];
-        const bool masked = kv8_masked(base, all_lo, all_hi, now.there);
-        const v4u* k_at = s_k[buf];
-        const v4u* v_at = s_v[buf];
-        kv8_step<D, MT>(sq.kv, base, now, masked, see, st,
-                        [&](int t, int i) {
-                          if constexpr (kQInLds)
-                            return __builtin_bit_cast(v8bf, s_q[((wave * MT + t) * (D / 32) + i) * 64 + lane]);
-                          else
-                            return qf[t][i];
-                        },
-                        [&](int j, int h) { return k_at[kv8_slot<kParts>(j * 16 + a, h * 4 + g)]; },
-                        [&](int i) { return v_at[kv8_slot<4>(i * 16 + a, g)]; });
+      for (; s < until; ++s) {
+        const int base = s * kKv8Step, buf = (s - first) & 1;
+        fetch(base + kKv8Step);  // past the last step: no block, or one that nobody will use
+        if (base < wave_hi && base + kKv8Step > wave_lo) {
+          const v4u* k_at = s_k[buf];
+          const v4u* v_at = s_v[buf];
+          const Kv8Scale now = s_scale[buf][g];
+          kv8_step<D, MT, decltype(mask)::value>(
+              sq.kv, base, now, see, st,
+              [&](int t, int i) {
+                if constexpr (kQInLds)
+                  return __builtin_bit_cast(v8bf, s_q[((wave * MT + t) * (D / 32) + i) * 64 + lane]);
+                else
+                  return qf[t][i];
+              },
+              [&](int j, int h) { return k_at[kv8_slot<kParts>(j * 16 + a, h * 4 + g)]; },
+              [&](int i) { return v_at[kv8_slot<4>(i * 16 + a, g)]; });
+        }
+        put(buf ^ 1);
+        __syncthreads();
       }
-      put(buf ^ 1);
-      __syncthreads();
+    };
+    // masked steps, steps that every row of the workgroup sees wholly, masked steps
+    const int whole0 = min(max((all_lo + kKv8Step - 1) / kKv8Step, first), last), whole1 = max(all_hi / kKv8Step, whole0);
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+      steps(part == 0 ? whole0 : last, std::true_type{});
+      if (part == 0) steps(min(whole1, last), std::false_type{});
     }
   }
 #pragma unroll
