@@ -1492,11 +1492,22 @@ int dg_kv8_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_
   // blocks that max_new tokens can touch, wherever the first one stands
   const int slots = (p.most + block - 2) / block + 1;
   if ((long long)slots >= (1LL << 24)) return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many new tokens (%d)", p.most);
-  const void* fn = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<64>)
-                   : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<128>)
-                              : reinterpret_cast<const void*>(&dg::kv8_append_kernel<256>);
+  // up to 4 new tokens are at most two groups of 4 positions of a block: one
+  // wave holds them (64 single tokens, 8 heads of 128: 5.0 against 5.9 us)
+  const bool few = p.most <= 4;
+  const int threads = few ? 64 : 256;
+  const int items = few ? 1 : (block * d + 8191) / 8192;  // of 4 tokens by 8 values, per thread
+  const void* fn = few ? (d == 64    ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<64, 1, 64>)
+                          : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<128, 1, 64>)
+                                     : reinterpret_cast<const void*>(&dg::kv8_append_kernel<256, 1, 64>))
+                   : d == 64 ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<64, 1, 256>)
+                   : d == 128 ? (items == 1 ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<128, 1, 256>)
+                                            : reinterpret_cast<const void*>(&dg::kv8_append_kernel<128, 2, 256>))
+                   : items == 1 ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<256, 1, 256>)
+                   : items == 2 ? reinterpret_cast<const void*>(&dg::kv8_append_kernel<256, 2, 256>)
+                                : reinterpret_cast<const void*>(&dg::kv8_append_kernel<256, 4, 256>);
   void* args[] = {&p};
-  return launch_plain("kv8_append", fn, dim3(slots, 2 * h_kv, batch), 256, args, stream);
+  return launch_plain("kv8_append", fn, dim3(slots, 2 * h_kv, batch), threads, args, stream, d * (block + 16));
 }
 
 int dg_kv8_attention_workspace_size(int d, size_t* bytes) {

@@ -106,14 +106,15 @@ struct Kv8AppendParams {
 // filled at once up to those.  amax counts finite values only; infinities
 // saturate at 448 s' and NaN is stored as NaN.
 //
-// The new values are read twice (amax, then codes; the second read comes from
-// the caches) rather than kept in registers, which bounds no tile size.
-// Values are turned on their way in an LDS tile of codes [d][block].
-template <int D>
-__global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendParams p) {
+// The new values stay in registers between their maximum and their codes.  A
+// thread takes items of 8 dimensions by 4 positions of the block (those with a
+// new token in them), so that values, which lie dimension by dimension, turn
+// in LDS by whole words of 4 tokens: D rows of `block` codes.
+template <int D, int ITEMS, int THREADS>
+__global__ __launch_bounds__(THREADS) void kv8_append_kernel(Kv8AppendParams p) {
   constexpr int kPer = D / 8;  // 16-byte pieces of a token's head
-  __shared__ float s_max[4];
-  __shared__ __align__(16) uint8_t turn[D * (128 + 16)];
+  __shared__ float s_max[THREADS / 64];
+  extern __shared__ __align__(16) uint8_t turn[];  // values: [D][block + 16]
   const int seq = blockIdx.z, head = blockIdx.y >> 1;
   const int block = p.c.block, tid = threadIdx.x;
   int first, count;
@@ -129,28 +130,43 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendParams p) {
   const bool values = (blockIdx.y & 1) != 0;
   const uint16_t* x = values ? p.v : p.k;
   const long long stride = values ? p.v_stride : p.k_stride;
-  const uint16_t* src = x + (long long)(first + base + old - ctx) * stride + (long long)head * D;
+  const uint16_t* src = x + (long long)(first + base - ctx) * stride + (long long)head * D;  // position 0's row
   const size_t tile = (size_t)page * p.c.h_kv + head;
   float* scale = (values ? p.c.v_scales : p.c.k_scales) + tile;
   uint8_t* codes = (values ? p.c.v_codes : p.c.k_codes) + tile * (size_t)block * D;
   const float was = old > 0 ? *scale : 0.f;
 
-  const int pieces = (stop - old) * kPer;
+  const int group0 = old >> 2, items = (((stop + 3) >> 2) - group0) * kPer;
+  v4u held[ITEMS][4];
   float amax = 0.f;
-  for (int e = tid; e < pieces; e += 256) {
-    float f[8];
-    w4_read8<true>(src + (long long)(e / kPer) * stride, (size_t)(e % kPer) * 8, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(f[i]);
-      amax = fmaxf(amax, a < __builtin_huge_valf() ? a : 0.f);
+  for (int n = 0; n < ITEMS; ++n) {
+    const int e = tid + n * THREADS, pos = (group0 + e / kPer) * 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      held[n][j] = v4u{0, 0, 0, 0};
+      if (e < items && pos + j >= old && pos + j < stop)
+        held[n][j] = *(const v4u*)(src + (long long)(pos + j) * stride + e % kPer * 8);
     }
   }
 #pragma unroll
+  for (int n = 0; n < ITEMS; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float lo = fabsf(__uint_as_float(held[n][j][i] << 16)), hi = fabsf(__uint_as_float(held[n][j][i] & 0xFFFF0000u));
+        amax = fmaxf(amax, lo < __builtin_huge_valf() ? lo : 0.f);
+        amax = fmaxf(amax, hi < __builtin_huge_valf() ? hi : 0.f);
+      }
+#pragma unroll
   for (int s = 32; s >= 1; s >>= 1) amax = fmaxf(amax, __shfl_xor(amax, s, 64));
-  if ((tid & 63) == 0) s_max[tid >> 6] = amax;
-  __syncthreads();
-  amax = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  if constexpr (THREADS > 64) {
+    if ((tid & 63) == 0) s_max[tid >> 6] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) amax = fmaxf(amax, s_max[w]);
+  }
   const float now = fmaxf(was, kv8_scale(amax));
   const float inv = 1.f / now;  // a power of two: exact
   const bool grow = old > 0 && now > was;
@@ -158,23 +174,43 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendParams p) {
   if (tid == 0) *scale = now;
 
   const int pitch = block + 16;
-  for (int e = tid; e < pieces; e += 256) {
-    const int t = e / kPer, c = e % kPer;
-    float f[8];
-    w4_read8<true>(src + (long long)t * stride, (size_t)c * 8, f);
-    const uint32_t lo = kv8_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-    const uint32_t hi = kv8_pack4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+#pragma unroll
+  for (int n = 0; n < ITEMS; ++n) {
+    const int e = tid + n * THREADS, pos = (group0 + e / kPer) * 4, c = e % kPer;
+    if (e >= items) continue;
+    uint32_t code[4][2];  // of each token, 4 dimensions a word
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t a = held[n][j][2 * i], b = held[n][j][2 * i + 1];
+        code[j][i] = kv8_pack4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xFFFF0000u) * inv,
+                               __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv);
+      }
     if (!values) {
-      *(uint2*)(codes + (size_t)(old + t) * D + c * 8) = make_uint2(lo, hi);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (pos + j >= old && pos + j < stop)
+          *(uint2*)(codes + (size_t)(pos + j) * D + c * 8) = make_uint2(code[j][0], code[j][1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        turn[(c * 8 + i) * pitch + old + t] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+      for (int i = 0; i < 2; ++i) {
+        // a 4 x 4 transpose of bytes: words of one dimension, 4 tokens each
+        const uint32_t lo01 = __builtin_amdgcn_perm(code[1][i], code[0][i], 0x05010400u);
+        const uint32_t lo23 = __builtin_amdgcn_perm(code[3][i], code[2][i], 0x05010400u);
+        const uint32_t hi01 = __builtin_amdgcn_perm(code[1][i], code[0][i], 0x07030602u);
+        const uint32_t hi23 = __builtin_amdgcn_perm(code[3][i], code[2][i], 0x07030602u);
+        uint8_t* to = turn + (c * 8 + i * 4) * pitch + pos;
+        *(uint32_t*)(to) = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+        *(uint32_t*)(to + pitch) = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+        *(uint32_t*)(to + 2 * pitch) = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+        *(uint32_t*)(to + 3 * pitch) = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+      }
     }
   }
   if (!values) {
     if (grow)
-      for (int e = tid; e < old * kPer; e += 256) {
+      for (int e = tid; e < old * kPer; e += THREADS) {
         uint2* at = (uint2*)(codes + (size_t)e * 8);
         const uint2 w = *at;
         *at = make_uint2(kv8_rescale4(w.x, by), kv8_rescale4(w.y, by));
@@ -186,7 +222,7 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendParams p) {
   // rounded anew, bytes past the new tokens as they were
   const int lo16 = grow ? 0 : old >> 4, hi16 = (stop + 15) >> 4;
   const int per_row = hi16 - lo16;
-  for (int e = tid; e < D * per_row; e += 256) {
+  for (int e = tid; e < D * per_row; e += THREADS) {
     const int row = e / per_row, t0 = (lo16 + e % per_row) * 16;
     v4u* at = (v4u*)(codes + (size_t)row * block + t0);
     const v4u fresh = *(const v4u*)(turn + row * pitch + t0);
@@ -198,15 +234,11 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendParams p) {
     v4u w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t kept = grow ? kv8_rescale4(held[i], by) : held[i];
-      uint32_t r = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int t = t0 + i * 4 + b;
-        const uint32_t from = t < old ? kept : (t < stop ? fresh[i] : held[i]);
-        r |= from & (0xFFu << (8 * b));
-      }
-      w[i] = r;
+      const uint32_t was4 = held[i], fresh4 = fresh[i];
+      const uint32_t kept = grow ? kv8_rescale4(was4, by) : was4;
+      const int o = min(max(old - (t0 + i * 4), 0), 4), s = min(max(stop - (t0 + i * 4), 0), 4);
+      const uint32_t is_old = o == 4 ? ~0u : (1u << (8 * o)) - 1u, is_in = s == 4 ? ~0u : (1u << (8 * s)) - 1u;
+      w[i] = (kept & is_old) | (fresh4 & is_in & ~is_old) | (was4 & ~is_in);
     }
     *at = w;
   }
@@ -384,10 +416,10 @@ __device__ __forceinline__ uint32_t pack2_f16(float a, float b) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
-// Bytes of `w` whose code is NaN (0x7F, 0xFF), as 0x01 in each such byte.
-__device__ __forceinline__ uint32_t kv8_nan_bytes(uint32_t w) {
-  // 0x7F + 1 carries into bit 7 of the byte, any smaller magnitude does not
-  return ((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u;
+// Halves of `w` (two fp16) that are NaN, as 1 in bit 0 and bit 16.
+__device__ __forceinline__ uint32_t f16_nans(uint32_t w) {
+  // a magnitude above that of infinity carries into the sign bit
+  return ((w & 0x7FFF7FFFu) + 0x03FF03FFu) >> 15 & 0x00010001u;
 }
 
 // A wave's running state for 16 MT rows: lane l holds, for each tile of 16,
@@ -501,50 +533,53 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
     }
     st.l[t] += (sum[0] + sum[1]) * sc.inv_vs;
   }
-  // Parts of a step stay apart: mixed, their operands do not fit the registers
-  // of two waves a SIMD (prompts of 2048: 499 us with spills, @@ without).
-  __builtin_amdgcn_sched_barrier(0);
   if constexpr (!MASKED) {
+    v8h v[2][2];
+    v[0][0] = load_v(0, 0);
+    v[0][1] = load_v(0, 1);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      if (i % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-      const v4u w = load_v(i);
-      const v8h v0 = e4m3_to_f16(w[0], w[1]), v1 = e4m3_to_f16(w[2], w[3]);
+      if (i + 1 < D / 16) {
+        v[(i + 1) & 1][0] = load_v(i + 1, 0);
+        v[(i + 1) & 1][1] = load_v(i + 1, 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-        st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, __builtin_bit_cast(v8h, pw[t][0]), st.u[t][i], 0, 0, 0);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-        st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, __builtin_bit_cast(v8h, pw[t][1]), st.u[t][i], 0, 0, 0);
+        for (int t = 0; t < MT; ++t)
+          st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[i & 1][h], __builtin_bit_cast(v8h, pw[t][h]), st.u[t][i], 0, 0, 0);
     }
     return;
   }
-  // Bytes past the sequence's end, or of a block that is not there, hold
-  // anything: zero them.  A NaN code of a token that some rows see and others
-  // do not must reach the former only, and 0 * NaN would reach both: such
-  // codes are zeroed, and a second product counts, per row and dimension, the
-  // NaN that the row sees.
-  v4u keep;
+  // Values past the sequence's end, or of a block that is not there, may be
+  // anything: zero them.  A NaN of a token that some rows see and others do
+  // not must reach the former only, and 0 * NaN would reach both: such values
+  // are zeroed, and a second product counts, per row and dimension, the NaN
+  // that the row sees.
+  uint32_t keep[8];  // of each pair of the lane's 16 keys
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = sc.there ? min(max(kv - (run_v + 4 * i), 0), 4) : 0;
-    keep[i] = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+  for (int i = 0; i < 8; ++i) {
+    const int n = sc.there ? kv - (run_v + 2 * i) : 0;
+    keep[i] = n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u;
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     __builtin_amdgcn_sched_barrier(0);
-    v4u w = load_v(i) & keep;
+    v4u w[2] = {__builtin_bit_cast(v4u, load_v(i, 0)), __builtin_bit_cast(v4u, load_v(i, 1))};
     uint32_t bad = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bad |= kv8_nan_bytes(w[e]);
+    for (int e = 0; e < 8; ++e) {
+      w[e / 4][e % 4] &= keep[e];
+      bad |= f16_nans(w[e / 4][e % 4]);
+    }
     if (__any(bad != 0)) {
       v4u ind[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t b = kv8_nan_bytes(w[e]);
-        w[e] &= ~(b * 255u);
-        ind[e / 2][2 * (e & 1)] = (b & 1u) * 0x3C00u | (b >> 8 & 1u) * 0x3C000000u;
-        ind[e / 2][2 * (e & 1) + 1] = (b >> 16 & 1u) * 0x3C00u | (b >> 24 & 1u) * 0x3C000000u;
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t nan = f16_nans(w[e / 4][e % 4]);
+        w[e / 4][e % 4] &= ~(nan * 0xFFFFu);
+        ind[e / 4][e % 4] = nan * 0x3C00u;
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
@@ -562,7 +597,7 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
         for (int e = 0; e < 4; ++e) st.u[t][i][e] = cnt[e] > 0.f ? __builtin_nanf("") : st.u[t][i][e];
       }
     }
-    const v8h v0 = e4m3_to_f16(w[0], w[1]), v1 = e4m3_to_f16(w[2], w[3]);
+    const v8h v0 = __builtin_bit_cast(v8h, w[0]), v1 = __builtin_bit_cast(v8h, w[1]);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       v4f u = st.u[t][i];
@@ -574,10 +609,11 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
   }
 }
 
-// One step: 64 keys from token `base` on, against 16 MT rows.  load_k(j, h)
-// gives the lane's 16 bytes h * 64 + 16 g .. of key (a / 4) * 16 + 4 j + a % 4,
-// load_v(i) those of dimension 16 i + a at keys 16 g .. (a = lane % 16, g =
-// lane / 16), load_q(t, i) B fragment i of the lane's row of tile t.  MASKED:
+// One step: 64 keys from token `base` on, against 16 MT rows.  load_k(j, h, o)
+// gives the lane's values h * 64 + 16 g + 8 o .. of key (a / 4) * 16 + 4 j +
+// a % 4, load_v(i, o) those of dimension 16 i + a at keys 16 g + 8 o .. (a =
+// lane % 16, g = lane / 16), load_q(t, i) B fragment i of the lane's row of
+// tile t.  MASKED:
 // some row may not see some of the keys, or the sequence end inside the step;
 // such steps are the first and last ones of a run and have loops of their own.
 template <int D, int MT, bool MASKED, class LoadQ, class LoadK, class LoadV>
@@ -589,23 +625,26 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, c
   for (int t = 0; t < MT; ++t)
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) qf[t][i] = load_q(t, i);
+  // The next product's operands are on their way while one runs; a fence a
+  // product keeps the compiler from fetching more than registers hold.
+  v8bf k[2][D / 32];
+  auto fetch = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) k[j & 1][i] = load_k(j, i / 2, i % 2);
+  };
+  fetch(0);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+    if (j + 1 < 4) fetch(j + 1);
+    __builtin_amdgcn_sched_barrier(0);
     v4f acc[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      const v4u w = load_k(j, h);
-      const v8bf k0 = e4m3_to_bf16(w[0], w[1]), k1 = e4m3_to_bf16(w[2], w[3]);
+    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int t = 0; t < MT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[t][2 * h], acc[t], 0, 0, 0);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[t][2 * h + 1], acc[t], 0, 0, 0);
-    }
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j & 1][i], qf[t][i], acc[t], 0, 0, 0);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -760,17 +799,13 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
         kv8_pages(p.c, seq, sq.kv, base + 4 * kKv8Step, &next_pk, &next_pv);
         auto step = [&](auto mask) {
           kv8_step<D, 1, decltype(mask)::value>(sq.kv, here, now, see, st, [&](int t, int i) { return qf[t][i]; },
-                       [&](int j, int h) {
-                         const v4u w = regs.k[j][h];
-                         return w;
-                       },
-                       [&](int i) {
-                         if (i == 0 && more) {
+                       [&](int j, int h, int o) { return e4m3_to_bf16(regs.k[j][h][2 * o], regs.k[j][h][2 * o + 1]); },
+                       [&](int i, int o) {
+                         if (i == 0 && o == 0 && more) {
                            regs.load_k(p.c, head, base, pk);
                            run = kv8_run(p.c, head, pv);
                          }
-                         const v4u w = regs.v[i];
-                         return w;
+                         return e4m3_to_f16(regs.v[i][2 * o], regs.v[i][2 * o + 1]);
                        });
         };
         if (masked) step(std::true_type{}); else step(std::false_type{});
@@ -854,24 +889,27 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttnParams p) {
 }
 
 // Where the 16-byte piece `part` of row `row` lies in an LDS tile of rows of
-// `kParts` pieces: the 16 lanes that read one piece each of rows 0..15 of a
-// tile then fall on all 64 banks once.
+// `kParts` pieces (a multiple of 8): the 16 lanes that read one piece each of
+// rows 0..15 of a tile then fall on all 64 banks once.
 template <int kParts>
 __device__ __forceinline__ int kv8_slot(int row, int part) {
-  constexpr int kShift = kParts == 4 ? 2 : kParts == 8 ? 1 : 0;
-  return row * kParts + (part ^ ((row >> kShift) & (kParts - 1)));
+  return row * kParts + (part ^ (kParts == 8 ? (row >> 1) & 7 : row & 15));
 }
 
 // Prompts: one workgroup takes 64 MT rows of one key/value head, 16 MT of them
-// a wave, and walks all keys that they see.  Each step's codes go to LDS once
-// for the four waves, in two buffers: while one is worked on, the next step's
-// pieces are on their way to registers, and from there to the other.  Wave w
+// a wave, and walks all keys that they see.  Each step's codes are widened once
+// for the four waves (K to bf16, V to fp16) on their way to LDS, in two
+// buffers: while one is worked on, the next step's pieces are on their way to
+// registers, and from there to the other.  (Codes in LDS, widened by each wave,
+// take a quarter less LDS time but 96 more of some 400 vector instructions a
+// step: 308 us for prompts of 2048; widened, and fetched one product ahead,
+// 293.) Wave w
 // brings keys 16 w .. 16 w + 15 of a step, K and V: they are of one block, so
 // its number, its scales and all addresses are uniform in the wave.
 template <int D, int MT>
 __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
-  constexpr int kRows = 64 * MT, kParts = D / 16, kPer = D / 64;
-  __shared__ v4u s_k[2][64 * kParts], s_v[2][D * 4];
+  constexpr int kRows = 64 * MT, kParts = D / 8, kPer = D / 64;
+  __shared__ v4u s_k[2][64 * kParts], s_v[2][D * 8];  // pieces of 8 values
   __shared__ Kv8Scale s_scale[2][4];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
   const int head = blockIdx.x, seq = blockIdx.y;
@@ -891,24 +929,12 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
     kv8_sees(p, sq, wave1 / p.group, &unused, &wave_hi);
     kv8_sees(p, sq, wave0 / p.group, &wave_lo, &unused);
   }
-  // Where q's fragments stay between steps: registers, or, at d = 128, where
-  // these are all taken, LDS, fragment by fragment (of this wave: no barrier).
-  constexpr bool kQInLds = D == 128;
-  __shared__ v4u s_q[kQInLds ? kRows * (D / 8) : 1];
-  v8bf qf[MT][kQInLds ? 1 : D / 32];
+  v8bf qf[MT][D / 32];
   Kv8Rows<MT> see;
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int row = min(wave0 + t * 16 + a, rows - 1);
-    if constexpr (kQInLds) {
-      v8bf once[D / 32];
-      kv8_load_q<D>(p, sq, head, row, once);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        s_q[((wave * MT + t) * (D / 32) + i) * 64 + lane] = __builtin_bit_cast(v4u, once[i]);
-    } else {
-      kv8_load_q<D>(p, sq, head, row, qf[t]);
-    }
+    kv8_load_q<D>(p, sq, head, row, qf[t]);
     kv8_sees(p, sq, row / p.group, &see.lo[t], &see.hi[t]);
   }
   Kv8State<D, MT> st;
@@ -946,11 +972,15 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
     const uint32_t keep = page < 0 ? 0u : 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int key = (lane + 64 * i) / kParts, part = (lane + 64 * i) % kParts;
+      const int key = (lane + 64 * i) / (D / 16), part = (lane + 64 * i) % (D / 16) * 2;
       // row 16 j + a of the tile is the key that lane a takes in product j
       const int row = (key >> 2) * 16 + wave * 4 + (key & 3);
-      s_k[buf][kv8_slot<kParts>(row, part)] = held_k[i] & keep;
-      s_v[buf][kv8_slot<4>(lane + 64 * i, wave)] = held_v[i] & keep;
+      const v4u k = held_k[i] & keep, v = held_v[i] & keep;
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        s_k[buf][kv8_slot<kParts>(row, part + o)] = __builtin_bit_cast(v4u, e4m3_to_bf16(k[2 * o], k[2 * o + 1]));
+        s_v[buf][kv8_slot<8>(lane + 64 * i, wave * 2 + o)] = __builtin_bit_cast(v4u, e4m3_to_f16(v[2 * o], v[2 * o + 1]));
+      }
     }
     if (lane == 0) {
       Kv8Scale sc = kv8_scale_of(run, p.scale_log2);
@@ -976,14 +1006,11 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
           const Kv8Scale now = s_scale[buf][g];
           kv8_step<D, MT, decltype(mask)::value>(
               sq.kv, base, now, see, st,
-              [&](int t, int i) {
-                if constexpr (kQInLds)
-                  return __builtin_bit_cast(v8bf, s_q[((wave * MT + t) * (D / 32) + i) * 64 + lane]);
-                else
-                  return qf[t][i];
+              [&](int t, int i) { return qf[t][i]; },
+              [&](int j, int h, int o) {
+                return __builtin_bit_cast(v8bf, k_at[kv8_slot<kParts>(j * 16 + a, h * 8 + g * 2 + o)]);
               },
-              [&](int j, int h) { return k_at[kv8_slot<kParts>(j * 16 + a, h * 4 + g)]; },
-              [&](int i) { return v_at[kv8_slot<4>(i * 16 + a, g)]; });
+              [&](int i, int o) { return __builtin_bit_cast(v8h, v_at[kv8_slot<8>(i * 16 + a, g * 2 + o)]); });
         }
         put(buf ^ 1);
         __syncthreads();
