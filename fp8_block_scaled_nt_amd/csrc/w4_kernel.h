@@ -549,6 +549,18 @@ __device__ __forceinline__ void w4_read8(const void* x, size_t at, float (&v)[8]
   }
 }
 
+// x / s for one s and many x, correctly rounded as one division each would be,
+// in three instructions instead of ten: with r = 1 / s correctly rounded, q = x
+// r and the exact remainder x - q s, q + r (x - q s) rounds to the quotient
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990; s has 8 significant bits, so it is none of the theorem's
+// exceptions).  Remainders that underflow belong to quotients that round to
+// the code of zero.
+__device__ __forceinline__ float w4_quotient(float x, float s, float r) {
+  const float q = x * r;
+  return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, s, x), r, q), x);  // -0 stays -0
+}
+
 // A thread holds 8 values of a group, GROUP / 8 neighbouring lanes a group.
 //   e2m1: s = bf16(max(amax, 1e-4) / 6), c = e2m1(x / s)
 //   u4:   lo = min(x, 0), hi = max(x, 0) over the group, s = bf16(max(hi - lo, 1e-4) / 15),
@@ -580,17 +592,21 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const void* __restrict__ 
   }
   if (!live) return;
   const uint16_t sb = f32_to_bf16(fmaxf(hi - lo, kAmaxFloor) / (FMT == kW4E2m1 ? kE2m1Max : 15.f));
-  const float sc = bf16_to_f32(sb);
+  const float sc = bf16_to_f32(sb), r = 1.f / sc;
   uint32_t c = 0;
   float z = 0.f;
-  if constexpr (FMT == kW4E2m1) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c |= e2m1_code(v[e] / sc) << (4 * e);
+  for (int e = 0; e < 8; ++e) v[e] = w4_quotient(v[e], sc, r);
+  if constexpr (FMT == kW4E2m1) {
+    // v_cvt_scalef32_pk_fp4_f32: nearest, ties to even, saturating at 6
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], 1.0f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], 1.0f, 3);
   } else {
     z = fminf(rintf(-lo / sc), 15.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      c |= (uint32_t)(int)fminf(fmaxf(rintf(v[e] / sc) + z, 0.f), 15.f) << (4 * e);
+    for (int e = 0; e < 8; ++e) c |= (uint32_t)(int)fminf(fmaxf(rintf(v[e]) + z, 0.f), 15.f) << (4 * e);
   }
   *(uint32_t*)(codes + i * 4) = c;
   if ((threadIdx.x & (kLanes - 1)) == 0) {

@@ -125,6 +125,24 @@ def test_quantize(gpu, fmt, n, k, group, dtype):
     assert np.array_equal(w.float().cpu().numpy(), oracle.bf16_round(oracle.dequantize_w4(*ref)))
 
 
+def test_quantize_ties_and_many_scales(gpu):
+    # every midpoint between e2m1 values and its neighbours, at scales over many binades; random values for
+    # the correctly rounded quotient
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    near = np.concatenate([np.nextafter(mids, np.float32(0)), mids, np.nextafter(mids, np.float32(9)), [6.0, 0.0, -0.0]])
+    row = np.concatenate([near, -near, np.zeros(128 - 2 * near.size)]).astype(np.float32)
+    x = np.stack([row * np.float32(s) for s in (1.0, 0.5, 2.0 ** -10, 2.0 ** 20, 1.0078125, 1.9921875 * 2.0 ** -7)])
+    rng = np.random.default_rng(31)
+    more = (rng.standard_normal((200, 128)) * np.exp2(rng.integers(-12, 12, (200, 1)))).astype(np.float32)
+    x = np.concatenate([x, more])
+    for fmt in ("e2m1", "u4"):
+        codes, scales, zeros = dg.quantize_b_w4(H.f32_to_device(x, gpu), fmt, 128)
+        ref = oracle.quantize_w4(x, fmt, 128)
+        assert np.array_equal(scales.float().cpu().numpy(), ref[1])
+        assert np.array_equal(codes.cpu().numpy(), ref[0])
+        assert zeros is None if ref[2] is None else np.array_equal(zeros.cpu().numpy(), ref[2])
+
+
 def test_binding_refuses(gpu):
     a = torch.zeros((2, 128), dtype=torch.bfloat16, device=gpu)
     d = torch.zeros((2, 8), dtype=torch.bfloat16, device=gpu)
