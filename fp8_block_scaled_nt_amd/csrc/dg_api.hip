@@ -1544,8 +1544,7 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
     return fail(DG_ERR_MISALIGNED, "out must be 16-byte aligned, lse and lengths 4-byte");
   if (batch == 0 || total == 0 || max_q == 0) return ok();
   p.most = max_q < total ? max_q : total;
-  const long long tiles = ((long long)p.most * (h_q / h_kv) + 15) / 16;
-  if ((long long)p.most * h_q > 0x3FFFFFFFLL || tiles >= (1LL << 24))
+  if ((long long)p.most * h_q * d > 0x7FFFFFFFLL)  // of one sequence; 32-bit counts of its elements
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many queries per sequence (%d of %d heads)", p.most, h_q);
   int dev;
   DeviceInfo* info;
@@ -1582,16 +1581,13 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   p.workers = kv8_workers(info);
   char* base = nullptr;
   if (int s = ensure_workspace(dev, (hipStream_t)stream, kv8_part_floats(p.workers, d) * sizeof(float), &base)) return s;
+  p.arrived = (int*)base;
   p.part_u = (float*)(base + kWsHeader);
   p.part_ml = p.part_u + (size_t)p.workers * 2 * 16 * d;
   const void* fn = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_attn_kernel<64>)
                    : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_attn_kernel<128>)
                               : reinterpret_cast<const void*>(&dg::kv8_attn_kernel<256>);
-  const void* join = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_join_kernel<64>)
-                     : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_join_kernel<128>)
-                                : reinterpret_cast<const void*>(&dg::kv8_join_kernel<256>);
-  if (int s = launch_plain("kv8_attn", fn, dim3(p.workers), 256, args, stream)) return s;
-  return launch_plain("kv8_join", join, dim3((unsigned)tiles, h_kv, batch), 256, args, stream);
+  return launch_plain("kv8_attn", fn, dim3(p.workers), 256, args, stream);
 }
 
 }  // extern "C"

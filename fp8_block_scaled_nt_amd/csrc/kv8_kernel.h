@@ -284,6 +284,7 @@ struct Kv8AttnParams {
   // split work: workgroup w computes its share of the units below
   float* part_u;   // [workers][2][16][d]
   float* part_ml;  // [workers][2][16][2]
+  int* arrived;    // [workers] counters, zero between calls
   int workers;
 };
 
@@ -333,17 +334,11 @@ __device__ __forceinline__ long long kv8_sum256(long long v, long long* box) {
   return box[0] + box[1] + box[2] + box[3];
 }
 
-// Units of all sequences, and of the sequences before `upto`.
-__device__ __forceinline__ void kv8_total(const Kv8AttnParams& p, int upto, long long* total, long long* before,
-                                          long long* box) {
-  long long all = 0, some = 0;
-  for (int i = threadIdx.x; i < p.batch; i += 256) {
-    const long long u = kv8_units(p, kv8_seq(p, i));
-    all += u;
-    some += i < upto ? u : 0;
-  }
-  *total = kv8_sum256(all, box);
-  *before = kv8_sum256(some, box);
+// Units of all sequences.
+__device__ __forceinline__ long long kv8_total(const Kv8AttnParams& p, long long* box) {
+  long long all = 0;
+  for (int i = threadIdx.x; i < p.batch; i += 256) all += kv8_units(p, kv8_seq(p, i));
+  return kv8_sum256(all, box);
 }
 
 // The sequence that unit `at` (below the total) is of, and its first unit.
@@ -728,19 +723,36 @@ __device__ __forceinline__ void kv8_write(const Kv8AttnParams& p, const Kv8Seq& 
 // A workgroup of four waves takes an equal share of all (sequence, head, row
 // tile, 64-key step) units, in that order; within a run of steps of one tile
 // its waves take every fourth step each and merge in LDS.  Runs that cover a
-// tile's steps wholly are written out, others leave their (u, m, l) to
-// kv8_join_kernel.  The shares come from the lengths on the device: nothing
-// of the launch depends on them, and the longest sequence spreads over as
-// many workgroups as its part of the batch's keys is worth.
+// tile's steps wholly are written out; of the others, the last workgroup of a
+// tile joins all parts.  The shares come from the lengths on the device:
+// nothing of the launch depends on them, and the longest sequence spreads over
+// as many workgroups as its part of the batch's keys is worth.
+//
+// Parts pass between XCDs, whose L2s do not see each other's lines, by stores
+// and loads at agent scope (SC1): each thread waits until its stores are
+// complete, a barrier and a relaxed counter at the same scope follow, and the
+// workgroup that finds all others counted loads the parts, in workgroup order,
+// after a barrier behind its own count.  A tile's counter is its first
+// workgroup's: no other tile starts in that one and goes on.  (A second kernel
+// for the joining took 4 to 11 us and its launch.)
 template <int D>
 __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
   constexpr int kPitch = D + 4;
   __shared__ float s_u[4][16][kPitch];
   __shared__ float s_m[4][16], s_l[4][16];
   __shared__ long long box[6];
+  __shared__ int s_last;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, a = lane & 15, g = lane >> 4;
-  long long total, unused;
-  kv8_total(p, 0, &total, &unused, box);
+  // rows of sequences without keys
+  for (int i = blockIdx.x; i < p.batch; i += p.workers) {
+    const Kv8Seq s = kv8_seq(p, i);
+    if (s.steps > 0) continue;
+    for (int e = tid; e < s.count * p.h_q * (D / 2); e += 256)
+      ((uint32_t*)p.out)[(size_t)s.first * p.h_q * (D / 2) + e] = 0u;
+    if (p.lse)
+      for (int e = tid; e < s.count * p.h_q; e += 256) p.lse[(size_t)s.first * p.h_q + e] = -__builtin_huge_valf();
+  }
+  const long long total = kv8_total(p, box);
   const int workers = kv8_workers(p, total);
   if ((int)blockIdx.x >= workers) return;
   const long long begin = kv8_share(total, blockIdx.x, workers), end = kv8_share(total, blockIdx.x + 1, workers);
@@ -750,6 +762,10 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
   kv8_find(p, at, &seq, &seq0, box);
   Kv8Seq sq = kv8_seq(p, seq);
   long long units = kv8_units(p, sq);
+  const __amdgpu_buffer_rsrc_t rs_u =
+      __builtin_amdgcn_make_buffer_rsrc(p.part_u, 0, p.workers * 2 * 16 * D * 4, kBufferRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rs_ml =
+      __builtin_amdgcn_make_buffer_rsrc(p.part_ml, 0, p.workers * 2 * 16 * 2 * 4, kBufferRsrcWord3);
   while (at < end) {
     while (at >= seq0 + units) {
       seq0 += units;
@@ -840,52 +856,67 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
       if (t0 == 0 && t1 == sq.steps) {
         kv8_write<D>(p, sq, head, tile * 16 + r, part, u, m, l);
       } else {
-        const size_t slot = ((size_t)blockIdx.x * 2 + (at == begin ? 0 : 1)) * 16 + r;
+        const int slot = ((int)blockIdx.x * 2 + (at == begin ? 0 : 1)) * 16 + r;
+        const bool live = tile * 16 + r < rows;
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) p.part_u[slot * D + part * (D / 16) + i] = u[i];
-        if (part == 0) {
-          p.part_ml[slot * 2] = m;
-          p.part_ml[slot * 2 + 1] = l;
+          for (int i = 0; i < D / 16; i += 4)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v4f{u[i], u[i + 1], u[i + 2], u[i + 3]}), rs_u,
+                                                   (slot * D + part * (D / 16) + i) * 4, 0, kCpolSc1);
+          if (part == 0)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, v2f{m, l}), rs_ml, slot * 8, 0, kCpolSc1);
+        }
+        // the tile's steps, and the workgroups that have some of them
+        const long long s0 = seq0 + (long long)tile_no * sq.steps;
+        const int w0 = kv8_owner(total, s0, workers), w1 = kv8_owner(total, s0 + sq.steps - 1, workers);
+        wait_vmem_all();
+        __syncthreads();
+        if (tid == 0)
+          s_last = __hip_atomic_fetch_add(p.arrived + w0, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == w1 - w0;
+        __syncthreads();
+        if (s_last) {
+          if (tid == 0) __hip_atomic_store(p.arrived + w0, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+          // only the first of them can have had another tile before this one
+          const int slot0 = (w0 * 2 + (s0 > kv8_share(total, w0, workers) ? 1 : 0)) * 16 + r;
+          auto slot_of = [&](int w) { return w == w0 ? slot0 : w * 32 + r; };
+          auto load_ml = [&](int w) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs_ml, slot_of(w) * 8, 0, kCpolSc1);
+            return __builtin_bit_cast(v2f, v);
+          };
+          if (live) {
+            // reference and sum of the row: its 16 threads take every 16th part each
+            m = -__builtin_huge_valf();
+            for (int w = w0 + part; w <= w1; w += 16) m = fmaxf(m, load_ml(w)[0]);
+#pragma unroll
+            for (int s = 8; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
+            const float all = m == -__builtin_huge_valf() ? 0.f : m;
+            l = 0.f;
+            for (int w = w0 + part; w <= w1; w += 16) {
+              const v2f ml = load_ml(w);
+              l += ml[1] * __builtin_amdgcn_exp2f(ml[0] - all);
+            }
+#pragma unroll
+            for (int s = 8; s >= 1; s >>= 1) l += __shfl_xor(l, s, 64);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) u[i] = 0.f;
+#pragma unroll 4
+            for (int w = w0; w <= w1; ++w) {
+              const float f = __builtin_amdgcn_exp2f(load_ml(w)[0] - all);
+#pragma unroll
+              for (int i = 0; i < D / 16; i += 4) {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs_u, (slot_of(w) * D + part * (D / 16) + i) * 4, 0, kCpolSc1);
+                const v4f x = __builtin_bit_cast(v4f, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[i + e] += x[e] * f;
+              }
+            }
+          }
+          kv8_write<D>(p, sq, head, tile * 16 + r, part, u, m, l);
         }
       }
     }
     at += t1 - t0;
   }
-}
-
-// Joins the parts of every tile that more than one workgroup had, in their
-// order, and writes the rows of sequences without keys.  One workgroup a
-// (tile, head, sequence).
-template <int D>
-__global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttnParams p) {
-  __shared__ long long box[4];
-  const int tile = blockIdx.x, head = blockIdx.y, seq = blockIdx.z;
-  const Kv8Seq sq = kv8_seq(p, seq);
-  if (tile >= sq.tiles) return;
-  const int r = threadIdx.x >> 4, part = threadIdx.x & 15;
-  float u[D / 16];
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) u[i] = 0.f;
-  float m = -__builtin_huge_valf(), l = 0.f;
-  if (sq.steps > 0) {
-    long long total, seq0;
-    kv8_total(p, seq, &total, &seq0, box);
-    const long long s0 = seq0 + ((long long)head * sq.tiles + tile) * sq.steps;
-    const int workers = kv8_workers(p, total);
-    const int w0 = kv8_owner(total, s0, workers), w1 = kv8_owner(total, s0 + sq.steps - 1, workers);
-    if (w0 == w1) return;  // one workgroup had all of it and wrote it
-    for (int w = w0; w <= w1; ++w) {
-      const size_t slot = ((size_t)w * 2 + (s0 > kv8_share(total, w, workers) ? 1 : 0)) * 16 + r;
-      const float mw = p.part_ml[slot * 2], lw = p.part_ml[slot * 2 + 1];
-      const float to = fmaxf(m, mw), ref = to == -__builtin_huge_valf() ? 0.f : to;
-      const float f = __builtin_amdgcn_exp2f(m - ref), fw = __builtin_amdgcn_exp2f(mw - ref);
-      l = l * f + lw * fw;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) u[i] = u[i] * f + p.part_u[slot * D + part * (D / 16) + i] * fw;
-      m = to;
-    }
-  }
-  kv8_write<D>(p, sq, head, tile * 16 + r, part, u, m, l);
 }
 
 // Where the 16-byte piece `part` of row `row` lies in an LDS tile of rows of
