@@ -883,20 +883,31 @@ template <int FMT, int GROUP, bool WHOLE>
 W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
   const int units = (k + 127) / 128;
   if (m <= 16) {
-    // about 16 waves per CU, and a unit or more for each of them
+    // 8 waves for up to one and a half workgroups per CU, then 4, which leave
+    // more of them side by side (us, 4 / 8 / 16 waves: 1 x 2112 x 7168 5.2 / 4.7
+    // / 4.9, 1 x 4096 x 7168 6.1 / 5.9 / 6.2, 8 x 4096 x 7168 8.9 / 7.7 / 8.0,
+    // 1 x 7168 x 16384 12.6 / 14.1 / 15.3, 1 x 16384 x 2048 6.7 / 7.6 / 12.7);
+    // 4 also where 8 would have two units each or fewer (1 x 512 x 1024 3.1 /
+    // 3.3 / 3.6).  With more than 8 rows always 8, as there is more to compute
+    // than to load (16 x 7168 x 16384, groups of 32: 33.5 / 27.1).
     const dim3 grid((n + 15) / 16);
-    const long long want = 16LL * info->cus / grid.x;
-    int waves = want > 8 && units >= 16 ? 16 : want > 4 && units >= 8 ? 8 : 4;
+    const int waves = units >= 16 && (m > 8 || 2LL * grid.x <= 3LL * info->cus) ? 8 : 4;
+    // rows of a staged: no more than needed (8 waves; 4 / 8 / 16 rows: 1 x 4096 x
+    // 7168 6.0 / 6.4 / 7.3; 4 x 4096 x 7168 7.6 / 7.7 / 8.5; 5 x 2112 x 7168 - /
+    // 5.2 / 6.3)
     if (m <= 4)
       return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 2, 4, WHOLE>), grid, waves * 64,
               dg::w4_rows_smem<FMT, GROUP, 2, 4, WHOLE>(waves), 0, 0};
     if (m <= 8)
       return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 8, WHOLE>), grid, waves * 64,
               dg::w4_rows_smem<FMT, GROUP, 1, 8, WHOLE>(waves), 0, 0};
-    if (waves > 8) waves = 8;  // 64 KB of LDS
     return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 16, WHOLE>), grid, waves * 64,
             dg::w4_rows_smem<FMT, GROUP, 1, 16, WHOLE>(waves), 0, 0};
   }
+  // (at m = 16 tiles of 32 rows take 11.5 us for 4096 x 7168 against 7.7, 10.8
+  // for 2112 x 7168 against 6.5, and 19.2 for 7168 x 16384 against 20.8; at m =
+  // 17 and 32 tiles of 64 take 16.7 us for 4096 x 7168 against 12.9 and 27.3 for
+  // 7168 x 16384 against 20.0)
   const int rows = m <= 32 ? 32 : 64;
   const int tiles_n = (n + 127) / 128, tiles_m = (m + rows - 1) / rows;
   const long long tiles = (long long)tiles_n * tiles_m;
@@ -999,9 +1010,12 @@ int check_batch(int batch, int total, int most) {
   return DG_OK;
 }
 
-// Workgroups that share an attention call: two per CU (each keeps 64 KB of
-// codes in flight).  Each leaves at most two unfinished 16-row tiles.
-int kv8_workers(const DeviceInfo* info) { return 2 * info->cus; }
+// Workgroups that share an attention call: one per CU.  Its four waves keep 64
+// KB of codes in flight, enough for HBM, and fewer shares leave fewer parts to
+// join (us, one / two per CU: 4 x 65536 keys, 64 / 8 heads of 128 97 / 101; 32 x
+// 4096, 32 / 8 heads of 128 44.0 / 43.5; 4 x 8192, 16 / 4 heads of 256 31 / 34).
+// Each leaves at most two unfinished 16-row tiles.
+int kv8_workers(const DeviceInfo* info) { return info->cus; }
 size_t kv8_part_floats(int workers, int d) { return (size_t)workers * 2 * 16 * (d + 2); }
 
 }  // namespace
@@ -1493,7 +1507,8 @@ int dg_kv8_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_
   const int slots = (p.most + block - 2) / block + 1;
   if ((long long)slots >= (1LL << 24)) return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many new tokens (%d)", p.most);
   // up to 4 new tokens are at most two groups of 4 positions of a block: one
-  // wave holds them (64 single tokens, 8 heads of 128: 5.0 against 5.9 us)
+  // wave holds them (single tokens, 8 heads of 128, one wave / four: 64
+  // sequences 6.3 / 6.9 us, 128 in blocks of 16 6.4 / 8.1, one 4.6 / 4.5)
   const bool few = p.most <= 4;
   const int threads = few ? 64 : 256;
   const int items = few ? 1 : (block * d + 8191) / 8192;  // of 4 tokens by 8 values, per thread
@@ -1557,7 +1572,7 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   p.lse = lse;
   p.scale_log2 = scale * 1.44269504088896340736f;
   p.causal = causal != 0;
-  p.window = window;
+  p.window = window < (1 << 30) ? window : 1 << 30;  // no sequence is longer: differences stay in 32 bits
   p.batch = batch;
   p.total = total;
   p.h_q = h_q;
@@ -1565,7 +1580,11 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   if (num_blocks == 0) p.c.max_blocks = 0;  // no blocks: no tokens, whatever the lengths say
   void* args[] = {&p};
   // Prompts: rows in workgroups of 128 (64 for d = 256) that walk all their
-  // keys, as long as there are enough of them to fill the GPU.
+  // keys, if there is one for every CU; else 16-row tiles whose keys are shared
+  // out (us, shared out / prompts; 32 / 8 heads of 128: 4 x 256 new of 2048 106 /
+  // 64 with 256 such workgroups, 1 x 1024 of 1024 63 / 38 with 256, 4 x 128 of
+  // 2048 57 / 63 with 128, 1 x 512 of 4096 99 / 114 with 128, 1 x 16 of 4096 18 /
+  // 107 with 8).
   const int prompt_rows = d == 256 ? 64 : 128;
   const long long rows = (long long)p.most * p.group;
   const long long prompt_tiles = (rows + prompt_rows - 1) / prompt_rows;

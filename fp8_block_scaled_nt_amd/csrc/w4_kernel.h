@@ -273,13 +273,13 @@ __device__ __forceinline__ int w4_slot_a(int row, int part) {
   return (GROUP == 128 ? (part & 3) * 4 + (part >> 2) : part) ^ (row & 15);
 }
 
-// Up to 16 rows of a: a workgroup takes 16 weight rows, and its waves (4 to
-// 16) every so many-th unit of K each.  A wave keeps kDepth units of weights
-// in flight and refills a unit's registers as soon as it is used.
+// Up to 16 rows of a: a workgroup takes 16 weight rows, and its 4 or 8 waves
+// every so many-th unit of K each.  A wave keeps kW4Depth units of weights in
+// flight and refills a unit's registers as soon as it is used.
 //
 // a is the same for all workgroups and comes from L2, but a fragment of it is
-// 16 rows wide whatever m is.  So each wave loads U units of at most kW4Rows(U)
-// rows densely, a chunk ahead, and turns them into fragments through its LDS.
+// 16 rows wide whatever m is.  So each wave loads U units of ROWS rows
+// densely, a chunk ahead, and turns them into fragments through its LDS.
 // Row i of a becomes row 4 (i % 4) + i / 4 of A: of the four sums that a lane
 // has of every product, only the first E are then of rows below m, and only
 // these are scaled.
@@ -289,9 +289,8 @@ __device__ __forceinline__ int w4_slot_a(int row, int part) {
 // costs them more than a branch a unit (with separate code for the last units
 // 7.4 us for 5 x 1001 x 1056, without 4.2).
 constexpr int kW4Depth = 4;
-// rows of a that U units of it are staged for: 4 for U = 2, 8 or 16 for U = 1
 template <int FMT, int GROUP, int U, int ROWS, bool WHOLE>
-__global__ __launch_bounds__(1024) void w4_rows_kernel(W4Params p) {
+__global__ __launch_bounds__(512, 4) void w4_rows_kernel(W4Params p) {
   using Rows = W4Rows<FMT, GROUP, WHOLE>;
   constexpr int E = ROWS / 4, kLoads = U * ROWS / 4, kChunk = U * ROWS * 256;
   extern __shared__ __align__(16) uint8_t lds[];  // of each wave: a chunk of a, then Rows::kLds; later the waves' sums
