@@ -1417,7 +1417,8 @@ int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* 
   if (int s = current_device(&dev, &info)) return s;
   const W4Plan w = w4_plan(m, n, k, group, format, info);
   if (w.grid.z > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m too large (%d)", m);
-  dg::W4Params p{a, codes, scales, zeros, d, m, n, k, nullptr, nullptr};
+  const int units = (k + 127) / 128;
+  dg::W4Params p{a, codes, scales, zeros, d, m, n, k, nullptr, nullptr, units / (int)w.grid.y, units % (int)w.grid.y};
   if (w.partial_bytes) {
     char* base = nullptr;
     if (int s = ensure_workspace(dev, (hipStream_t)stream, w.partial_bytes, &base)) return s;

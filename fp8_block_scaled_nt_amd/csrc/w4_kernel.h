@@ -112,6 +112,7 @@ struct W4Params {
   int m, n, k;
   float* partial;  // w4_tile_kernel with splits: [tiles][splits] partial tiles
   int* count;      // and their arrival counters, zero between calls
+  int per, more;   // units of a split; the first `more` splits have one more (a division less in the kernel)
 };
 
 // Quarters (32 of K) of unit u that lie inside K; K is a multiple of 32, and
@@ -294,11 +295,11 @@ __global__ __launch_bounds__(512, 4) void w4_rows_kernel(W4Params p) {
   using Rows = W4Rows<FMT, GROUP, WHOLE>;
   constexpr int E = ROWS / 4, kLoads = U * ROWS / 4, kChunk = U * ROWS * 256;
   extern __shared__ __align__(16) uint8_t lds[];  // of each wave: a chunk of a, then Rows::kLds; later the waves' sums
-  const int waves = blockDim.x >> 6;
+  const int waves = blockDim.x >> 6, waves_log2 = waves == 8 ? 3 : 2;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * 16;
   const int units = (p.k + 127) / 128;
-  const int count = (units - wave + waves - 1) / waves;  // this wave's units: wave, wave + waves, ..
+  const int count = (units - wave + waves - 1) >> waves_log2;  // this wave's units: wave, wave + waves, ..
   v4u* mine = (v4u*)(lds + wave * (kChunk + Rows::kLds));
   uint8_t* mine_w = (uint8_t*)mine + kChunk;
   const Rows rows(p, n0);
@@ -399,8 +400,8 @@ __global__ __launch_bounds__(256, 2) void w4_tile_kernel(W4Params p) {
   __shared__ int s_last;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4;
   const int n0 = blockIdx.x * 128 + wave * 32, m0 = blockIdx.z * 16 * MT;
-  const int units = (p.k + 127) / 128, splits = gridDim.y;
-  const int u0 = (int)((long long)units * blockIdx.y / splits), u1 = (int)((long long)units * (blockIdx.y + 1) / splits);
+  const int split = blockIdx.y, splits = gridDim.y;
+  const int u0 = split * p.per + min(split, p.more), u1 = u0 + p.per + (split < p.more);
   const Rows rows[NT] = {Rows(p, n0), Rows(p, n0 + 16)};
 
   v4u held[2][MT];
@@ -492,10 +493,13 @@ done:
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-    for (int s0 = 0; s0 < splits; s0 += 2) {
-      v4f part[2][MT][NT];
+    // four splits' parts in flight: the loads come from beyond L2, and every
+    // round of them costs its latency
+    constexpr int kRound = 4;
+    for (int s0 = 0; s0 < splits; s0 += kRound) {
+      v4f part[kRound][MT][NT];
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < kRound; ++s)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -506,7 +510,7 @@ done:
             part[s][i][j] = __builtin_bit_cast(v4f, v);
           }
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < kRound; ++s)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
