@@ -236,7 +236,9 @@ const SkinnyConfig* find_skinny(const char* name) {
   return nullptr;
 }
 
-// the two ways of an attention call over the 8-bit cache
+// the two ways of a product with 4-bit weights, and of an attention call over the 8-bit cache
+constexpr const char* kW4RowsName = "w4_rows";
+constexpr const char* kW4TileName = "w4_tile";
 constexpr const char* kKv8Split = "kv8_split";
 constexpr const char* kKv8Prompt = "kv8_prompt";
 
@@ -250,7 +252,8 @@ int forced_config(int variant, const Config** out, int dtype = dg::kFp8, int epi
   const Config* t = configs(&cnt);
   bool known = false;
   for (int i = 0; i < cnt; ++i) known = known || strcmp(t[i].name, e) == 0;
-  known = known || find_skinny(e) != nullptr || strcmp(e, kKv8Split) == 0 || strcmp(e, kKv8Prompt) == 0;
+  known = known || find_skinny(e) != nullptr || strcmp(e, kKv8Split) == 0 || strcmp(e, kKv8Prompt) == 0 ||
+          strcmp(e, kW4RowsName) == 0 || strcmp(e, kW4TileName) == 0;
   if (!known) return fail(DG_ERR_INVALID_ARGUMENT, "DG_FORCE_CONFIG names no configuration: %s", e);
   *out = find_config(e, variant, dtype, epi);
   return DG_OK;
@@ -868,9 +871,9 @@ int check_w4(int n, int k, int group, int format, const void* zeros) {
   return DG_OK;
 }
 
-// How a product is launched: up to 16 rows of a, workgroups of 16 weight rows
-// whose waves split K; more, tiles of 128 weight rows by 32 or 64 rows of a
-// and K in splits.
+// How a product is launched: workgroups of 16 weight rows by up to 16 rows of a
+// whose waves split K, or tiles of 128 weight rows by 32 or 64 rows of a and K
+// in splits.
 struct W4Plan {
   const void* fn;
   dim3 grid;
@@ -882,7 +885,15 @@ struct W4Plan {
 template <int FMT, int GROUP, bool WHOLE>
 W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
   const int units = (k + 127) / 128;
-  if (m <= 16) {
+  // 16 x 16 tiles up to 16 rows, and beyond while each CU has no more than about
+  // 112 units of them (us, 16 x 16 / larger tiles, units per CU: 64 x 512 x 1024
+  // 3.3 / 8.8 with 4, 64 x 4096 x 1024 4.9 / 8.9 with 32, 24 x 7168 x 2048 8.4 /
+  // 8.5 with 56, 48 x 2112 x 7168 11.2 / 15.5 with 87, 32 x 4096 x 7168 13.4 /
+  // 12.5 with 112, 64 x 4096 x 7168 21.8 / 18.0 with 224).
+  const long long small_tiles = (long long)((n + 15) / 16) * ((m + 15) / 16);
+  bool small = m <= 16 || small_tiles * units <= 112LL * info->cus;
+  if (const char* e = getenv("DG_FORCE_CONFIG")) small = strcmp(e, kW4RowsName) == 0 || (small && strcmp(e, kW4TileName) != 0);
+  if (small) {
     // 8 waves for up to one and a half workgroups per CU, then 4, which leave
     // more of them side by side (us, 4 / 8 / 16 waves: 1 x 2112 x 7168 5.2 / 4.7
     // / 4.9, 1 x 4096 x 7168 6.1 / 5.9 / 6.2, 8 x 4096 x 7168 8.9 / 7.7 / 8.0,
@@ -890,7 +901,7 @@ W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
     // 4 also where 8 would have two units each or fewer (1 x 512 x 1024 3.1 /
     // 3.3 / 3.6).  With more than 8 rows always 8, as there is more to compute
     // than to load (16 x 7168 x 16384, groups of 32: 33.5 / 27.1).
-    const dim3 grid((n + 15) / 16);
+    const dim3 grid((n + 15) / 16, (m + 15) / 16);
     const int waves = units >= 16 && (m > 8 || 2LL * grid.x <= 3LL * info->cus) ? 8 : 4;
     // rows of a staged: no more than needed (8 waves; 4 / 8 / 16 rows: 1 x 4096 x
     // 7168 6.0 / 6.4 / 7.3; 4 x 4096 x 7168 7.6 / 7.7 / 8.5; 5 x 2112 x 7168 - /
@@ -904,10 +915,8 @@ W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
     return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 16, WHOLE>), grid, waves * 64,
             dg::w4_rows_smem<FMT, GROUP, 1, 16, WHOLE>(waves), 0, 0};
   }
-  // (at m = 16 tiles of 32 rows take 11.5 us for 4096 x 7168 against 7.7, 10.8
-  // for 2112 x 7168 against 6.5, and 19.2 for 7168 x 16384 against 20.8; at m =
-  // 17 and 32 tiles of 64 take 16.7 us for 4096 x 7168 against 12.9 and 27.3 for
-  // 7168 x 16384 against 20.0)
+  // (at m = 17 and 32 tiles of 64 rows take 16.7 us for 4096 x 7168 against 12.9
+  // and 27.3 for 7168 x 16384 against 20.0)
   const int rows = m <= 32 ? 32 : 64;
   const int tiles_n = (n + 127) / 128, tiles_m = (m + rows - 1) / rows;
   const long long tiles = (long long)tiles_n * tiles_m;
@@ -1416,7 +1425,7 @@ int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* 
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
   const W4Plan w = w4_plan(m, n, k, group, format, info);
-  if (w.grid.z > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m too large (%d)", m);
+  if (w.grid.y > 65535 || w.grid.z > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m too large (%d)", m);
   const int units = (k + 127) / 128;
   dg::W4Params p{a, codes, scales, zeros, d, m, n, k, nullptr, nullptr, units / (int)w.grid.y, units % (int)w.grid.y};
   if (w.partial_bytes) {

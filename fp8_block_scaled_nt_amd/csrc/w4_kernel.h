@@ -274,8 +274,8 @@ __device__ __forceinline__ int w4_slot_a(int row, int part) {
   return (GROUP == 128 ? (part & 3) * 4 + (part >> 2) : part) ^ (row & 15);
 }
 
-// Up to 16 rows of a: a workgroup takes 16 weight rows, and its 4 or 8 waves
-// every so many-th unit of K each.  A wave keeps kW4Depth units of weights in
+// Few rows of a: a workgroup takes up to 16 of them and 16 weight rows, and its
+// 4 or 8 waves every so many-th unit of K each.  A wave keeps kW4Depth units of weights in
 // flight and refills a unit's registers as soon as it is used.
 //
 // a is the same for all workgroups and comes from L2, but a fragment of it is
@@ -297,14 +297,14 @@ __global__ __launch_bounds__(512, 4) void w4_rows_kernel(W4Params p) {
   extern __shared__ __align__(16) uint8_t lds[];  // of each wave: a chunk of a, then Rows::kLds; later the waves' sums
   const int waves = blockDim.x >> 6, waves_log2 = waves == 8 ? 3 : 2;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * ROWS, m = min(p.m - m0, ROWS);
   const int units = (p.k + 127) / 128;
   const int count = (units - wave + waves - 1) >> waves_log2;  // this wave's units: wave, wave + waves, ..
   v4u* mine = (v4u*)(lds + wave * (kChunk + Rows::kLds));
   uint8_t* mine_w = (uint8_t*)mine + kChunk;
   const Rows rows(p, n0);
   const __amdgpu_buffer_rsrc_t src_a =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.a, 0, p.m * p.k * 2, kBufferRsrcWord3);
+      __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + (size_t)m0 * p.k), 0, m * p.k * 2, kBufferRsrcWord3);
 
   // chunk of a from the wave's unit number u on: load i brings piece `part` of
   // unit number u + v of row row_of(i), and zeros for rows past m
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(512, 4) void w4_rows_kernel(W4Params p) {
   auto row_of = [&](int i) { return i * (4 / U) + lane / (16 * U); };
   auto fetch = [&](int u, int i) {
     const int unit = wave + (u + v) * waves;
-    const bool in = row_of(i) < p.m && unit < units && (WHOLE || part < 4 * w4_quarters<WHOLE>(p.k, unit));
+    const bool in = row_of(i) < m && unit < units && (WHOLE || part < 4 * w4_quarters<WHOLE>(p.k, unit));
     const uint32_t at = (uint32_t)row_of(i) * (uint32_t)p.k + unit * 128 + part * 8;
     const auto x = __builtin_amdgcn_raw_buffer_load_b128(src_a, in ? at * 2 : kW4Nowhere, 0, 0);
     held[i] = __builtin_bit_cast(v4u, x);
@@ -376,7 +376,7 @@ done:
 #pragma unroll 1
   for (int w = 1; w < waves; ++w) sum += red[(w * E + e) * 64 + lane];
   const int out = q + 4 * e, col = n0 + r;
-  if (out < p.m && col < p.n) p.d[(size_t)out * p.n + col] = f32_to_bf16(sum);
+  if (out < m && col < p.n) p.d[(size_t)(m0 + out) * p.n + col] = f32_to_bf16(sum);
 }
 // LDS of a workgroup
 template <int FMT, int GROUP, int U, int ROWS, bool WHOLE>
@@ -384,7 +384,7 @@ constexpr int w4_rows_smem(int waves) {
   return waves * (U * ROWS * 256 + W4Rows<FMT, GROUP, WHOLE>::kLds);
 }
 
-// More than 16 rows of a: a workgroup of four waves takes 16 MT rows and 128
+// Many rows of a: a workgroup of four waves takes 16 MT rows and 128
 // weight rows, 32 a wave, over one split of K.  The unit of a that all four
 // waves multiply with goes through LDS, in two buffers, fetched two units
 // ahead; each wave brings its own weights, kAhead units ahead.  Splits meet in

@@ -414,6 +414,21 @@ def test_decode_loop_in_a_graph(gpu):
                  kv8.attention_ref(wide[:, :hq], want, table, [a + 1 for a in now], [0, 1, 2], d ** -0.5))
 
 
+def test_capture_needs_a_reserved_workspace(gpu):
+    rng = np.random.default_rng(30)
+    cache, table = make_cache(rng, [200], 32, 1, 64)
+    q = H.f32_to_device(bf16(rng.standard_normal((1, 4, 64))), gpu).bfloat16()
+    out, c, t, kv, cu = torch.empty_like(q), to_device(cache, gpu), i32(table, gpu), i32([200], gpu), i32([0, 1], gpu)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with pytest.raises(dg.DGError) as refused:
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            dg.kv8_attention(q, c, t, kv, cu, 1, out)
+    assert refused.value.status == 7
+    torch.cuda.synchronize()
+
+
 def test_binding_refuses(gpu):
     cache = dg.empty_kv8_cache(4, 2, 64, 16, gpu)
     t, lens, cu = i32([[0, 1]], gpu), i32([3], gpu), i32([0, 1], gpu)

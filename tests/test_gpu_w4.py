@@ -43,9 +43,17 @@ SIZES = [
 ]
 
 
+@pytest.fixture(params=["", "w4_rows", "w4_tile"])
+def way(request, monkeypatch):
+    """The library's own choice between its two ways of a product, and each of them."""
+    if request.param:
+        monkeypatch.setenv("DG_FORCE_CONFIG", request.param)
+    return request.param
+
+
 @pytest.mark.parametrize("fmt", ["e2m1", "u4"])
 @pytest.mark.parametrize("m,n,k,group", SIZES)
-def test_gemm(gpu, m, n, k, group, fmt):
+def test_gemm(way, gpu, m, n, k, group, fmt):
     print(f"[case] w4 {fmt} {m}x{n}x{k} g{group}", flush=True)
     w = oracle.quantize_w4(weights(n, k, n + k), fmt, group)
     a, ref_a = activations(m, k, m + k, gpu)
@@ -57,8 +65,56 @@ def test_gemm(gpu, m, n, k, group, fmt):
     assert H.guard_untouched(flat, m * n)
 
 
+# large enough for tiles to be chosen, K in splits, odd sizes, more than one tile of rows
+@pytest.mark.parametrize("fmt,m,n,k,group", [("u4", 65, 2113, 7264, 32), ("e2m1", 64, 4096, 7168, 64), ("u4", 33, 4001, 7168, 128)])
+def test_gemm_large(gpu, fmt, m, n, k, group):
+    print(f"[case] w4 {fmt} {m}x{n}x{k} g{group}", flush=True)
+    w = oracle.quantize_w4(weights(n, k, n + k), fmt, group)
+    a, ref_a = activations(m, k, m + k, gpu)
+    assert dg.bf16_w4_workspace_size(m, n, k, group, fmt) > 0
+    d, flat = H.sentinel_bf16((m, n), gpu, 256)
+    dev = to_device(*w, gpu)
+    dg.bf16_w4_gemm_nt(a, dev, d)
+    again = torch.empty_like(d)
+    dg.bf16_w4_gemm_nt(a, dev, again)
+    torch.cuda.synchronize()
+    res = oracle.tolerance_check(H.d_float(d), oracle.w4_gemm_ref(ref_a, *w))
+    assert res["ok"], res
+    assert H.guard_untouched(flat, m * n) and torch.equal(d, again)
+
+
+def test_gemm_split_in_a_graph(gpu):
+    m, n, k = 48, 4096, 8192
+    w = to_device(*oracle.quantize_w4(weights(n, k, 5), "u4", 128), gpu)
+    a, _ = activations(m, k, 6, gpu)
+    d = torch.empty((m, n), dtype=torch.bfloat16, device=gpu)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    # a stream that has no workspace yet cannot get one while it captures
+    with pytest.raises(dg.DGError) as refused:
+        with torch.cuda.graph(graph, stream=side):
+            dg.bf16_w4_gemm_nt(a, w, d)
+    assert refused.value.status == 7
+    torch.cuda.synchronize()
+    dg.reserve_workspace(dg.bf16_w4_workspace_size(m, n, k, 128, "u4"), side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        dg.bf16_w4_gemm_nt(a, w, d)
+    for i in range(4):
+        x, _ = activations(m, k, 7 + i, gpu)
+        want = torch.empty_like(d)
+        dg.bf16_w4_gemm_nt(x, w, want)
+        a.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(d, want)
+
+
 @pytest.mark.parametrize("fmt", ["e2m1", "u4"])
-def test_gemm_extremes(gpu, fmt):
+def test_gemm_extremes(way, gpu, fmt):
     # every code, scales over 2^+-40, zeros at both ends, large and tiny activations
     n, k, group = 48, 256, 32
     rng = np.random.default_rng(9)
@@ -79,7 +135,7 @@ def test_gemm_extremes(gpu, fmt):
             assert abs(got[i, j] - r[i, j]) <= 2 ** -8 * abs(r[i, j]) + (k + 8) * 2 ** -24 * 19 * size, (i, j)
 
 
-def test_gemm_nan_and_inf_stay_in_their_row(gpu):
+def test_gemm_nan_and_inf_stay_in_their_row(way, gpu):
     w = oracle.quantize_w4(weights(40, 256, 1), "u4", 64)
     a, _ = activations(3, 256, 2, gpu)
     clean = torch.empty((3, 40), dtype=torch.bfloat16, device=gpu)
@@ -91,7 +147,7 @@ def test_gemm_nan_and_inf_stay_in_their_row(gpu):
     assert torch.equal(d[0], clean[0]) and torch.isnan(d[1]).all() and not torch.isfinite(d[2]).any()
 
 
-def test_gemm_repeats_and_streams(gpu):
+def test_gemm_repeats_and_streams(way, gpu):
     w = to_device(*oracle.quantize_w4(weights(96, 2048, 3), "e2m1", 128), gpu)
     a, _ = activations(7, 2048, 4, gpu)
     d = [torch.empty((7, 96), dtype=torch.bfloat16, device=gpu) for _ in range(3)]
