@@ -324,48 +324,51 @@ __device__ __forceinline__ void kv8_sees(const Kv8AttnParams& p, const Kv8Seq& s
   *lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
 }
 
-// Sum over a workgroup of 256 threads; every thread gets it.  `box` is 4 longs of LDS.
-__device__ __forceinline__ long long kv8_sum256(long long v, long long* box) {
+// Inclusive running sum over a workgroup of 256 threads, and its total.
+__device__ __forceinline__ long long kv8_scan256(long long v, long long* total, long long* box) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, 64);
+  for (int s = 1; s < 64; s <<= 1) {
+    const long long o = __shfl_up(v, s, 64);
+    if (lane >= s) v += o;
+  }
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) box[threadIdx.x >> 6] = v;
+  if (lane == 63) box[wave] = v;
   __syncthreads();
-  return box[0] + box[1] + box[2] + box[3];
+  for (int w = 0; w < wave; ++w) v += box[w];
+  *total = box[0] + box[1] + box[2] + box[3];
+  return v;
 }
 
-// Units of all sequences.
-__device__ __forceinline__ long long kv8_total(const Kv8AttnParams& p, long long* box) {
-  long long all = 0;
-  for (int i = threadIdx.x; i < p.batch; i += 256) all += kv8_units(p, kv8_seq(p, i));
-  return kv8_sum256(all, box);
+// Units of 256 sequences from `first` on: this thread's, the units before
+// them among the 256, and the total.
+struct Kv8Chunk {
+  long long units, before, total;
+};
+
+__device__ __forceinline__ Kv8Chunk kv8_chunk(const Kv8AttnParams& p, int first, long long* box) {
+  const int i = first + threadIdx.x;
+  Kv8Chunk c;
+  c.units = i < p.batch ? kv8_units(p, kv8_seq(p, i)) : 0;
+  c.before = kv8_scan256(c.units, &c.total, box) - c.units;
+  return c;
 }
 
-// The sequence that unit `at` (below the total) is of, and its first unit.
-__device__ __forceinline__ void kv8_find(const Kv8AttnParams& p, long long at, int* seq, long long* seq0,
+// The sequence that unit `at` is of, and its first unit; `c` is the chunk of
+// the first 256 sequences, the only one of most batches.
+__device__ __forceinline__ void kv8_find(const Kv8AttnParams& p, Kv8Chunk c, long long at, int* seq, long long* seq0,
                                          long long* box) {
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   long long carry = 0;
-  for (int c = 0; c < p.batch; c += 256) {
-    const int i = c + tid;
-    const long long u = i < p.batch ? kv8_units(p, kv8_seq(p, i)) : 0;
-    long long sum = u;  // of the wave's lanes up to this one
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const long long o = __shfl_up(sum, s, 64);
-      if (lane >= s) sum += o;
-    }
-    __syncthreads();
-    if (lane == 63) box[wave] = sum;
-    __syncthreads();
-    long long before = carry + sum - u;
-    for (int w = 0; w < wave; ++w) before += box[w];
-    carry += box[0] + box[1] + box[2] + box[3];
-    if (u > 0 && at >= before && at < before + u) {
-      box[4] = i;
-      box[5] = before;
-    }
-    if (at < carry) break;
+  int first = 0;
+  while (at >= carry + c.total) {
+    carry += c.total;
+    first += 256;
+    c = kv8_chunk(p, first, box);
+  }
+  const long long from = carry + c.before;
+  if (at >= from && at < from + c.units) {
+    box[4] = first + threadIdx.x;
+    box[5] = from;
   }
   __syncthreads();
   *seq = (int)box[4];
@@ -752,14 +755,16 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
     if (p.lse)
       for (int e = tid; e < s.count * p.h_q; e += 256) p.lse[(size_t)s.first * p.h_q + e] = -__builtin_huge_valf();
   }
-  const long long total = kv8_total(p, box);
+  const Kv8Chunk chunk = kv8_chunk(p, 0, box);
+  long long total = chunk.total;
+  for (int i = 256; i < p.batch; i += 256) total += kv8_chunk(p, i, box).total;
   const long long share = kv8_share(p, total);
   const long long begin = blockIdx.x * share, end = min(begin + share, total);
   if (begin >= end) return;
   long long at = begin;
   int seq;
   long long seq0;  // first unit of seq
-  kv8_find(p, at, &seq, &seq0, box);
+  kv8_find(p, chunk, at, &seq, &seq0, box);
   Kv8Seq sq = kv8_seq(p, seq);
   long long units = kv8_units(p, sq);
   const __amdgpu_buffer_rsrc_t rs_u =
