@@ -736,8 +736,9 @@ __device__ __forceinline__ void kv8_write(const Kv8AttnParams& p, const Kv8Seq& 
 // complete, a barrier and a relaxed counter at the same scope follow, and the
 // workgroup that finds all others counted loads the parts, in workgroup order,
 // after a barrier behind its own count.  A tile's counter is its first
-// workgroup's: no other tile starts in that one and goes on.  (A second kernel
-// for the joining took 4 to 11 us and its launch.)
+// workgroup's: no other tile starts in that one and goes on.  (With a
+// second kernel for the joining 1 x 777 keys took 11.4 us against 8.9, 32 x
+// 4096 47 against 43, 4 x 65536 107 against 101.)
 template <int D>
 __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
   constexpr int kPitch = D + 4;

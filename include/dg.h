@@ -26,9 +26,10 @@
  *   performs no host<->device copy and no synchronisation, and reads no
  *   device value on the host; every one can be captured into a HIP graph
  *   (see the workspace rule below).
- * - Split-K workspace.  Dense calls (fp8, bf16, fp4) whose K is split over
- *   several workgroups keep fp32 partial tiles and arrival counters in a
- *   library-owned workspace, one per (device, stream).  Calls on one stream
+ * - Split-K workspace.  Dense calls (fp8, bf16, fp4, 4-bit weights) whose K is
+ *   split over several workgroups, and attention calls whose keys are, keep
+ *   fp32 partial results and arrival counters in a library-owned workspace,
+ *   one per (device, stream).  Calls on one stream
  *   share it in stream order; calls on different streams never share one, so
  *   split-K calls may overlap in time on different streams.  A call that
  *   needs more than its stream's workspace holds makes a larger one (one
@@ -39,7 +40,8 @@
  *   captured earlier may still use it.  While `stream` is capturing a graph
  *   such a growth is refused with DG_ERR_WORKSPACE and nothing is enqueued:
  *   size the workspace first with dg_reserve_workspace(bytes, stream), bytes
- *   from dg_dense_workspace_size.  A captured call keeps using the workspace
+ *   from dg_dense_workspace_size (dg_bf16_w4_workspace_size,
+ *   dg_kv8_attention_workspace_size).  A captured call keeps using the workspace
  *   its capture stream had; a replay must not overlap in time with other
  *   split-K work on that same workspace (replaying on the capture stream, or
  *   on any stream ordered with it, is safe).  dg_fp8_gemm_nt_noalloc uses a
@@ -342,7 +344,8 @@ typedef enum { DG_W4_E2M1 = 0, DG_W4_U4 = 1 } dg_w4_format;
 int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
                        uint16_t* d, int m, int n, int k, int group, int format, dg_stream_t stream);
 
-/* Bytes of the stream's workspace that dg_bf16_w4_gemm_nt takes for a shape on the current device (0 for m <= 16). */
+/* Bytes of the stream's workspace that dg_bf16_w4_gemm_nt takes for a shape on
+ * the current device: 0 for m <= 16, and for more rows while the product is small. */
 int dg_bf16_w4_workspace_size(int m, int n, int k, int group, int format, size_t* bytes);
 
 /*
