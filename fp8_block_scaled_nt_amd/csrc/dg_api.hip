@@ -886,12 +886,13 @@ template <int FMT, int GROUP, bool WHOLE>
 W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
   const int units = (k + 127) / 128;
   // 16 x 16 tiles up to 16 rows, and beyond while each CU has no more than about
-  // 112 units of them (us, 16 x 16 / larger tiles, units per CU: 64 x 512 x 1024
+  // 100 units of them (us, 16 x 16 / larger tiles, units per CU: 64 x 512 x 1024
   // 3.3 / 8.8 with 4, 64 x 4096 x 1024 4.9 / 8.9 with 32, 24 x 7168 x 2048 8.4 /
   // 8.5 with 56, 48 x 2112 x 7168 11.2 / 15.5 with 87, 32 x 4096 x 7168 13.4 /
-  // 12.5 with 112, 64 x 4096 x 7168 21.8 / 18.0 with 224).
+  // 12.5 and 64 x 7168 x 2048 12.6 / 10.8 with 112, 64 x 4096 x 7168 21.8 / 18.0
+  // with 224).
   const long long small_tiles = (long long)((n + 15) / 16) * ((m + 15) / 16);
-  bool small = m <= 16 || small_tiles * units <= 112LL * info->cus;
+  bool small = m <= 16 || small_tiles * units <= 100LL * info->cus;
   if (const char* e = getenv("DG_FORCE_CONFIG")) small = strcmp(e, kW4RowsName) == 0 || (small && strcmp(e, kW4TileName) != 0);
   if (small) {
     // 8 waves for up to one and a half workgroups per CU, then 4, which leave
@@ -920,11 +921,25 @@ W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
   const int rows = m <= 32 ? 32 : 64;
   const int tiles_n = (n + 127) / 128, tiles_m = (m + rows - 1) / rows;
   const long long tiles = (long long)tiles_n * tiles_m;
-  // two workgroups per CU, at least four units a split, at most 8 splits (the
-  // last of them adds all up): 64 x 2112 x 7168 15.1 us with 8, 18.6 with 16
-  long long splits = 2LL * info->cus / tiles;
-  if (splits > units / 4) splits = units / 4;
-  if (splits > 8) splits = 8;
+  // At least four units a split and at most 8 splits (the last of them adds all
+  // up: 64 x 2112 x 7168 15.1 us with 8, 18.6 with 16).  Within that, as many as
+  // give each CU one workgroup or, where those have many units, two.  One takes
+  // about 0.6 us a unit, two side by side 1.0 us for a unit of each and 2.5 us
+  // more (us, one / two per CU: 128 x 2112 x 7168 15.4 / 19.9, 128 x 4096 x 7168
+  // 16.8 / 20.6, 48 x 5120 x 5120 14.9 / 16.8, 64 x 10240 x 4096 18.7 / 19.5;
+  // 200 x 2112 x 7168 31.5 / 29.4, 96 x 7168 x 7168 35.1 / 31.6, 128 x 7168 x
+  // 16384 47.7 / 43.6, 512 x 2112 x 7168 39.8 / 31.3).  Other shapes, against two
+  // per CU always: 70 x 2112 x 16384 28.1 for 34.9, 160 x 1536 x 8192 17.7 for
+  // 22.0, 40 x 6144 x 6144 15.1 for 16.1; near the border u4 can lose (24 x 14336
+  // x 4096 16.5 for 15.5, 80 x 8192 x 4096 23.2 for 22.0).
+  const long long most = units / 4 < 8 ? units / 4 : 8;
+  const auto fit = [&](long long per_cu) {
+    const long long s = per_cu * info->cus / tiles;
+    return s < 1 || most < 1 ? 1 : s < most ? s : most;
+  };
+  const long long one = fit(1), two = fit(2);
+  const long long of_one = (units + one - 1) / one, of_two = (units + two - 1) / two;
+  long long splits = tiles > info->cus || 6 * of_one > 10 * of_two + 25 ? two : one;
   if (const char* e = getenv("DG_SPLIT_K")) splits = atoi(e) < units ? atoi(e) : units;
   if (splits < 1 || tiles > (long long)kCounterInts) splits = 1;
   return {rows == 32 ? reinterpret_cast<const void*>(&dg::w4_tile_kernel<FMT, GROUP, 2, WHOLE>)
