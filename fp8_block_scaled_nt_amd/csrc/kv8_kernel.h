@@ -26,6 +26,7 @@ namespace dg {
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v2f __attribute__((ext_vector_type(2)));
+typedef int16_t v2s __attribute__((ext_vector_type(2)));
 
 struct Kv8Cache {
   uint8_t* k_codes;
@@ -253,18 +254,34 @@ __global__ __launch_bounds__(THREADS) void kv8_append_kernel(Kv8AppendParams p) 
 // the queries of one key/value head: row r of a sequence is query r / g, head
 // r % g of the group of g = h_q / h_kv heads that share the keys.
 //
-// Per row the kernels carry a reference m close to the running maximum of t[j] = log2(e) x[j] +
-// log2(vs[j]), u = sum_j 2^(t[j] - m) vc[j] and l = sum_j 2^(t[j] - m) / vs[j],
-// all in fp32.  With the values' scale inside the exponent, p = 2^(t - m) is
-// what multiplies the codes, whichever block they are in: one accumulator
-// serves blocks of any scale, o = u / l, and lse = (m + log2 l) ln 2.
+// Per row the kernels carry a reference m, 7 to 11 below the running maximum of
+// t[j] = log2(e) x[j] + log2(vs[j]), u = sum_j 2^(t[j] - m) vc[j] and l = sum_j
+// 2^(t[j] - m) / vs[j], all in fp32.  With the values' scale inside the
+// exponent, p = 2^(t - m) is what multiplies the codes, whichever block they are
+// in: one accumulator serves blocks of any scale, o = u / l, and lse = (m + log2
+// l) ln 2.
 //
 // Both products run on the matrix cores with the 16 (or 32) rows as columns:
 // x^T = K q^T in bf16 (e4m3 codes are exact in bf16, q is bf16 anyway) and
-// u^T = V^T p^T in fp16.  fp16 holds e4m3 codes exactly too and rounds p to
-// 11 bits where bf16 keeps 8; p is at most 2^8, and where it falls below 2^-14,
-// to fp16's steps of 2^-24, beside a p of 2^-8 or more in the same row, it adds
-// nothing that bf16 output could show.
+// u^T = V^T p^T with p in one of two forms.  A small p may be all that an element
+// has, as the codes beside a large one may be zeros in its dimension:
+//
+//   narrow: fp16, which holds e4m3 codes exactly too and rounds p to 11 bits.  p
+//     goes up to 2^11, its normal range ends 2^-21 or less below the row's
+//     largest p, and what lies below is off by at most 2^-32 of that largest.
+//     Only where value scales are within 2^kKv8Near of the largest one met: an
+//     element is then off by no more than 2^(kKv8Near - 32) of the largest weight
+//     times value scale, per key, whatever the codes are.
+//   wide: two bf16 pieces, 16 bits with the range of fp32, against codes in
+//     bf16: where value scales lie further apart, and in steps that need masks
+//     (rows that see few keys, all of them in such a step, have large outputs
+//     that no averaging of rounding errors helps: 11 bits left 5 of 493568
+//     outputs of prompts of up to 150 tokens off by more than 70% of 8e-3 |r| +
+//     1e-3 rms, the worst by 129%).
+//
+// (With fp16 alone prompts of 2048 took 296 us against 297, 4 x 2048 within a
+// window of 512 144 against 151, 32 x 4096 single tokens 45.4 against 46.6; where
+// value scales were 2^16 apart elements were then off by up to all of themselves.)
 // The keys of a 64-key step are dealt to the rows of the A operand so that
 // lane group g (lanes 16 g ..) ends up with p for keys 16 g .. 16 g + 15,
 // which is how a lane of the second product's B operand wants them against
@@ -289,7 +306,12 @@ struct Kv8AttnParams {
 };
 
 constexpr int kKv8Step = 64;       // keys of one step of one wave
-constexpr float kKv8Slack = 8.f;  // log2 of how far p may pass 1 before its reference moves
+constexpr float kKv8Lead = 7.f;    // log2 of a row's largest p when its reference has moved
+constexpr float kKv8Slack = 11.f;  // and of how large p may get before it moves again
+constexpr float kKv8WideLog2 = 112.f;  // log2 of what p is multiplied with in the wide form: 16 keys' sum stays below 2^128
+constexpr float kKv8WideInv = 1.925929944387236e-34f;  // 2^-112
+constexpr float kKv8Near = 4.f;        // log2 of how far value scales may lie apart in narrow steps
+constexpr float kKv8NearRatio = 16.f;  // 2^kKv8Near
 constexpr float kKv8MinVs = 5.421010862427522e-20f;  // 2^-64: scales below are taken as this
 
 // What a sequence asks for.
@@ -414,10 +436,27 @@ __device__ __forceinline__ uint32_t pack2_f16(float a, float b) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
-// Halves of `w` (two fp16) that are NaN, as 1 in bit 0 and bit 16.
-__device__ __forceinline__ uint32_t f16_nans(uint32_t w) {
-  // a magnitude above that of infinity carries into the sign bit
-  return ((w & 0x7FFF7FFFu) + 0x03FF03FFu) >> 15 & 0x00010001u;
+// Two e4m3 values held as fp16, as bf16 times 2^-112: the exponent's and the
+// three upper fraction bits move to their places, and the biases differ by 112.
+// `keep` has kKv8Halves' bits of the halves to keep; the others become zero.
+// NaN keeps its all-ones exponent, of five bits, which is a finite value then.
+constexpr uint32_t kKv8Halves = 0x8FFF8FFFu;
+__device__ __forceinline__ uint32_t f16_to_small_bf16(uint32_t w, uint32_t keep) {
+  const v2s r = __builtin_bit_cast(v2s, w) >> 3;
+  return __builtin_bit_cast(uint32_t, r) & keep;
+}
+// Which halves of such a pair are NaN (e4m3 has no infinities), as 1 in bit 0 and bit 16.
+__device__ __forceinline__ uint32_t small_bf16_nans(uint32_t w) {
+  return ((w & 0x0FFF0FFFu) + 0x00800080u) >> 12 & 0x00010001u;
+}
+
+// The largest x of the four lane groups (of lanes l % 16 alike).
+__device__ __forceinline__ float kv8_group_max(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const v2u r = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+  const uint32_t c = __float_as_uint(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+  const v2u s = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane16_swap(c, c, false, false));
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
 
 // A wave's running state for 16 MT rows: lane l holds, for each tile of 16,
@@ -469,14 +508,23 @@ __device__ __forceinline__ Kv8Scale kv8_scale_of(const Kv8Run& run, float scale_
   return Kv8Scale{run.ks * scale_log2, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs), there};
 }
 
+// Whether a step needs the wide form for its value scales, whose log2 are lv
+// (-inf: the block is not there); `top` is the largest so far and takes this
+// step's in.
+__device__ __forceinline__ bool kv8_far(float lv, float& top) {
+  if (__any(lv > top)) top = fmaxf(top, kv8_group_max(lv));
+  return __any(lv > -__builtin_huge_valf() && lv < top - kKv8Near);
+}
+
 // What remains of a step when its raw products s[4 j + e] with keys run_v + 4 j
-// + e are there: t = s ks + lv, the reference, p, and the second product.
-template <int D, int MT, bool MASKED, class LoadV>
+// + e are there: t = s ks + lv, the reference, p, and the second product,
+// narrow or (WIDE) wide and with masks.
+template <int D, int MT, bool WIDE, class LoadV>
 __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Scale& sc, const Kv8Rows<MT>& rows,
                                                  float (&s)[MT][16], Kv8State<D, MT>& st, LoadV load_v) {
   float ks = sc.ks, lv = sc.lv;
   uint32_t seen[MT];  // bit i: the row sees key run_v + i
-  if constexpr (MASKED) {
+  if constexpr (WIDE) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       // keys [lo, hi) of the 16, none if the block is not there
@@ -497,11 +545,10 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
     m = m * ks + lv;
     m = fmaxf(m, __shfl_xor(m, 16, 64));
     m = fmaxf(m, __shfl_xor(m, 32, 64));
-    // The reference follows the maximum only when a row's has grown by more
-    // than kKv8Slack: p is then at most 2^kKv8Slack, and few steps pay for
-    // scaling u.
+    // The reference follows the maximum only when a row's p would pass
+    // 2^kKv8Slack, and is put 2^kKv8Lead below it: few steps pay for scaling u.
     if (__any(m > st.m[t] + kKv8Slack)) {
-      m = fmaxf(m, st.m[t]);
+      m = fmaxf(m - kKv8Lead, st.m[t]);
       const float shrink = __builtin_amdgcn_exp2f(st.m[t] - (m == -__builtin_huge_valf() ? 0.f : m));
       st.l[t] *= shrink;
 #pragma unroll
@@ -509,30 +556,25 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
       st.m[t] = m;
     }
     const float ref = st.m[t] == -__builtin_huge_valf() ? 0.f : st.m[t];  // nothing seen yet: any finite reference
-    const float off = lv - ref;
+    const float off = lv - ref + (WIDE ? kKv8WideLog2 : 0.f);
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       const float p0 = __builtin_amdgcn_exp2f(s[t][i] * ks + off), p1 = __builtin_amdgcn_exp2f(s[t][i + 1] * ks + off);
       sum[0] += p0;
       sum[1] += p1;
-      const uint32_t both = pack2_f16(p0, p1);
-      pw[t][i / 8][(i / 2) & 3] = both;
-      if constexpr (MASKED) {
-        // What fp16 left of p, as a second fp16: rows that see few keys (all
-        // of them in a masked step) have large outputs that no averaging of
-        // the rounding errors helps; with one piece 5 of 493568 outputs of
-        // prompts of up to 150 tokens were off by more than 70% of 8e-3 |r| +
-        // 1e-3 rms, the worst by 129%, with two in these steps none, the
-        // worst 49% (bf16's own rounding).
-        const v2h hi = __builtin_bit_cast(v2h, both);
-        rest[t][i / 8][(i / 2) & 3] = pack2_f16(p0 - (float)hi[0], p1 - (float)hi[1]);
+      if constexpr (!WIDE) {
+        pw[t][i / 8][(i / 2) & 3] = pack2_f16(p0, p1);
+      } else {
+        const uint32_t both = pack2_bf16(p0, p1);
+        pw[t][i / 8][(i / 2) & 3] = both;
+        rest[t][i / 8][(i / 2) & 3] = pack2_bf16(p0 - __uint_as_float(both << 16), p1 - __uint_as_float(both & 0xFFFF0000u));
       }
     }
-    st.l[t] += (sum[0] + sum[1]) * sc.inv_vs;
+    st.l[t] += (sum[0] + sum[1]) * (WIDE ? kKv8WideInv : 1.f) * sc.inv_vs;
   }
-  if constexpr (!MASKED) {
-    v8h v[2][2];
+  if constexpr (!WIDE) {
+    v4u v[2][2];
     v[0][0] = load_v(0, 0);
     v[0][1] = load_v(0, 1);
 #pragma unroll
@@ -546,7 +588,8 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
-          st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[i & 1][h], __builtin_bit_cast(v8h, pw[t][h]), st.u[t][i], 0, 0, 0);
+          st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, v[i & 1][h]),
+                                                                __builtin_bit_cast(v8h, pw[t][h]), st.u[t][i], 0, 0, 0);
     }
     return;
   }
@@ -559,25 +602,25 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int n = sc.there ? kv - (run_v + 2 * i) : 0;
-    keep[i] = n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u;
+    keep[i] = (n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u) & kKv8Halves;
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     __builtin_amdgcn_sched_barrier(0);
-    v4u w[2] = {__builtin_bit_cast(v4u, load_v(i, 0)), __builtin_bit_cast(v4u, load_v(i, 1))};
+    v4u w[2] = {load_v(i, 0), load_v(i, 1)};
     uint32_t bad = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      w[e / 4][e % 4] &= keep[e];
-      bad |= f16_nans(w[e / 4][e % 4]);
+      w[e / 4][e % 4] = f16_to_small_bf16(w[e / 4][e % 4], keep[e]);
+      bad |= small_bf16_nans(w[e / 4][e % 4]);
     }
     if (__any(bad != 0)) {
       v4u ind[2];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t nan = f16_nans(w[e / 4][e % 4]);
+        const uint32_t nan = small_bf16_nans(w[e / 4][e % 4]);
         w[e / 4][e % 4] &= ~(nan * 0xFFFFu);
-        ind[e / 4][e % 4] = nan * 0x3C00u;
+        ind[e / 4][e % 4] = nan * 0x3F80u;
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
@@ -587,22 +630,22 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
           v4u sw;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            sw[e] = (seen[t] >> (8 * h + 2 * e) & 1u) * 0x3C00u | (seen[t] >> (8 * h + 2 * e + 1) & 1u) * 0x3C000000u;
-          cnt = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, ind[h]), __builtin_bit_cast(v8h, sw),
+            sw[e] = (seen[t] >> (8 * h + 2 * e) & 1u) * 0x3F80u | (seen[t] >> (8 * h + 2 * e + 1) & 1u) * 0x3F800000u;
+          cnt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, ind[h]), __builtin_bit_cast(v8bf, sw),
                                                        cnt, 0, 0, 0);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.u[t][i][e] = cnt[e] > 0.f ? __builtin_nanf("") : st.u[t][i][e];
       }
     }
-    const v8h v0 = __builtin_bit_cast(v8h, w[0]), v1 = __builtin_bit_cast(v8h, w[1]);
+    const v8bf v0 = __builtin_bit_cast(v8bf, w[0]), v1 = __builtin_bit_cast(v8bf, w[1]);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       v4f u = st.u[t][i];
-      u = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, __builtin_bit_cast(v8h, rest[t][0]), u, 0, 0, 0);
-      u = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, __builtin_bit_cast(v8h, rest[t][1]), u, 0, 0, 0);
-      u = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, __builtin_bit_cast(v8h, pw[t][0]), u, 0, 0, 0);
-      st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, __builtin_bit_cast(v8h, pw[t][1]), u, 0, 0, 0);
+      u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, __builtin_bit_cast(v8bf, rest[t][0]), u, 0, 0, 0);
+      u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, __builtin_bit_cast(v8bf, rest[t][1]), u, 0, 0, 0);
+      u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, __builtin_bit_cast(v8bf, pw[t][0]), u, 0, 0, 0);
+      st.u[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, __builtin_bit_cast(v8bf, pw[t][1]), u, 0, 0, 0);
     }
   }
 }
@@ -610,11 +653,11 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
 // One step: 64 keys from token `base` on, against 16 MT rows.  load_k(j, h, o)
 // gives the lane's values h * 64 + 16 g + 8 o .. of key (a / 4) * 16 + 4 j +
 // a % 4, load_v(i, o) those of dimension 16 i + a at keys 16 g + 8 o .. (a =
-// lane % 16, g = lane / 16), load_q(t, i) B fragment i of the lane's row of
-// tile t.  MASKED:
-// some row may not see some of the keys, or the sequence end inside the step;
-// such steps are the first and last ones of a run and have loops of their own.
-template <int D, int MT, bool MASKED, class LoadQ, class LoadK, class LoadV>
+// lane % 16, g = lane / 16) in fp16, load_q(t, i) B fragment i of the lane's row of
+// tile t.  WIDE: some row may not see some of the keys, or the sequence end
+// inside the step (such steps are the first and last ones of a run), or the
+// value scales are far apart.
+template <int D, int MT, bool WIDE, class LoadQ, class LoadK, class LoadV>
 __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, const Kv8Rows<MT>& rows,
                                          Kv8State<D, MT>& st, LoadQ load_q, LoadK load_k, LoadV load_v) {
   float s[MT][16];
@@ -650,7 +693,7 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, c
   }
   __builtin_amdgcn_sched_barrier(0);
   const int run_v = base + ((threadIdx.x & 63) >> 4) * 16;
-  kv8_rest_of_step<D, MT, MASKED>(kv, run_v, sc, rows, s, st, load_v);
+  kv8_rest_of_step<D, MT, WIDE>(kv, run_v, sc, rows, s, st, load_v);
 }
 
 // The B fragments of one row of q.
@@ -804,6 +847,7 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
     const int last = min(t1, (any_hi + kKv8Step - 1) / kKv8Step - sq.step0);
     if (first < last) {
       Kv8Regs<D> regs;
+      float top = -__builtin_huge_valf();  // log2 of the largest value scale so far
       int base = (sq.step0 + first) * kKv8Step, pk, pv, next_pk, next_pv;
       kv8_pages(p.c, seq, sq.kv, base, &pk, &pv);
       kv8_pages(p.c, seq, sq.kv, base + 4 * kKv8Step, &next_pk, &next_pv);
@@ -812,25 +856,26 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
       regs.load_v(p.c, head, base, pv);
       for (int t = first; t < last; t += 4) {
         const bool more = t + 4 < last;
-        const bool masked = kv8_masked(base, all_lo, all_hi, pv >= 0);
         const Kv8Scale now = kv8_scale_of(run, p.scale_log2);
+        const bool far = kv8_far(now.there ? now.lv : -__builtin_huge_valf(), top);
+        const bool wide = kv8_masked(base, all_lo, all_hi, pv >= 0) || far;
         const int here = base;
         base += 4 * kKv8Step;
         pk = next_pk;
         pv = next_pv;
         kv8_pages(p.c, seq, sq.kv, base + 4 * kKv8Step, &next_pk, &next_pv);
-        auto step = [&](auto mask) {
-          kv8_step<D, 1, decltype(mask)::value>(sq.kv, here, now, see, st, [&](int t, int i) { return qf[t][i]; },
+        auto step = [&](auto form) {
+          kv8_step<D, 1, decltype(form)::value>(sq.kv, here, now, see, st, [&](int t, int i) { return qf[t][i]; },
                        [&](int j, int h, int o) { return e4m3_to_bf16(regs.k[j][h][2 * o], regs.k[j][h][2 * o + 1]); },
                        [&](int i, int o) {
                          if (i == 0 && o == 0 && more) {
                            regs.load_k(p.c, head, base, pk);
                            run = kv8_run(p.c, head, pv);
                          }
-                         return e4m3_to_f16(regs.v[i][2 * o], regs.v[i][2 * o + 1]);
+                         return __builtin_bit_cast(v4u, e4m3_to_f16(regs.v[i][2 * o], regs.v[i][2 * o + 1]));
                        });
         };
-        if (masked) step(std::true_type{}); else step(std::false_type{});
+        if (wide) step(std::true_type{}); else step(std::false_type{});
         if (more) regs.load_v(p.c, head, base, pv);
       }
     }
@@ -948,6 +993,7 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
   constexpr int kRows = 64 * MT, kParts = D / 8, kPer = D / 64;
   __shared__ v4u s_k[2][64 * kParts], s_v[2][D * 8];  // pieces of 8 values
   __shared__ Kv8Scale s_scale[2][4];
+  __shared__ float s_vs[4][2];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
   const int head = blockIdx.x, seq = blockIdx.y;
   const Kv8Seq sq = kv8_seq(p, seq);
@@ -1029,10 +1075,30 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
   if (first < last) {
     look(first * kKv8Step);
     fetch(first * kKv8Step);
+    // the smallest and the largest value scale of the blocks that the workgroup sees
+    float least = __builtin_huge_valf(), most = 0.f;
+    const int j1 = min((min(any_hi, sq.kv) - 1) >> c.block_log2, c.max_blocks - 1);
+#pragma unroll 4
+    for (int j = (any_lo >> c.block_log2) + tid; j <= j1; j += 256) {
+      const int at = c.table[(size_t)seq * c.max_blocks + j];
+      if ((unsigned)at >= (unsigned)c.num_blocks) continue;
+      const float vs = fmaxf(c.v_scales[(size_t)at * c.h_kv + head], kKv8MinVs);
+      least = fminf(least, vs);
+      most = fmaxf(most, vs);
+    }
+#pragma unroll
+    for (int i = 32; i >= 1; i >>= 1) {
+      least = fminf(least, __shfl_xor(least, i, 64));
+      most = fmaxf(most, __shfl_xor(most, i, 64));
+    }
+    if (lane == 0) {
+      s_vs[wave][0] = least;
+      s_vs[wave][1] = most;
+    }
     put(0);
     __syncthreads();
     int s = first;
-    auto steps = [&](int until, auto mask) {
+    auto steps = [&](int until, auto form) {
 #pragma unroll 1
       for (; s < until; ++s) {
         const int base = s * kKv8Step, buf = (s - first) & 1;
@@ -1041,20 +1107,29 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
           const v4u* k_at = s_k[buf];
           const v4u* v_at = s_v[buf];
           const Kv8Scale now = s_scale[buf][g];
-          kv8_step<D, MT, decltype(mask)::value>(
+          kv8_step<D, MT, decltype(form)::value>(
               sq.kv, base, now, see, st,
               [&](int t, int i) { return qf[t][i]; },
               [&](int j, int h, int o) {
                 return __builtin_bit_cast(v8bf, k_at[kv8_slot<kParts>(j * 16 + a, h * 8 + g * 2 + o)]);
               },
-              [&](int i, int o) { return __builtin_bit_cast(v8h, v_at[kv8_slot<8>(i * 16 + a, g * 2 + o)]); });
+              [&](int i, int o) { return v_at[kv8_slot<8>(i * 16 + a, g * 2 + o)]; });
         }
         put(buf ^ 1);
         __syncthreads();
       }
     };
-    // masked steps, steps that every row of the workgroup sees wholly, masked steps
-    const int whole0 = min(max((all_lo + kKv8Step - 1) / kKv8Step, first), last), whole1 = max(all_hi / kKv8Step, whole0);
+    // Wide steps, steps that every row of the workgroup sees wholly, wide
+    // steps; all wide if value scales are far apart.  (Decided for each step,
+    // from LDS and before its first product, it took the narrow steps 4 %.)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      least = fminf(least, s_vs[w][0]);
+      most = fmaxf(most, s_vs[w][1]);
+    }
+    const bool far = __any(most > least * kKv8NearRatio);  // uniform, and known to be
+    const int whole0 = far ? last : min(max((all_lo + kKv8Step - 1) / kKv8Step, first), last);
+    const int whole1 = max(all_hi / kKv8Step, whole0);
 #pragma unroll 1
     for (int part = 0; part < 2; ++part) {
       steps(part == 0 ? whole0 : last, std::true_type{});

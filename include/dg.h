@@ -418,11 +418,14 @@ int dg_kv8_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_
  * only).  A row that sees no token gets out = 0 and lse = -inf.  A NaN in a
  * key or value reaches the rows that see it and no others; what the cache
  * holds past kv_lens[s] reaches none.  Scales must be positive (a value scale
- * below 2^-64 counts as 2^-64).
+ * below 2^-64 counts as 2^-64), and the value scales that a row sees within
+ * 2^100 of each other.
  * out is bf16 [total][h_q][d], lse fp32 [total][h_q] or NULL.  max_q is the
  * most queries of one sequence.  Scores, the softmax's running maximum and
- * sums and the output's accumulator are fp32; probabilities are rounded to
- * fp16 for the second product.  Results do not depend on anything but the
+ * sums and the output's accumulator are fp32; for the second product each
+ * probability times its value scale is rounded to 11 bits or more (and, where
+ * the value scales of a sequence are within 2^4 of each other, to steps of
+ * 2^-31 of the row's largest).  Results do not depend on anything but the
  * arguments: the same call gives the same bits.
  * Needs dg_kv8_attention_workspace_size bytes of the stream's workspace (see
  * the workspace rule above: reserve it before capturing).  The work is shared
