@@ -49,11 +49,13 @@ __device__ __forceinline__ int kv8_page(const Kv8Cache& c, int seq, int token) {
 
 // New rows of sequence `seq`: [first, first + count) of the packed tokens.
 // cu holds batch + 1 running sums; whatever it holds, the range stays inside
-// the `total` packed tokens, and count is at most `most`.
-__device__ __forceinline__ void kv8_rows(const int32_t* cu, int seq, int total, int most, int* first, int* count) {
-  const int lo = min(max(cu[seq], 0), total), hi = min(max(cu[seq + 1], 0), total);
+// the `total` packed tokens, and count is at most `most`.  Returns the
+// sequence's rows without that limit.
+__device__ __forceinline__ int kv8_rows(const int32_t* cu, int seq, int total, int most, int* first, int* count) {
+  const int lo = min(max(cu[seq], 0), total), hi = min(max(cu[seq + 1], 0), total), all = max(hi - lo, 0);
   *first = lo;
-  *count = min(max(hi - lo, 0), most);
+  *count = min(all, most);
+  return all;
 }
 
 // ---- append
@@ -317,18 +319,20 @@ constexpr float kKv8MinVs = 5.421010862427522e-20f;  // 2^-64: scales below are 
 // What a sequence asks for.
 struct Kv8Seq {
   int first, count;   // its rows of q
-  int kv;             // its tokens in the cache
+  int kv;             // its tokens in the cache that the table has room for
+  int pos;            // where its first query stands (negative: before the cache), by its length whatever the table's
   int step0, steps;   // steps of keys that any of its queries sees: step0 .. step0 + steps - 1
   int tiles;          // 16-row tiles of one key/value head
 };
 
 __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8AttnParams& p, int seq) {
   Kv8Seq s;
-  kv8_rows(p.cu, seq, p.total, p.most, &s.first, &s.count);
+  const int all = kv8_rows(p.cu, seq, p.total, p.most, &s.first, &s.count);
   const long long room = (long long)p.c.max_blocks << p.c.block_log2;
   const int kv = max(p.kv_lens[seq], 0);
   s.kv = kv < room ? kv : (int)room;
-  const int lo = p.window > 0 ? max(s.kv - s.count - p.window + 1, 0) : 0;
+  s.pos = kv - all;
+  const int lo = p.window > 0 ? max(max(s.pos, -1) - p.window + 1, 0) : 0;
   s.step0 = min(lo, s.kv) / kKv8Step;
   s.steps = (s.kv + kKv8Step - 1) / kKv8Step - s.step0;
   s.tiles = (s.count * p.group + 15) / 16;
@@ -341,8 +345,8 @@ __device__ __forceinline__ long long kv8_units(const Kv8AttnParams& p, const Kv8
 
 // Keys [lo, hi) that query `i` of the sequence sees.
 __device__ __forceinline__ void kv8_sees(const Kv8AttnParams& p, const Kv8Seq& s, int i, int* lo, int* hi) {
-  const int pos = s.kv - s.count + i;  // where the query stands (negative: before the cache, it sees nothing)
-  *hi = p.causal ? min(max(pos + 1, 0), s.kv) : s.kv;
+  const int pos = max(s.pos + i, -1);  // -1: before the cache, it sees nothing if causal
+  *hi = p.causal ? min(pos + 1, s.kv) : s.kv;
   *lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
 }
 

@@ -77,17 +77,20 @@ def gather(cache, table, seq, head, length):
 
 
 def attention_ref(q, cache, table, kv_lens, cu, scale, causal=True, window=0):
-    """(out [total, h_q, d], lse [total, h_q]) in float64, row by row over the keys it sees."""
+    """(out [total, h_q, d], lse [total, h_q]) in float64, row by row over the keys it sees.
+
+    Queries stand where the lengths say; tokens past the table's room are seen by none."""
     total, hq, d = q.shape
     heads = cache[0].shape[1]
     room = table.shape[1] * cache[0].shape[2]
     out, lse = np.zeros((total, hq, d)), np.full((total, hq), -np.inf)
     for seq in range(table.shape[0]):
-        n, kv = int(cu[seq + 1] - cu[seq]), min(max(int(kv_lens[seq]), 0), room)
+        n, length = int(cu[seq + 1] - cu[seq]), max(int(kv_lens[seq]), 0)
+        kv = min(length, room)
         for head in range(heads):
             keys, vals, there = gather(cache, table, seq, head, kv)
             for i in range(n):
-                pos = kv - n + i
+                pos = length - n + i
                 hi = min(max(pos + 1, 0), kv) if causal else kv
                 lo = max(pos - window + 1, 0) if window else 0
                 see = [j for j in range(lo, hi) if there[j]]
