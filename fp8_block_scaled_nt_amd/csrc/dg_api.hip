@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -1609,22 +1610,44 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   // out (us, shared out / prompts; 32 / 8 heads of 128: 4 x 256 new of 2048 106 /
   // 64 with 256 such workgroups, 1 x 1024 of 1024 63 / 38 with 256, 4 x 128 of
   // 2048 57 / 63 with 128, 1 x 512 of 4096 99 / 114 with 128, 1 x 16 of 4096 18 /
-  // 107 with 8).
+  // 107 with 8).  The workgroups are counted from what the host knows: the
+  // packed rows, and half a workgroup more for each sequence that can have 64
+  // rows.  Sequences of fewer rows, whose keys a workgroup would walk for a few
+  // rows alone, are shared out in a second launch (us, one launch / two: 8 single
+  // tokens of 65536 beside a prompt of 2048 1550 / 272, 63 of 32768 1033 / 898,
+  // 28 of 8192 beside 4 x 512 of 2048 226 / 193; prompts of unequal lengths pay
+  // for it: 4 of up to 2048 behind up to 2048 295 / 303).
   const int prompt_rows = d == 256 ? 64 : 128;
-  const long long rows = (long long)p.most * p.group;
+  constexpr int kFew = 64;
+  const long long rows = (long long)p.most * p.group, all_rows = (long long)total * p.group;
   const long long prompt_tiles = (rows + prompt_rows - 1) / prompt_rows;
-  bool prompt = rows >= 64 && prompt_tiles * h_kv * batch >= info->cus;
-  if (const char* e = getenv("DG_FORCE_CONFIG"))
-    prompt = strcmp(e, kKv8Prompt) == 0 || (prompt && strcmp(e, kKv8Split) != 0);
-  if (prompt && prompt_tiles <= 65535) {
+  const long long long_seqs = all_rows / kFew < batch ? all_rows / kFew : batch;
+  const long long packed = all_rows / prompt_rows + long_seqs / 2;
+  const long long tiles = prompt_tiles * batch < packed ? prompt_tiles * batch : packed;
+  bool prompt = rows >= kFew && tiles * h_kv >= info->cus, split = true;
+  const bool alike = (long long)p.most * batch == total;  // every sequence has max_q rows, if cu is what it should be
+  if (prompt && alike) split = false;
+  if (const char* e = getenv("DG_FORCE_CONFIG")) {
+    if (strcmp(e, kKv8Prompt) == 0) prompt = true, split = false;
+    if (strcmp(e, kKv8Split) == 0) prompt = false, split = true;
+  }
+  if (prompt_tiles > 65535) prompt = false, split = true;
+  const int border = prompt && split ? kFew : 0;
+  char* base = nullptr;
+  p.workers = kv8_workers(info);
+  if (split)
+    if (int s = ensure_workspace(dev, (hipStream_t)stream, kv8_part_floats(p.workers, d) * sizeof(float), &base)) return s;
+  if (prompt) {
+    p.rows_lo = border;
+    p.rows_hi = INT_MAX;
     const void* fn = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<64, 2>)
                      : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<128, 2>)
                                 : reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<256, 1>);
-    return launch_plain("kv8_prompt", fn, dim3(h_kv, batch, (unsigned)prompt_tiles), 256, args, stream);
+    const int s = launch_plain("kv8_prompt", fn, dim3(h_kv, batch, (unsigned)prompt_tiles), 256, args, stream);
+    if (s || !split) return s;
   }
-  p.workers = kv8_workers(info);
-  char* base = nullptr;
-  if (int s = ensure_workspace(dev, (hipStream_t)stream, kv8_part_floats(p.workers, d) * sizeof(float), &base)) return s;
+  p.rows_lo = 0;
+  p.rows_hi = border ? border : INT_MAX;
   p.arrived = (int*)base;
   p.part_u = (float*)(base + kWsHeader);
   p.part_ml = p.part_u + (size_t)p.workers * 2 * 16 * d;

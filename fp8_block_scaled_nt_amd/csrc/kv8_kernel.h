@@ -300,6 +300,7 @@ struct Kv8AttnParams {
   float* lse;              // [total][h_q] or null
   float scale_log2;        // scale * log2(e)
   int causal, window, batch, total, most, h_q, group;
+  int rows_lo, rows_hi;    // only sequences of rows_lo .. rows_hi - 1 rows (queries x group) are this launch's
   // split work: workgroup w computes its share of the units below
   float* part_u;   // [workers][2][16][d]
   float* part_ml;  // [workers][2][16][2]
@@ -328,6 +329,7 @@ struct Kv8Seq {
 __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8AttnParams& p, int seq) {
   Kv8Seq s;
   const int all = kv8_rows(p.cu, seq, p.total, p.most, &s.first, &s.count);
+  if (s.count * p.group < p.rows_lo || s.count * p.group >= p.rows_hi) s.count = 0;
   const long long room = (long long)p.c.max_blocks << p.c.block_log2;
   const int kv = max(p.kv_lens[seq], 0);
   s.kv = kv < room ? kv : (int)room;
