@@ -245,8 +245,8 @@ constexpr const char* kKv8Prompt = "kv8_prompt";
 
 // DG_FORCE_CONFIG=<name> pins the configuration of the variant it names (for
 // tuning sweeps); an unknown name is an error rather than silently ignored.
-int forced_config(int variant, const Config** out, int dtype = dg::kFp8, int epi = dg::kEpiBf16) {
-  *out = nullptr;
+int forced_name(const char** name) {
+  *name = nullptr;
   const char* e = getenv("DG_FORCE_CONFIG");
   if (!e || !*e) return DG_OK;
   int cnt = 0;
@@ -256,7 +256,25 @@ int forced_config(int variant, const Config** out, int dtype = dg::kFp8, int epi
   known = known || find_skinny(e) != nullptr || strcmp(e, kKv8Split) == 0 || strcmp(e, kKv8Prompt) == 0 ||
           strcmp(e, kW4RowsName) == 0 || strcmp(e, kW4TileName) == 0;
   if (!known) return fail(DG_ERR_INVALID_ARGUMENT, "DG_FORCE_CONFIG names no configuration: %s", e);
-  *out = find_config(e, variant, dtype, epi);
+  *name = e;
+  return DG_OK;
+}
+
+int forced_config(int variant, const Config** out, int dtype = dg::kFp8, int epi = dg::kEpiBf16) {
+  *out = nullptr;
+  const char* name;
+  if (int s = forced_name(&name)) return s;
+  if (name) *out = find_config(name, variant, dtype, epi);
+  return DG_OK;
+}
+
+// The same for calls that choose between two ways: the one pinned, or null.
+int forced_way(const char* one, const char* other, const char** way) {
+  const char* name;
+  *way = nullptr;
+  if (int s = forced_name(&name)) return s;
+  if (name && strcmp(name, one) == 0) *way = one;
+  if (name && strcmp(name, other) == 0) *way = other;
   return DG_OK;
 }
 
@@ -876,6 +894,7 @@ int check_w4(int n, int k, int group, int format, const void* zeros) {
 // whose waves split K, or tiles of 128 weight rows by 32 or 64 rows of a and K
 // in splits.
 struct W4Plan {
+  const char* name;
   const void* fn;
   dim3 grid;
   int threads, smem;
@@ -884,7 +903,7 @@ struct W4Plan {
 };
 
 template <int FMT, int GROUP, bool WHOLE>
-W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
+W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info, const char* way) {
   const int units = (k + 127) / 128;
   // 16 x 16 tiles up to 16 rows, and beyond while each CU has no more than about
   // 100 units of them (us, 16 x 16 / larger tiles, units per CU: 64 x 512 x 1024
@@ -894,7 +913,7 @@ W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
   // with 224).
   const long long small_tiles = (long long)((n + 15) / 16) * ((m + 15) / 16);
   bool small = m <= 16 || small_tiles * units <= 100LL * info->cus;
-  if (const char* e = getenv("DG_FORCE_CONFIG")) small = strcmp(e, kW4RowsName) == 0 || (small && strcmp(e, kW4TileName) != 0);
+  if (way) small = way == kW4RowsName;
   if (small) {
     // 8 waves for up to one and a half workgroups per CU, then 4, which leave
     // more of them side by side (us, 4 / 8 / 16 waves: 1 x 2112 x 7168 5.2 / 4.7
@@ -909,12 +928,12 @@ W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
     // 7168 6.0 / 6.4 / 7.3; 4 x 4096 x 7168 7.6 / 7.7 / 8.5; 5 x 2112 x 7168 - /
     // 5.2 / 6.3)
     if (m <= 4)
-      return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 2, 4, WHOLE>), grid, waves * 64,
+      return {kW4RowsName, reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 2, 4, WHOLE>), grid, waves * 64,
               dg::w4_rows_smem<FMT, GROUP, 2, 4, WHOLE>(waves), 0, 0};
     if (m <= 8)
-      return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 8, WHOLE>), grid, waves * 64,
+      return {kW4RowsName, reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 8, WHOLE>), grid, waves * 64,
               dg::w4_rows_smem<FMT, GROUP, 1, 8, WHOLE>(waves), 0, 0};
-    return {reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 16, WHOLE>), grid, waves * 64,
+    return {kW4RowsName, reinterpret_cast<const void*>(&dg::w4_rows_kernel<FMT, GROUP, 1, 16, WHOLE>), grid, waves * 64,
             dg::w4_rows_smem<FMT, GROUP, 1, 16, WHOLE>(waves), 0, 0};
   }
   // (at m = 17 and 32 tiles of 64 rows take 16.7 us for 4096 x 7168 against 12.9
@@ -943,27 +962,30 @@ W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
   long long splits = tiles > info->cus || 6 * of_one > 10 * of_two + 25 ? two : one;
   if (const char* e = getenv("DG_SPLIT_K")) splits = atoi(e) < units ? atoi(e) : units;
   if (splits < 1 || tiles > (long long)kCounterInts) splits = 1;
-  return {rows == 32 ? reinterpret_cast<const void*>(&dg::w4_tile_kernel<FMT, GROUP, 2, WHOLE>)
+  return {kW4TileName,
+          rows == 32 ? reinterpret_cast<const void*>(&dg::w4_tile_kernel<FMT, GROUP, 2, WHOLE>)
                      : reinterpret_cast<const void*>(&dg::w4_tile_kernel<FMT, GROUP, 4, WHOLE>),
           dim3(tiles_n, (unsigned)splits, tiles_m), 256, 0,
           splits > 1 ? (size_t)tiles * splits * rows * 128 * sizeof(float) : 0, (int)tiles};
 }
 
 template <int FMT, int GROUP>
-W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info) {
-  if constexpr (GROUP == 128) return w4_plan<FMT, GROUP, true>(m, n, k, info);
-  return k % 128 == 0 ? w4_plan<FMT, GROUP, true>(m, n, k, info) : w4_plan<FMT, GROUP, false>(m, n, k, info);
+W4Plan w4_plan(int m, int n, int k, const DeviceInfo* info, const char* way) {
+  if constexpr (GROUP == 128) return w4_plan<FMT, GROUP, true>(m, n, k, info, way);
+  return k % 128 == 0 ? w4_plan<FMT, GROUP, true>(m, n, k, info, way) : w4_plan<FMT, GROUP, false>(m, n, k, info, way);
 }
 
 template <int FMT>
-W4Plan w4_plan(int m, int n, int k, int group, const DeviceInfo* info) {
-  return group == 32   ? w4_plan<FMT, 32>(m, n, k, info)
-         : group == 64 ? w4_plan<FMT, 64>(m, n, k, info)
-                       : w4_plan<FMT, 128>(m, n, k, info);
+W4Plan w4_plan(int m, int n, int k, int group, const DeviceInfo* info, const char* way) {
+  return group == 32   ? w4_plan<FMT, 32>(m, n, k, info, way)
+         : group == 64 ? w4_plan<FMT, 64>(m, n, k, info, way)
+                       : w4_plan<FMT, 128>(m, n, k, info, way);
 }
 
-W4Plan w4_plan(int m, int n, int k, int group, int format, const DeviceInfo* info) {
-  return format == DG_W4_E2M1 ? w4_plan<dg::kW4E2m1>(m, n, k, group, info) : w4_plan<dg::kW4U4>(m, n, k, group, info);
+// `way`: kW4RowsName, kW4TileName, or null for the rule's choice
+W4Plan w4_plan(int m, int n, int k, int group, int format, const DeviceInfo* info, const char* way) {
+  return format == DG_W4_E2M1 ? w4_plan<dg::kW4E2m1>(m, n, k, group, info, way)
+                              : w4_plan<dg::kW4U4>(m, n, k, group, info, way);
 }
 
 template <int FMT, bool BF16>
@@ -1437,10 +1459,12 @@ int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* 
   if (!aligned16(a) || !aligned16(codes) || !aligned16(scales) || !aligned16(d) || !aligned16(zeros))
     return fail(DG_ERR_MISALIGNED, "pointers must be 16-byte aligned");
   if (m == 0) return ok();
+  const char* way;
+  if (int s = forced_way(kW4RowsName, kW4TileName, &way)) return s;
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
-  const W4Plan w = w4_plan(m, n, k, group, format, info);
+  const W4Plan w = w4_plan(m, n, k, group, format, info, way);
   if (w.grid.y > 65535 || w.grid.z > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m too large (%d)", m);
   const int units = (k + 127) / 128;
   dg::W4Params p{a, codes, scales, zeros, d, m, n, k, nullptr, nullptr, units / (int)w.grid.y, units % (int)w.grid.y};
@@ -1451,7 +1475,7 @@ int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* 
     p.partial = (float*)(base + kWsHeader);
   }
   void* args[] = {&p};
-  return launch_plain("w4_gemm", w.fn, w.grid, w.threads, args, stream, w.smem);
+  return launch_plain(w.name, w.fn, w.grid, w.threads, args, stream, w.smem);
 }
 
 int dg_bf16_w4_workspace_size(int m, int n, int k, int group, int format, size_t* bytes) {
@@ -1461,10 +1485,12 @@ int dg_bf16_w4_workspace_size(int m, int n, int k, int group, int format, size_t
   const uint8_t any = 0;
   if (int s = check_w4(n, k, group, format, format == DG_W4_U4 ? &any : nullptr)) return s;
   if (m == 0) return ok();
+  const char* way;
+  if (int s = forced_way(kW4RowsName, kW4TileName, &way)) return s;
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
-  *bytes = w4_plan(m, n, k, group, format, info).partial_bytes;
+  *bytes = w4_plan(m, n, k, group, format, info, way).partial_bytes;
   return ok();
 }
 
@@ -1587,6 +1613,8 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   p.most = max_q < total ? max_q : total;
   if ((long long)p.most * h_q * d > 0x7FFFFFFFLL)  // of one sequence; 32-bit counts of its elements
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many queries per sequence (%d of %d heads)", p.most, h_q);
+  const char* way;
+  if (int s = forced_way(kKv8Split, kKv8Prompt, &way)) return s;
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
@@ -1627,10 +1655,7 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   bool prompt = rows >= kFew && tiles * h_kv >= info->cus, split = true;
   const bool alike = (long long)p.most * batch == total;  // every sequence has max_q rows, if cu is what it should be
   if (prompt && alike) split = false;
-  if (const char* e = getenv("DG_FORCE_CONFIG")) {
-    if (strcmp(e, kKv8Prompt) == 0) prompt = true, split = false;
-    if (strcmp(e, kKv8Split) == 0) prompt = false, split = true;
-  }
+  if (way) prompt = way == kKv8Prompt, split = !prompt;
   if (prompt_tiles > 65535) prompt = false, split = true;
   const int border = prompt && split ? kFew : 0;
   char* base = nullptr;
@@ -1643,7 +1668,7 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
     const void* fn = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<64, 2>)
                      : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<128, 2>)
                                 : reinterpret_cast<const void*>(&dg::kv8_prompt_kernel<256, 1>);
-    const int s = launch_plain("kv8_prompt", fn, dim3(h_kv, batch, (unsigned)prompt_tiles), 256, args, stream);
+    const int s = launch_plain(kKv8Prompt, fn, dim3(h_kv, batch, (unsigned)prompt_tiles), 256, args, stream);
     if (s || !split) return s;
   }
   p.rows_lo = 0;
@@ -1654,7 +1679,7 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   const void* fn = d == 64    ? reinterpret_cast<const void*>(&dg::kv8_attn_kernel<64>)
                    : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_attn_kernel<128>)
                               : reinterpret_cast<const void*>(&dg::kv8_attn_kernel<256>);
-  return launch_plain("kv8_attn", fn, dim3(p.workers), 256, args, stream);
+  return launch_plain(kKv8Split, fn, dim3(p.workers), 256, args, stream);
 }
 
 }  // extern "C"
