@@ -460,6 +460,14 @@ int get_workspace(const WsSource& src, int dev, hipStream_t stream, size_t parti
   return DG_OK;
 }
 
+// A GEMM's launch: records the events of dg_profile_next_launch if there are any.
+hipError_t launch_gemm_kernel(const void* fn, dim3 grid, int threads, void** args, int smem, hipStream_t stream) {
+  if (!g_prof_start && !g_prof_stop) return hipLaunchKernel(fn, grid, dim3(threads), args, smem, stream);
+  const hipError_t e = hipExtLaunchKernel(fn, grid, dim3(threads), args, smem, stream, g_prof_start, g_prof_stop, 0);
+  g_prof_start = g_prof_stop = nullptr;
+  return e;
+}
+
 int launch(const Config& c, dg::GemmParams& p, int grid, hipStream_t stream) {
   if (int s = ensure_kernel_attributes()) return s;
   if (log_enabled())
@@ -467,14 +475,7 @@ int launch(const Config& c, dg::GemmParams& p, int grid, hipStream_t stream) {
             p.m, p.n, p.k, p.num_groups, grid, c.threads(), c.smem, per_cu(&c), p.splits);
   if (grid <= 0) return ok();
   void* args[] = {&p};
-  hipError_t e;
-  if (g_prof_start || g_prof_stop) {
-    e = hipExtLaunchKernel(c.fn, dim3(grid), dim3(c.threads()), args, c.smem, stream, g_prof_start,
-                           g_prof_stop, 0);
-    g_prof_start = g_prof_stop = nullptr;
-  } else {
-    e = hipLaunchKernel(c.fn, dim3(grid), dim3(c.threads()), args, c.smem, stream);
-  }
+  const hipError_t e = launch_gemm_kernel(c.fn, dim3(grid), c.threads(), args, c.smem, stream);
   if (e != hipSuccess) return fail(DG_ERR_HIP, "launch of %s failed: %s", c.name, hipGetErrorString(e));
   return ok();
 }
@@ -794,14 +795,7 @@ int launch_skinny(const SkinnyPlan& pl, const uint8_t* a, const float* sfa, cons
     fprintf(stderr, "[dg] %s m=%d n=%d k=%d grid=%d threads=%d smem=%d per=%d rem=%d contrib=%d ws=%zu\n", c.name, m,
             n, k, pl.grid, c.threads(), c.smem(), pl.per, pl.rem, pl.max_contrib, pl.ws_bytes);
   void* args[] = {&p};
-  hipError_t e;
-  if (g_prof_start || g_prof_stop) {
-    e = hipExtLaunchKernel(c.fn, dim3(pl.grid), dim3(c.threads()), args, c.smem(), (hipStream_t)stream,
-                           g_prof_start, g_prof_stop, 0);
-    g_prof_start = g_prof_stop = nullptr;
-  } else {
-    e = hipLaunchKernel(c.fn, dim3(pl.grid), dim3(c.threads()), args, c.smem(), (hipStream_t)stream);
-  }
+  const hipError_t e = launch_gemm_kernel(c.fn, dim3(pl.grid), c.threads(), args, c.smem(), (hipStream_t)stream);
   if (e != hipSuccess) return fail(DG_ERR_HIP, "launch of %s failed: %s", c.name, hipGetErrorString(e));
   return ok();
 }
@@ -1002,10 +996,12 @@ const void* w4_dequant_fn(int group) {
                        : reinterpret_cast<const void*>(&dg::w4_dequant_kernel<FMT, 128>);
 }
 
-int launch_plain(const char* what, const void* fn, dim3 grid, int threads, void** args, dg_stream_t stream, int smem = 0) {
+int launch_plain(const char* what, const void* fn, dim3 grid, int threads, void** args, dg_stream_t stream, int smem = 0,
+                 bool gemm = false) {
   if (log_enabled())
     fprintf(stderr, "[dg] %s grid=%ux%ux%u threads=%d\n", what, grid.x, grid.y, grid.z, threads);
-  hipError_t e = hipLaunchKernel(fn, grid, dim3(threads), args, smem, (hipStream_t)stream);
+  const hipError_t e = gemm ? launch_gemm_kernel(fn, grid, threads, args, smem, (hipStream_t)stream)
+                            : hipLaunchKernel(fn, grid, dim3(threads), args, smem, (hipStream_t)stream);
   if (e != hipSuccess) return fail(DG_ERR_HIP, "launch of %s failed: %s", what, hipGetErrorString(e));
   return ok();
 }
@@ -1475,7 +1471,7 @@ int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* 
     p.partial = (float*)(base + kWsHeader);
   }
   void* args[] = {&p};
-  return launch_plain(w.name, w.fn, w.grid, w.threads, args, stream, w.smem);
+  return launch_plain(w.name, w.fn, w.grid, w.threads, args, stream, w.smem, true);
 }
 
 int dg_bf16_w4_workspace_size(int m, int n, int k, int group, int format, size_t* bytes) {
