@@ -1008,9 +1008,10 @@ int launch_plain(const char* what, const void* fn, dim3 grid, int threads, void*
 
 // ---- 8-bit key/value cache (kv8_kernel.h)
 
-int check_cache(const void* k_codes, const void* v_codes, const void* k_scales, const void* v_scales,
-                const void* table, int h_kv, int d, int block, int num_blocks, int max_blocks, dg::Kv8Cache* c) {
-  if (!k_codes || !v_codes || !k_scales || !v_scales || !table)
+// Arrays without elements may be null: no pool, no table, no sequences.
+int check_cache(const void* k_codes, const void* v_codes, const void* k_scales, const void* v_scales, const void* table,
+                int batch, int h_kv, int d, int block, int num_blocks, int max_blocks, dg::Kv8Cache* c) {
+  if ((num_blocks != 0 && (!k_codes || !v_codes || !k_scales || !v_scales)) || (batch != 0 && max_blocks != 0 && !table))
     return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (h_kv < 1 || h_kv > 32767) return fail(DG_ERR_INVALID_ARGUMENT, "h_kv must be 1..32767 (got %d)", h_kv);
   if (num_blocks < 0 || max_blocks < 0) return fail(DG_ERR_INVALID_ARGUMENT, "block counts must be >= 0");
@@ -1530,10 +1531,11 @@ int dg_kv8_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_
                   uint8_t* v_codes, float* k_scales, float* v_scales, const int32_t* block_table,
                   const int32_t* ctx_lens, const int32_t* cu_new, int batch, int total, int max_new, int h_kv, int d,
                   int block, int num_blocks, int max_blocks, dg_stream_t stream) {
-  if (!ctx_lens || !cu_new || (total > 0 && (!k || !v))) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if ((batch != 0 && !ctx_lens) || !cu_new || (total > 0 && (!k || !v)))
+    return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
   dg::Kv8AppendParams p{};
-  if (int s = check_cache(k_codes, v_codes, k_scales, v_scales, block_table, h_kv, d, block, num_blocks, max_blocks,
-                          &p.c)) return s;
+  if (int s = check_cache(k_codes, v_codes, k_scales, v_scales, block_table, batch, h_kv, d, block, num_blocks,
+                          max_blocks, &p.c)) return s;
   if (int s = check_batch(batch, total, max_new)) return s;
   if (int s = check_packed(k, k_stride, h_kv, d, "k")) return s;
   if (int s = check_packed(v, v_stride, h_kv, d, "v")) return s;
@@ -1590,10 +1592,11 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
                      const int32_t* kv_lens, const int32_t* cu_q, uint16_t* out, float* lse, float scale, int causal,
                      int window, int batch, int total, int max_q, int h_q, int h_kv, int d, int block, int num_blocks,
                      int max_blocks, dg_stream_t stream) {
-  if (!kv_lens || !cu_q || (total > 0 && (!q || !out))) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if ((batch != 0 && !kv_lens) || !cu_q || (total > 0 && (!q || !out)))
+    return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
   dg::Kv8AttnParams p{};
-  if (int s = check_cache(k_codes, v_codes, k_scales, v_scales, block_table, h_kv, d, block, num_blocks, max_blocks,
-                          &p.c)) return s;
+  if (int s = check_cache(k_codes, v_codes, k_scales, v_scales, block_table, batch, h_kv, d, block, num_blocks,
+                          max_blocks, &p.c)) return s;
   if (int s = check_batch(batch, total, max_q)) return s;
   if (h_q < 1 || h_q % h_kv != 0)
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "h_q must be a positive multiple of h_kv = %d (got %d)", h_kv, h_q);

@@ -377,7 +377,8 @@ int dg_dequantize_b_w4(const uint8_t* codes, const uint16_t* scales, const uint8
  * names the block that holds tokens j * block .. j * block + block - 1 of each
  * sequence.  Entries that no token in question falls into are not read; tokens
  * whose entry lies outside [0, num_blocks), or past max_blocks, are neither
- * written nor seen.  Code arrays may pass 4 GiB.
+ * written nor seen.  Code arrays may pass 4 GiB.  An array without elements (no
+ * blocks, no sequences, a table of no width) may be NULL.
  *
  * Packed tokens: q, k, v hold the rows of all sequences one after the other,
  * [total][heads][d] bf16 with *_stride elements (a multiple of 8) from token to
