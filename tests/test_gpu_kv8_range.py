@@ -85,3 +85,17 @@ def test_a_token_of_most_weight_and_no_values(way, gpu, new, kv, log2w):  # noqa
     q[..., 7] = np.log(2)
     q = bf16(q)
     hold_each(attend(gpu, q, cache, table, [kv], [0, new], scale=1.0), q, cache, table, [kv], [0, new], 1.0)
+
+
+@pytest.mark.parametrize("new,kv", [(1, 700), (12, 300), (150, 400)])
+def test_blocks_of_zeros_beside_large_and_small_values(way, gpu, new, kv):  # noqa: F811
+    # scales as the append gives them: 2^-22 for blocks of zeros, and values of 2^-12, 1 and 2^10 in blocks of their own
+    h, d, block = 1, 64, 64
+    rng = np.random.default_rng(kv)
+    k, v = bf16(rng.standard_normal((kv, h, d))), rng.standard_normal((kv, h, d))
+    v *= np.array([1.0, 0.0, 2.0 ** 10, 2.0 ** -12])[np.arange(kv) // block % 4][:, None, None]
+    v[np.arange(kv) // block % 4 == 2, :, 1:] = 0
+    table, blocks = pages(rng, [kv], block)
+    cache = kv8.append_ref(k, bf16(v), blank(blocks, h, block, d), table, [0], [0, kv])
+    q = bf16(rng.standard_normal((new, 4, d)))
+    hold_each(attend(gpu, q, cache, table, [kv], [0, new]), q, cache, table, [kv], [0, new], 0.125)
