@@ -9,21 +9,26 @@
 // K (element 2i in the low nibble), scales are bf16, groups are 32, 64 or 128
 // wide.
 //
-// The weights are read once, half a byte each, and serve at most 64 rows of a:
-// the product is bound by HBM on all but the smallest sizes, so the kernel is
-// laid out around its loads.  A wave owns 16 NT weight rows and a run of K in
-// units of 128; lane l loads 16 bytes (32 codes) of row l % 16 at K offset
-// 32 (l / 16), so one instruction takes 64 contiguous bytes of 16 rows, and
-// the same registers are the B operand of v_mfma_f32_16x16x32_bf16 once their
-// nibbles are widened.  The waves of a workgroup split K and add their fp32
-// sums in LDS in wave order: one launch, no scratch memory, and the same bits
-// on every call.
+// Weights are half a byte each and serve few rows of a, so the kernels are laid
+// out around their loads.  K is walked in units of 128.  A wave takes 16 weight
+// rows of a unit with one load of 16 bytes (32 codes) a lane, four lanes to a
+// row; the codes change lanes in LDS, and are the B operand of
+// v_mfma_f32_16x16x32_bf16 once their nibbles are widened.  Two kernels, both one
+// launch with the same bits on every call:
+//
+//   w4_rows_kernel: 16 weight rows by up to 16 rows of a.  The waves of a
+//     workgroup split K and add their fp32 sums in LDS in wave order, without
+//     scratch memory.  More rows of a read the weights again for every 16.
+//   w4_tile_kernel: 128 weight rows by 32 or 64 rows of a, K in splits that are
+//     added in split order by way of the stream's workspace.
 //
 // Widening is exact.  e2m1 codes go through the hardware conversion to bf16;
 // integer codes become bf16 128 + c by setting bits under the exponent of 128
 // (bf16 has 7 fraction bits), and the 128 is taken out again with the zero
 // point: sum (128 + c) a - (128 + z) sum a, both sums in fp32 from the matrix
-// cores.  The scale multiplies the fp32 sum of its group, so no weight is
+// cores.  They hold terms of up to 143 |a|, where (c - z) a has up to 15 |a|: an
+// fp32 rounding is then up to 2^-17 of the group's sum |a| (times the scale), and
+// the output is bf16.  The scale multiplies the fp32 sum of its group, so no weight is
 // rounded to bf16 after scaling.
 #pragma once
 

@@ -335,11 +335,19 @@ typedef enum { DG_W4_E2M1 = 0, DG_W4_U4 = 1 } dg_w4_format;
  * tokens meet weights that are read once.  Products and sums are fp32 (the
  * scale meets the fp32 sum of its group, so no weight is rounded after
  * scaling), in one launch, with the same bits on every call.  Any m >= 0 (0: a
- * no-op) is computed; up to 64 rows share one read of the weights, more rows
- * read them again for every 64, so a long prompt is better served by
- * dg_dequantize_b_w4 and dg_bf16_gemm_nt.  With m > 16, K may be split over
- * workgroups: the call then needs dg_bf16_w4_workspace_size bytes of the
- * stream's workspace (see the workspace rule above).
+ * no-op) is computed.  The weights are read once for m <= 16; more rows read them
+ * again for every 16 while the product is small, else for every 32 (m <= 32) or
+ * 64, so a long prompt is better served by dg_dequantize_b_w4 and
+ * dg_bf16_gemm_nt.  With m > 16, K may be split over workgroups: the call then
+ * needs dg_bf16_w4_workspace_size bytes of the stream's workspace (see the
+ * workspace rule above).
+ *
+ * DG_W4_U4 codes enter the products as 128 + c, and (128 + z) sum a is taken off
+ * in fp32: an output carries fp32 roundings of terms up to 143 s |a|, for weights
+ * of up to 15 s.  So rows of a whose sum of 143 |a| over a group passes fp32's
+ * range give outputs that are not finite, and rows with an infinity NaN, whatever
+ * the weights' signs.  DG_W4_E2M1 has no such limit.  NaN and infinities stay in
+ * their row.
  */
 int dg_bf16_w4_gemm_nt(const uint16_t* a, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
                        uint16_t* d, int m, int n, int k, int group, int format, dg_stream_t stream);
@@ -350,7 +358,7 @@ int dg_bf16_w4_workspace_size(int m, int n, int k, int group, int format, size_t
 
 /*
  * Quantise a weight matrix x[n][k] (bf16 bits if x_bf16, else fp32) into that
- * form; x must be finite.  Per row and group:
+ * form; x must be finite, and for DG_W4_U4 hi - lo too.  Per row and group:
  *   DG_W4_E2M1: s = bf16(max(amax, 1e-4) / 6), code = e2m1(x / s), nearest, ties to even
  *   DG_W4_U4:   lo = min(x, 0), hi = max(x, 0), s = bf16(max(hi - lo, 1e-4) / 15),
  *               z = min(rint(-lo / s), 15), code = clamp(rint(x / s) + z, 0, 15)
