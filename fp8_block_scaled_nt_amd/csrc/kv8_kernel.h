@@ -281,9 +281,9 @@ __global__ __launch_bounds__(THREADS) void kv8_append_kernel(Kv8AppendParams p) 
 //     outputs of prompts of up to 150 tokens off by more than 70% of 8e-3 |r| +
 //     1e-3 rms, the worst by 129%).
 //
-// (With fp16 alone prompts of 2048 took 296 us against 297, 4 x 2048 within a
-// window of 512 144 against 151, 32 x 4096 single tokens 45.4 against 46.6; where
-// value scales were 2^16 apart elements were then off by up to all of themselves.)
+// (With fp16 alone prompts of 2048 took 296 us against 300 and 4 x 256 of 256
+// 20.2 against 21.2; where value scales were 2^16 apart elements were then off by
+// up to all of themselves.)
 // The keys of a 64-key step are dealt to the rows of the A operand so that
 // lane group g (lanes 16 g ..) ends up with p for keys 16 g .. 16 g + 15,
 // which is how a lane of the second product's B operand wants them against
@@ -514,17 +514,22 @@ __device__ __forceinline__ Kv8Scale kv8_scale_of(const Kv8Run& run, float scale_
   return Kv8Scale{run.ks * scale_log2, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs), there};
 }
 
-// Whether a step needs the wide form for its value scales, whose log2 are lv
-// (-inf: the block is not there); `top` is the largest so far and takes this
-// step's in.
-__device__ __forceinline__ bool kv8_far(float lv, float& top) {
-  if (__any(lv > top)) top = fmaxf(top, kv8_group_max(lv));
-  return __any(lv > -__builtin_huge_valf() && lv < top - kKv8Near);
+// Whether a step needs the wide form for its blocks: one is not there, or value
+// scales are far apart; `top` is the log2 of the largest so far and takes this
+// step's in.  Most steps leave by one test.
+__device__ __forceinline__ bool kv8_far(const Kv8Scale& sc, float& top) {
+  if (!__any(!sc.there || sc.lv > top || sc.lv < top - kKv8Near)) return false;
+  top = fmaxf(top, kv8_group_max(sc.there ? sc.lv : -__builtin_huge_valf()));
+  return __any(!sc.there || sc.lv < top - kKv8Near);
 }
 
 // What remains of a step when its raw products s[4 j + e] with keys run_v + 4 j
 // + e are there: t = s ks + lv, the reference, p, and the second product,
-// narrow or (WIDE) wide and with masks.
+// narrow or (WIDE) wide and with masks.  load_v(i, o) gives the lane's values of
+// dimension 16 i + a at keys 16 g + 8 o .. (a = lane % 16, g = lane / 16) in fp16.
+// WIDE: some row may not see some of the keys, or the sequence end inside the
+// step (such steps are the first and last ones of a run), or the value scales are
+// far apart.
 template <int D, int MT, bool WIDE, class LoadV>
 __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Scale& sc, const Kv8Rows<MT>& rows,
                                                  float (&s)[MT][16], Kv8State<D, MT>& st, LoadV load_v) {
@@ -656,17 +661,11 @@ __device__ __forceinline__ void kv8_rest_of_step(int kv, int run_v, const Kv8Sca
   }
 }
 
-// One step: 64 keys from token `base` on, against 16 MT rows.  load_k(j, h, o)
-// gives the lane's values h * 64 + 16 g + 8 o .. of key (a / 4) * 16 + 4 j +
-// a % 4, load_v(i, o) those of dimension 16 i + a at keys 16 g + 8 o .. (a =
-// lane % 16, g = lane / 16) in fp16, load_q(t, i) B fragment i of the lane's row of
-// tile t.  WIDE: some row may not see some of the keys, or the sequence end
-// inside the step (such steps are the first and last ones of a run), or the
-// value scales are far apart.
-template <int D, int MT, bool WIDE, class LoadQ, class LoadK, class LoadV>
-__device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, const Kv8Rows<MT>& rows,
-                                         Kv8State<D, MT>& st, LoadQ load_q, LoadK load_k, LoadV load_v) {
-  float s[MT][16];
+// The raw products of a step of 64 keys with 16 MT rows.  load_k(j, h, o) gives
+// the lane's values h * 64 + 16 g + 8 o .. of key (a / 4) * 16 + 4 j + a % 4,
+// load_q(t, i) B fragment i of the lane's row of tile t.
+template <int D, int MT, class LoadQ, class LoadK>
+__device__ __forceinline__ void kv8_scores(float (&s)[MT][16], LoadQ load_q, LoadK load_k) {
   v8bf qf[MT][D / 32];
 #pragma unroll
   for (int t = 0; t < MT; ++t)
@@ -698,8 +697,6 @@ __device__ __forceinline__ void kv8_step(int kv, int base, const Kv8Scale& sc, c
       for (int e = 0; e < 4; ++e) s[t][4 * j + e] = acc[t][e];
   }
   __builtin_amdgcn_sched_barrier(0);
-  const int run_v = base + ((threadIdx.x & 63) >> 4) * 16;
-  kv8_rest_of_step<D, MT, WIDE>(kv, run_v, sc, rows, s, st, load_v);
 }
 
 // The B fragments of one row of q.
@@ -717,8 +714,8 @@ __device__ __forceinline__ void kv8_load_q(const Kv8AttnParams& p, const Kv8Seq&
 
 // Whether a step from token `base` on needs masks, given the keys [all_lo,
 // all_hi) that every row sees (all_hi is at most kv).
-__device__ __forceinline__ bool kv8_masked(int base, int all_lo, int all_hi, bool there) {
-  return base < all_lo || base + kKv8Step > all_hi || __any(!there);
+__device__ __forceinline__ bool kv8_masked(int base, int all_lo, int all_hi) {
+  return base < all_lo || base + kKv8Step > all_hi;
 }
 
 // A wave's loads of one step straight from the cache into registers.
@@ -863,25 +860,28 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8AttnParams p) {
       for (int t = first; t < last; t += 4) {
         const bool more = t + 4 < last;
         const Kv8Scale now = kv8_scale_of(run, p.scale_log2);
-        const bool far = kv8_far(now.there ? now.lv : -__builtin_huge_valf(), top);
-        const bool wide = kv8_masked(base, all_lo, all_hi, pv >= 0) || far;
         const int here = base;
         base += 4 * kKv8Step;
         pk = next_pk;
         pv = next_pv;
         kv8_pages(p.c, seq, sq.kv, base + 4 * kKv8Step, &next_pk, &next_pv);
-        auto step = [&](auto form) {
-          kv8_step<D, 1, decltype(form)::value>(sq.kv, here, now, see, st, [&](int t, int i) { return qf[t][i]; },
-                       [&](int j, int h, int o) { return e4m3_to_bf16(regs.k[j][h][2 * o], regs.k[j][h][2 * o + 1]); },
-                       [&](int i, int o) {
-                         if (i == 0 && o == 0 && more) {
-                           regs.load_k(p.c, head, base, pk);
-                           run = kv8_run(p.c, head, pv);
-                         }
-                         return __builtin_bit_cast(v4u, e4m3_to_f16(regs.v[i][2 * o], regs.v[i][2 * o + 1]));
-                       });
+        float scores[1][16];
+        kv8_scores<D, 1>(scores, [&](int t, int i) { return qf[t][i]; }, [&](int j, int h, int o) {
+          return e4m3_to_bf16(regs.k[j][h][2 * o], regs.k[j][h][2 * o + 1]);
+        });
+        auto rest = [&](auto form) {
+          kv8_rest_of_step<D, 1, decltype(form)::value>(sq.kv, here + g * 16, now, see, scores, st, [&](int i, int o) {
+            if (i == 0 && o == 0 && more) {
+              regs.load_k(p.c, head, base, pk);
+              run = kv8_run(p.c, head, pv);
+            }
+            return __builtin_bit_cast(v4u, e4m3_to_f16(regs.v[i][2 * o], regs.v[i][2 * o + 1]));
+          });
         };
-        if (wide) step(std::true_type{}); else step(std::false_type{});
+        // decided after the scores, when the scales are there (before them 32 x
+        // 4096 took 46.6 us against 44.4, with heads of 64 30.6 against 27.3)
+        const bool far = kv8_far(now, top);
+        if (far || kv8_masked(here, all_lo, all_hi)) rest(std::true_type{}); else rest(std::false_type{});
         if (more) regs.load_v(p.c, head, base, pv);
       }
     }
@@ -1113,13 +1113,13 @@ __global__ __launch_bounds__(256, 2) void kv8_prompt_kernel(Kv8AttnParams p) {
           const v4u* k_at = s_k[buf];
           const v4u* v_at = s_v[buf];
           const Kv8Scale now = s_scale[buf][g];
-          kv8_step<D, MT, decltype(form)::value>(
-              sq.kv, base, now, see, st,
-              [&](int t, int i) { return qf[t][i]; },
-              [&](int j, int h, int o) {
-                return __builtin_bit_cast(v8bf, k_at[kv8_slot<kParts>(j * 16 + a, h * 8 + g * 2 + o)]);
-              },
-              [&](int i, int o) { return v_at[kv8_slot<8>(i * 16 + a, g * 2 + o)]; });
+          float scores[MT][16];
+          kv8_scores<D, MT>(scores, [&](int t, int i) { return qf[t][i]; }, [&](int j, int h, int o) {
+            return __builtin_bit_cast(v8bf, k_at[kv8_slot<kParts>(j * 16 + a, h * 8 + g * 2 + o)]);
+          });
+          kv8_rest_of_step<D, MT, decltype(form)::value>(sq.kv, base + g * 16, now, see, scores, st, [&](int i, int o) {
+            return v_at[kv8_slot<8>(i * 16 + a, g * 2 + o)];
+          });
         }
         put(buf ^ 1);
         __syncthreads();
