@@ -1056,8 +1056,9 @@ int check_batch(int batch, int total, int most) {
 
 // Workgroups that share an attention call: one per CU.  Its four waves keep 64
 // KB of codes in flight, enough for HBM, and fewer shares leave fewer parts to
-// join (us, one / two per CU: 4 x 65536 keys, 64 / 8 heads of 128 97 / 101; 32 x
-// 4096, 32 / 8 heads of 128 44.0 / 43.5; 4 x 8192, 16 / 4 heads of 256 31 / 34).
+// join (us, one / two per CU: 4 x 65536 keys, 64 / 8 heads of 128 101 / 108; 32 x
+// 4096, 32 / 8 heads of 128 44 / 51, of 64 27 / 29; 4 x 8192, 16 / 4 heads of 256
+// 22 / 38).
 // Each leaves at most two unfinished 16-row tiles.
 int kv8_workers(const DeviceInfo* info) { return info->cus; }
 size_t kv8_part_floats(int workers, int d) { return (size_t)workers * 2 * 16 * (d + 2); }
@@ -1633,25 +1634,25 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
   if (num_blocks == 0) p.c.max_blocks = 0;  // no blocks: no tokens, whatever the lengths say
   void* args[] = {&p};
   // Prompts: rows in workgroups of 128 (64 for d = 256) that walk all their
-  // keys, if there is one for every CU; else 16-row tiles whose keys are shared
-  // out (us, shared out / prompts; 32 / 8 heads of 128: 4 x 256 new of 2048 106 /
-  // 64 with 256 such workgroups, 1 x 1024 of 1024 63 / 38 with 256, 4 x 128 of
-  // 2048 57 / 63 with 128, 1 x 512 of 4096 99 / 114 with 128, 1 x 16 of 4096 18 /
-  // 107 with 8).  The workgroups are counted from what the host knows: the
-  // packed rows, and half a workgroup more for each sequence that can have 64
-  // rows.  Sequences of fewer rows, whose keys a workgroup would walk for a few
-  // rows alone, are shared out in a second launch (us, one launch / two: 8 single
-  // tokens of 65536 beside a prompt of 2048 1550 / 272, 63 of 32768 1033 / 898,
-  // 28 of 8192 beside 4 x 512 of 2048 226 / 193; prompts of unequal lengths pay
-  // for it: 4 of up to 2048 behind up to 2048 295 / 303).
+  // keys, if the packed rows fill one for half of the CUs (five eighths for d =
+  // 256); else 16-row tiles whose keys are shared out (us, shared out / prompts;
+  // 32 / 8 heads of 128: 4 x 256 new of 2048 161 / 69 with 256 such workgroups, 6
+  // x 128 of 2048 124 / 66 and 1 x 768 of 4096 169 / 116 with 192, 4 x 128 of 2048
+  // 86 / 65, 1 x 512 of 512 35 / 26, 1 x 512 of 4096 112 / 115 and of 16384 382 /
+  // 427 with 128, 3 x 128 of 2048 58 / 65 with 96, 1 x 16 of 4096 16 / 109 with 8;
+  // 16 / 4 heads of 256: 1 x 640 of 2048 83 / 75 with 160, 4 x 128 of 2048 66 / 75
+  // with 128; full tiles are what counts: 16 x 16 of 2048, 16 workgroups of half as
+  // many rows a head, 48 / 61).  Sequences of fewer than 64 rows, whose keys a
+  // workgroup would walk for them alone, are shared out in a second launch (us,
+  // one launch / two: 8 single tokens of 65536 beside a prompt of 2048 1550 / 272,
+  // 63 of 32768 1033 / 898, 28 of 8192 beside 4 x 512 of 2048 226 / 193; prompts
+  // of unequal lengths pay for it: 4 of up to 2048 behind up to 2048 295 / 303).
   const int prompt_rows = d == 256 ? 64 : 128;
   constexpr int kFew = 64;
   const long long rows = (long long)p.most * p.group, all_rows = (long long)total * p.group;
   const long long prompt_tiles = (rows + prompt_rows - 1) / prompt_rows;
-  const long long long_seqs = all_rows / kFew < batch ? all_rows / kFew : batch;
-  const long long packed = all_rows / prompt_rows + long_seqs / 2;
-  const long long tiles = prompt_tiles * batch < packed ? prompt_tiles * batch : packed;
-  bool prompt = rows >= kFew && tiles * h_kv >= info->cus, split = true;
+  const long long tiles = min(prompt_tiles * batch, all_rows / prompt_rows);
+  bool prompt = rows >= kFew && 8 * tiles * h_kv >= (d == 256 ? 5LL : 4LL) * info->cus, split = true;
   const bool alike = (long long)p.most * batch == total;  // every sequence has max_q rows, if cu is what it should be
   if (prompt && alike) split = false;
   if (way) prompt = way == kKv8Prompt, split = !prompt;
