@@ -282,8 +282,8 @@ __global__ __launch_bounds__(THREADS) void kv8_append_kernel(Kv8AppendParams p) 
 //     1e-3 rms, the worst by 129%).
 //
 // (With fp16 alone prompts of 2048 took 296 us against 300 and 4 x 256 of 256
-// 20.2 against 21.2; where value scales were 2^16 apart elements were then off by
-// up to all of themselves.)
+// 20.2 against 21.2; with value scales 2^12 apart elements then missed their
+// bound, at 2^60 they were zero.)
 // The keys of a 64-key step are dealt to the rows of the A operand so that
 // lane group g (lanes 16 g ..) ends up with p for keys 16 g .. 16 g + 15,
 // which is how a lane of the second product's B operand wants them against
