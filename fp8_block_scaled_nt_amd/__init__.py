@@ -21,6 +21,8 @@ Layouts (all row-major, packed):
   KV8  (k_codes, v_codes, k_scales, v_scales): e4m3 [blocks, h_kv, block, d],
        e4m3 [blocks, h_kv, d, block], fp32 [blocks, h_kv] each; block tables
        int32 [batch, max_blocks]
+  latent  (latent, rope, scales): bf16 [blocks, block, L] and None, or e4m3 and
+       fp32 [blocks, block, L/128]; rope bf16 [blocks, block, L/8]; L 512 or 256
 """
 
 import ctypes
@@ -42,6 +44,8 @@ __all__ = [
     "reserve_workspace", "dense_workspace_size",
     "bf16_w4_gemm_nt", "bf16_w4_workspace_size", "quantize_b_w4", "dequantize_b_w4",
     "empty_kv8_cache", "kv8_append", "kv8_attention", "kv8_attention_workspace_size",
+    "empty_latent_cache", "latent_append", "latent_gather", "latent_attention", "latent_attention_workspace_size",
+    "latent_expanded_attention",
 ]
 
 
@@ -84,6 +88,13 @@ _SIGNATURES = {
     "dg_kv8_append": [_vp, _cl, _vp, _cl] + [_vp] * 7 + [_ci] * 8 + [_vp],
     "dg_kv8_attention": [_vp, _cl] + [_vp] * 9 + [ctypes.c_float] + [_ci] * 11 + [_vp],
     "dg_kv8_attention_workspace_size": [_ci, ctypes.POINTER(ctypes.c_size_t)],
+    "dg_latent_append": ([_vp, _cl, _vp, _cl] + [_vp] * 7 + [_ci, _vp, ctypes.c_float, _vp, _cl, _cl, _vp, _cl, _cl]
+                         + [_ci] * 9 + [_vp]),
+    "dg_latent_gather": [_vp] * 8 + [_ci] * 6 + [_vp],
+    "dg_latent_attention": ([_vp, _cl, _cl, _vp, _cl, _cl] + [_vp] * 7 + [_cl, _cl, _vp, ctypes.c_float]
+                            + [_ci] * 9 + [_vp]),
+    "dg_latent_attention_workspace_size": [_ci, _ci, _ci, ctypes.POINTER(ctypes.c_size_t)],
+    "dg_latent_expanded_attention": [_vp, _cl, _vp, _cl, _vp, _cl] + [_vp] * 4 + [ctypes.c_float] + [_ci] * 7 + [_vp],
 }
 _RESTYPES = {"dg_status_string": ctypes.c_char_p, "dg_last_error_message": ctypes.c_char_p,
              "dg_version": ctypes.c_char_p}
@@ -616,3 +627,183 @@ def kv8_attention_workspace_size(d):
     size = ctypes.c_size_t(0)
     _check(lib().dg_kv8_attention_workspace_size(int(d), ctypes.byref(size)))
     return size.value
+
+
+def empty_latent_cache(num_blocks, latent=512, block=64, fmt="e4m3", device="cuda"):
+    """A cache of num_blocks blocks of `block` tokens of latent attention, fmt "e4m3" or "bf16"."""
+    if fmt not in ("e4m3", "bf16"):
+        raise ValueError("fmt must be 'e4m3' or 'bf16'")
+    dtype = torch.float8_e4m3fn if fmt == "e4m3" else torch.bfloat16
+    return (torch.empty((num_blocks, block, latent), dtype=dtype, device=device),
+            torch.empty((num_blocks, block, latent // 8), dtype=torch.bfloat16, device=device),
+            torch.empty((num_blocks, block, latent // 128), dtype=torch.float32, device=device) if fmt == "e4m3" else None)
+
+
+def _latent_shape(cache, block_table, cu):
+    """(latent, rope, scales pointers, L, block, num_blocks, max_blocks, batch) of a cache and its tables, checked."""
+    latent, rope, scales = cache
+    _need(latent, "latent", (torch.bfloat16,) if scales is None else _FP8, 3)
+    _need(rope, "rope", (torch.bfloat16,), 3)
+    _need(block_table, "block_table", (torch.int32,), 2)
+    _need(cu, "cu", (torch.int32,), 1)
+    num_blocks, block, dim = latent.shape
+    if rope.shape != (num_blocks, block, dim // 8):
+        raise ValueError(f"rope {tuple(rope.shape)} does not fit latent {tuple(latent.shape)}")
+    if scales is not None:
+        _need(scales, "scales", (torch.float32,), 3)
+        if scales.shape != (num_blocks, block, dim // 128):
+            raise ValueError(f"scales {tuple(scales.shape)} do not fit latent {tuple(latent.shape)}")
+    batch, max_blocks = block_table.shape
+    if cu.shape[0] != batch + 1:
+        raise ValueError("the block table and cu (batch + 1) disagree on the batch")
+    return (latent.data_ptr(), rope.data_ptr(), None if scales is None else scales.data_ptr(), dim, block, num_blocks,
+            max_blocks, batch)
+
+
+def _lengths(x, name, batch):
+    _need(x, name, (torch.int32,), 1)
+    if x.shape[0] != batch:
+        raise ValueError(f"{name} must hold {batch} lengths, got {x.shape[0]}")
+    return x.data_ptr()
+
+
+def _rows(x, name, d):
+    """Checks bf16 [total, d] with packed values; returns (total, elements from token to token)."""
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
+        raise TypeError(f"{name} must be a bf16 device tensor [tokens, d]")
+    total, dim = x.shape
+    if dim != d or (x.stride(1) != 1 and d > 1):
+        raise ValueError(f"{name} must be [tokens, {d}] with packed values, got {tuple(x.shape)}")
+    return total, x.stride(0) if total > 1 else -(-d // 8) * 8
+
+
+def _heads(x, name, heads, d):
+    """Checks bf16 [total, heads, d] with packed values; returns (total, elements from token to token, from head to head)."""
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 3 or not x.is_cuda:
+        raise TypeError(f"{name} must be a bf16 device tensor [tokens, heads, d]")
+    total, h, dim = x.shape
+    if dim != d or (heads is not None and h != heads) or (x.stride(2) != 1 and d > 1):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {d}] with packed values, "
+                         f"got {tuple(x.shape)}")
+    return total, x.stride(0) if total > 1 else 0, x.stride(1) if h > 1 else d
+
+
+def latent_append(latent, rope, cache, block_table, ctx_lens, cu_new, max_new, angles, norm=None, eps=1e-6, q_rope=None,
+                  q_out=None, interleaved=True):
+    """Put new tokens' latents (bf16 [total, L], normalised on the way if norm
+    [L] bf16 is given) and rope parts (bf16 [total, L/8], turned by their
+    positions) behind the ctx_lens[i] cached tokens of each sequence, in place;
+    slices of a wider projection serve.  angles: fp32 [positions, L/8], cosines
+    then sines.  q_rope (bf16 [total, heads, L/8], any strides) are the queries'
+    rope parts, turned alike into q_out (in place if None)."""
+    at_latent, at_rope, at_scales, dim, block, num_blocks, max_blocks, batch = _latent_shape(cache, block_table, cu_new)
+    total, ls = _rows(latent, "latent", dim)
+    total_r, rs = _rows(rope, "rope", dim // 8)
+    if total != total_r:
+        raise ValueError(f"latent holds {total} tokens, rope {total_r}")
+    ctx = _lengths(ctx_lens, "ctx_lens", batch)
+    _need(angles, "angles", (torch.float32,), 2)
+    if angles.shape[1] != dim // 8:
+        raise ValueError(f"angles must be [positions, {dim // 8}], got {tuple(angles.shape)}")
+    if norm is not None:
+        _need(norm, "norm", (torch.bfloat16,), 1)
+        if norm.shape[0] != dim:
+            raise ValueError(f"norm must hold {dim} values, got {norm.shape[0]}")
+    heads, q, q_to = 0, (None, 0, 0), (None, 0, 0)
+    if q_rope is not None:
+        q_out = q_rope if q_out is None else q_out
+        total_q, qs, qh = _heads(q_rope, "q_rope", None, dim // 8)
+        heads = q_rope.shape[1]
+        total_o, os_, oh = _heads(q_out, "q_out", heads, dim // 8)
+        if total_q != total or total_o != total:
+            raise ValueError(f"latent holds {total} tokens, q_rope {total_q}, q_out {total_o}")
+        if heads:
+            q, q_to = (q_rope.data_ptr(), qs, qh), (q_out.data_ptr(), os_, oh)
+    elif q_out is not None:
+        raise ValueError("q_out without q_rope")
+    _check(lib().dg_latent_append(latent.data_ptr(), ls, rope.data_ptr(), rs, at_latent, at_rope, at_scales,
+                                  block_table.data_ptr(), ctx, cu_new.data_ptr(), angles.data_ptr(), angles.shape[0],
+                                  None if norm is None else norm.data_ptr(), eps, *q, *q_to, interleaved, batch, total,
+                                  max_new, heads, dim, block, num_blocks, max_blocks, _stream()))
+    return cache
+
+
+def latent_gather(cache, block_table, cu, latent, rope, starts=None):
+    """Cached tokens as packed rows, in place: row cu[i] + j of latent (bf16
+    [total, L]) and rope (bf16 [total, L/8]) is token starts[i] + j (starts None:
+    j) of sequence i.  cu: int32 [batch + 1] running sums of the rows."""
+    at_latent, at_rope, at_scales, dim, block, num_blocks, max_blocks, batch = _latent_shape(cache, block_table, cu)
+    _need(latent, "latent", (torch.bfloat16,), 2)
+    _need(rope, "rope", (torch.bfloat16,), 2)
+    total = latent.shape[0]
+    if latent.shape != (total, dim) or rope.shape != (total, dim // 8):
+        raise ValueError(f"rows must be [tokens, {dim}] and [tokens, {dim // 8}], got {tuple(latent.shape)}, {tuple(rope.shape)}")
+    _check(lib().dg_latent_gather(at_latent, at_rope, at_scales, block_table.data_ptr(),
+                                  None if starts is None else _lengths(starts, "starts", batch), cu.data_ptr(),
+                                  latent.data_ptr(), rope.data_ptr(), batch, total, dim, block, num_blocks, max_blocks,
+                                  _stream()))
+    return latent, rope
+
+
+def _need_lse(lse, total, heads):
+    if lse is None:
+        return None
+    _need(lse, "lse", (torch.float32,), 2)
+    if lse.shape != (total, heads):
+        raise ValueError(f"lse must be {(total, heads)}, got {tuple(lse.shape)}")
+    return lse.data_ptr()
+
+
+def latent_attention(q, q_rope, cache, block_table, kv_lens, cu_q, max_q, out, lse=None, scale=None, causal=True):
+    """Absorbed attention of packed queries over the cache: q (bf16 [total, h,
+    L], the queries' key parts times the up-projection's key weights) and q_rope
+    (bf16 [total, h, L/8]); out (bf16 [total, h, L]) and lse (fp32 [total, h], or
+    None) are written in place.  q, q_rope and out may have any strides from
+    token to token and head to head.  kv_lens counts the queries' own tokens;
+    scale: (3/8 L) ** -0.5 if None, that of heads of L/4 + L/8 values."""
+    at_latent, at_rope, at_scales, dim, block, num_blocks, max_blocks, batch = _latent_shape(cache, block_table, cu_q)
+    total, qs, qh = _heads(q, "q", None, dim)
+    heads = q.shape[1]
+    total_r, rs, rh = _heads(q_rope, "q_rope", heads, dim // 8)
+    total_o, os_, oh = _heads(out, "out", heads, dim)
+    if total_r != total or total_o != total:
+        raise ValueError(f"q holds {total} tokens, q_rope {total_r}, out {total_o}")
+    _check(lib().dg_latent_attention(q.data_ptr(), qs, qh, q_rope.data_ptr(), rs, rh, at_latent, at_rope, at_scales,
+                                     block_table.data_ptr(), _lengths(kv_lens, "kv_lens", batch), cu_q.data_ptr(),
+                                     out.data_ptr(), os_, oh, _need_lse(lse, total, heads),
+                                     (dim * 3 // 8) ** -0.5 if scale is None else scale, causal, batch, total, max_q,
+                                     heads, dim, block, num_blocks, max_blocks, _stream()))
+    return out
+
+
+def latent_attention_workspace_size(latent, max_q, heads):
+    """Bytes of a stream's workspace that latent_attention takes; give it to
+    reserve_workspace before capturing such calls."""
+    size = ctypes.c_size_t(0)
+    _check(lib().dg_latent_attention_workspace_size(int(latent), int(max_q), int(heads), ctypes.byref(size)))
+    return size.value
+
+
+def latent_expanded_attention(q, kv, k_rope, cu_q, cu_kv, max_q, out, lse=None, scale=None, causal=True):
+    """Expanded attention of packed prompts: q (bf16 [total, h, D + D/2]: key
+    part, then rope part), kv (bf16 [total_kv, h, 2 D]: the up-projection's key
+    parts and values), k_rope (bf16 [total_kv, D/2]); out (bf16 [total, h, D]) and
+    lse (fp32 [total, h], or None) are written in place.  cu_q, cu_kv: int32
+    [batch + 1] running sums; a sequence's queries are its last tokens."""
+    _need(cu_q, "cu_q", (torch.int32,), 1)
+    _need(cu_kv, "cu_kv", (torch.int32,), 1)
+    _need(out, "out", (torch.bfloat16,), 3)
+    total, heads, dim = out.shape
+    if cu_q.shape != cu_kv.shape or cu_q.shape[0] < 1:
+        raise ValueError("cu_q and cu_kv must hold batch + 1 running sums each")
+    total_q, qs = _packed(q, "q", heads, dim + dim // 2)
+    total_kv, ks = _packed(kv, "kv", heads, 2 * dim)
+    total_r, rs = _rows(k_rope, "k_rope", dim // 2)
+    if total_q != total or total_r != total_kv:
+        raise ValueError(f"out holds {total} tokens, q {total_q}; kv {total_kv}, k_rope {total_r}")
+    _check(lib().dg_latent_expanded_attention(q.data_ptr(), qs, kv.data_ptr(), ks, k_rope.data_ptr(), rs,
+                                              cu_q.data_ptr(), cu_kv.data_ptr(), out.data_ptr(),
+                                              _need_lse(lse, total, heads),
+                                              (dim + dim // 2) ** -0.5 if scale is None else scale, causal,
+                                              cu_q.shape[0] - 1, total, total_kv, max_q, heads, dim, _stream()))
+    return out

@@ -24,6 +24,7 @@
 
 #include "gemm_kernel.h"
 #include "kv8_kernel.h"
+#include "latent_kernel.h"
 #include "quant_kernel.h"
 #include "skinny_kernel.h"
 #include "w4_kernel.h"
@@ -1063,6 +1064,126 @@ int check_batch(int batch, int total, int most) {
 int kv8_workers(const DeviceInfo* info) { return info->cus; }
 size_t kv8_part_floats(int workers, int d) { return (size_t)workers * 2 * 16 * (d + 2); }
 
+// ---- latent attention (latent_kernel.h)
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_latent_dim(int latent) {
+  if (latent != 256 && latent != 512)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "the latent must have 256 or 512 values (got %d)", latent);
+  return DG_OK;
+}
+
+// Arrays without elements may be null: no pool, no table, no sequences.
+int check_latent_cache(const void* latent, const void* rope, const void* scales, const void* table, int batch,
+                       int latent_dim, int block, int num_blocks, int max_blocks, dg::LatentCache* c) {
+  if (int s = check_latent_dim(latent_dim)) return s;
+  if ((num_blocks != 0 && (!latent || !rope)) || (batch != 0 && max_blocks != 0 && !table))
+    return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (num_blocks < 0 || max_blocks < 0) return fail(DG_ERR_INVALID_ARGUMENT, "block counts must be >= 0");
+  int log2 = 4;
+  while (log2 < 7 && (1 << log2) != block) ++log2;
+  if ((1 << log2) != block)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "block must be 16, 32, 64 or 128 tokens (got %d)", block);
+  if (((long long)max_blocks << log2) > (1LL << 30))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "a sequence's table may span at most 2^30 tokens");
+  if (!aligned16(latent) || !aligned16(rope) || !aligned16(scales) || !aligned4(table))
+    return fail(DG_ERR_MISALIGNED, "cache arrays must be 16-byte aligned, the block table 4-byte");
+  c->latent = (uint8_t*)latent;
+  c->rope = (uint16_t*)rope;
+  c->scales = (float*)scales;
+  c->table = (const int32_t*)table;
+  c->block = block;
+  c->block_log2 = log2;
+  c->num_blocks = num_blocks;
+  c->max_blocks = num_blocks == 0 ? 0 : max_blocks;  // no blocks: no tokens, whatever the lengths say
+  return DG_OK;
+}
+
+// Rows of heads with strides of their own: from token to token and from head to head.
+int check_strided(const void* x, int64_t stride, int64_t head_stride, int heads, int d, int unit, const char* name) {
+  if ((reinterpret_cast<uintptr_t>(x) & (unit * 2 - 1)) != 0)
+    return fail(DG_ERR_MISALIGNED, "%s must be %d-byte aligned", name, unit * 2);
+  if (stride < 0 || head_stride < 0 || stride % unit != 0 || head_stride % unit != 0 ||
+      (heads > 1 && head_stride < d))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: strides must be multiples of %d elements, and at least %d from head to "
+                "head (got %lld, %lld)", name, unit, d, (long long)stride, (long long)head_stride);
+  return DG_OK;
+}
+
+// Tiles of 16 rows that a workgroup of absorbed attention takes at once: as
+// many as one sequence's queries fill, at most four.
+int latent_row_tiles(int max_q, int h_q) {
+  const long long rows = (long long)max_q * h_q;
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+}
+size_t latent_part_floats(int workers, int tiles, int latent) { return (size_t)workers * 2 * 16 * tiles * (latent + 2); }
+
+int check_latent_rows(int max_q, int h_q) {
+  if (h_q < 1 || h_q > 32767) return fail(DG_ERR_INVALID_ARGUMENT, "h_q must be 1..32767 (got %d)", h_q);
+  if ((long long)max_q * h_q > (1LL << 30))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many queries per sequence (%d of %d heads)", max_q, h_q);
+  return DG_OK;
+}
+
+struct LatentKernel {
+  const void* fn;
+  int smem;
+};
+
+template <int L, bool F8, int NT>
+LatentKernel latent_attn() {
+  return {reinterpret_cast<const void*>(&dg::latent_attn_kernel<L, F8, NT>), dg::LatentLds<L, F8, NT>::kBytes};
+}
+template <int L, bool F8>
+LatentKernel latent_attn(int tiles) {
+  return tiles == 1 ? latent_attn<L, F8, 1>() : tiles == 2 ? latent_attn<L, F8, 2>() : latent_attn<L, F8, 4>();
+}
+LatentKernel latent_attn(int latent, bool f8, int tiles) {
+  return latent == 512 ? (f8 ? latent_attn<512, true>(tiles) : latent_attn<512, false>(tiles))
+                       : (f8 ? latent_attn<256, true>(tiles) : latent_attn<256, false>(tiles));
+}
+
+template <int D, int MT>
+LatentKernel latent_expanded() {
+  return {reinterpret_cast<const void*>(&dg::latent_expanded_kernel<D, MT>), 2 * dg::kLatentStep * (4 * D + D)};
+}
+
+std::once_flag g_latent_once;
+hipError_t g_latent_err = hipSuccess;
+
+// These kernels take more LDS than a launch may ask for unasked.
+int ensure_latent_attributes() {
+  std::call_once(g_latent_once, []() {
+    const LatentKernel expanded[] = {latent_expanded<128, 2>(), latent_expanded<64, 2>()};
+    auto allow = [](const LatentKernel& k) {
+      const hipError_t e = hipFuncSetAttribute(k.fn, hipFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+      if (e != hipSuccess) g_latent_err = e;
+    };
+    for (int latent : {256, 512})
+      for (bool f8 : {false, true})
+        for (int tiles : {1, 2, 4}) allow(latent_attn(latent, f8, tiles));
+    for (const LatentKernel& k : expanded) allow(k);
+  });
+  if (g_latent_err != hipSuccess)
+    return fail(DG_ERR_HIP, "hipFuncSetAttribute: %s", hipGetErrorString(g_latent_err));
+  return DG_OK;
+}
+
+template <int L>
+const void* latent_append_fn(bool f8, bool pairs) {
+  return f8 ? (pairs ? reinterpret_cast<const void*>(&dg::latent_append_kernel<L, true, true>)
+                     : reinterpret_cast<const void*>(&dg::latent_append_kernel<L, true, false>))
+            : (pairs ? reinterpret_cast<const void*>(&dg::latent_append_kernel<L, false, true>)
+                     : reinterpret_cast<const void*>(&dg::latent_append_kernel<L, false, false>));
+}
+
+template <int L>
+const void* latent_gather_fn(bool f8) {
+  return f8 ? reinterpret_cast<const void*>(&dg::latent_gather_kernel<L, true>)
+            : reinterpret_cast<const void*>(&dg::latent_gather_kernel<L, false>);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1680,6 +1801,214 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
                    : d == 128 ? reinterpret_cast<const void*>(&dg::kv8_attn_kernel<128>)
                               : reinterpret_cast<const void*>(&dg::kv8_attn_kernel<256>);
   return launch_plain(kKv8Split, fn, dim3(p.workers), 256, args, stream);
+}
+
+int dg_latent_append(const uint16_t* latent, int64_t latent_stride, const uint16_t* rope, int64_t rope_stride,
+                     void* cache_latent, uint16_t* cache_rope, float* cache_scales, const int32_t* block_table,
+                     const int32_t* ctx_lens, const int32_t* cu_new, const float* angles, int positions,
+                     const uint16_t* norm, float eps, const uint16_t* q, int64_t q_stride, int64_t q_head_stride,
+                     uint16_t* q_out, int64_t q_out_stride, int64_t q_out_head_stride, int interleaved, int batch,
+                     int total, int max_new, int h_q, int latent_dim, int block, int num_blocks, int max_blocks,
+                     dg_stream_t stream) {
+  if ((batch != 0 && !ctx_lens) || !cu_new || (total > 0 && (!latent || !rope)) || (positions > 0 && !angles) ||
+      (q && !q_out))
+    return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  dg::LatentAppendParams p{};
+  if (int s = check_latent_cache(cache_latent, cache_rope, cache_scales, block_table, batch, latent_dim, block,
+                                 num_blocks, max_blocks, &p.c)) return s;
+  if (int s = check_batch(batch, total, max_new)) return s;
+  const int rope_dim = latent_dim / 8;
+  if (int s = check_packed(latent, latent_stride, 1, latent_dim, "latent")) return s;
+  if (int s = check_packed(rope, rope_stride, 1, rope_dim, "rope")) return s;
+  if (positions < 0) return fail(DG_ERR_INVALID_ARGUMENT, "positions must be >= 0 (got %d)", positions);
+  if (!(eps >= 0.f && eps <= 3.4e38f)) return fail(DG_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0 (got %g)", (double)eps);
+  if (q) {
+    if (h_q < 1 || h_q > 32767) return fail(DG_ERR_INVALID_ARGUMENT, "h_q must be 1..32767 (got %d)", h_q);
+    if (int s = check_strided(q, q_stride, q_head_stride, h_q, rope_dim, 8, "q")) return s;
+    if (int s = check_strided(q_out, q_out_stride, q_out_head_stride, h_q, rope_dim, 8, "q_out")) return s;
+    if (q == q_out && (q_stride != q_out_stride || q_head_stride != q_out_head_stride))
+      return fail(DG_ERR_INVALID_ARGUMENT, "in place q and q_out must have the same strides");
+  }
+  if (!aligned16(angles) || !aligned16(norm) || !aligned4(ctx_lens) || !aligned4(cu_new))
+    return fail(DG_ERR_MISALIGNED, "angles and norm must be 16-byte aligned, lengths 4-byte");
+  if (batch == 0 || total == 0 || max_new == 0 || positions == 0) return ok();
+  if (total > (1 << 25)) return fail(DG_ERR_UNSUPPORTED_SHAPE, "at most 2^25 new tokens (got %d)", total);
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  p.latent = latent;
+  p.rope = rope;
+  p.latent_stride = latent_stride;
+  p.rope_stride = rope_stride;
+  p.ctx = ctx_lens;
+  p.cu = cu_new;
+  p.angles = angles;
+  p.positions = positions;
+  p.norm = norm;
+  p.eps = eps;
+  p.q = q;
+  p.q_out = q_out;
+  p.q_stride = q_stride;
+  p.q_head_stride = q_head_stride;
+  p.q_out_stride = q_out_stride;
+  p.q_out_head_stride = q_out_head_stride;
+  p.h_q = q ? h_q : 0;
+  p.batch = batch;
+  p.total = total;
+  p.most = max_new;
+  const bool f8 = cache_scales != nullptr;
+  const void* fn = latent_dim == 512 ? latent_append_fn<512>(f8, interleaved != 0) : latent_append_fn<256>(f8, interleaved != 0);
+  const int parts = p.h_q > dg::kLatentHeads ? (p.h_q + dg::kLatentHeads - 1) / dg::kLatentHeads : 1;
+  void* args[] = {&p};
+  return launch_plain("latent_append", fn, dim3((total + 3) / 4, parts), 256, args, stream);
+}
+
+int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const float* cache_scales,
+                     const int32_t* block_table, const int32_t* starts, const int32_t* cu, uint16_t* latent,
+                     uint16_t* rope, int batch, int total, int latent_dim, int block, int num_blocks, int max_blocks,
+                     dg_stream_t stream) {
+  if (!cu || (total > 0 && (!latent || !rope))) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  dg::LatentGatherParams p{};
+  if (int s = check_latent_cache(cache_latent, cache_rope, cache_scales, block_table, batch, latent_dim, block,
+                                 num_blocks, max_blocks, &p.c)) return s;
+  if (int s = check_batch(batch, total, 0)) return s;
+  if (!aligned16(latent) || !aligned16(rope) || !aligned4(starts) || !aligned4(cu))
+    return fail(DG_ERR_MISALIGNED, "rows must be 16-byte aligned, lengths 4-byte");
+  if (batch == 0 || total == 0 || p.c.max_blocks == 0) return ok();
+  if (total > (1 << 25)) return fail(DG_ERR_UNSUPPORTED_SHAPE, "at most 2^25 rows (got %d)", total);
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  p.starts = starts;
+  p.cu = cu;
+  p.latent = latent;
+  p.rope = rope;
+  p.batch = batch;
+  p.total = total;
+  const bool f8 = cache_scales != nullptr;
+  const void* fn = latent_dim == 512 ? latent_gather_fn<512>(f8) : latent_gather_fn<256>(f8);
+  void* args[] = {&p};
+  return launch_plain("latent_gather", fn, dim3((total + 3) / 4), 256, args, stream);
+}
+
+int dg_latent_attention_workspace_size(int latent_dim, int max_q, int h_q, size_t* bytes) {
+  if (!bytes) return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  *bytes = 0;
+  if (int s = check_latent_dim(latent_dim)) return s;
+  if (max_q < 0) return fail(DG_ERR_INVALID_ARGUMENT, "max_q must be >= 0 (got %d)", max_q);
+  if (int s = check_latent_rows(max_q, h_q)) return s;
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  *bytes = latent_part_floats(info->cus, latent_row_tiles(max_q, h_q), latent_dim) * sizeof(float);
+  return ok();
+}
+
+int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stride, const uint16_t* q_rope,
+                        int64_t q_rope_stride, int64_t q_rope_head_stride, const void* cache_latent,
+                        const uint16_t* cache_rope, const float* cache_scales, const int32_t* block_table,
+                        const int32_t* kv_lens, const int32_t* cu_q, uint16_t* out, int64_t out_stride,
+                        int64_t out_head_stride, float* lse, float scale, int causal, int batch, int total, int max_q,
+                        int h_q, int latent_dim, int block, int num_blocks, int max_blocks, dg_stream_t stream) {
+  if ((batch != 0 && !kv_lens) || !cu_q || (total > 0 && (!q || !q_rope || !out)))
+    return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  dg::LatentAttnParams p{};
+  if (int s = check_latent_cache(cache_latent, cache_rope, cache_scales, block_table, batch, latent_dim, block,
+                                 num_blocks, max_blocks, &p.c)) return s;
+  if (int s = check_batch(batch, total, max_q)) return s;
+  if (int s = check_latent_rows(max_q, h_q)) return s;
+  if (!(scale >= 0.f && scale <= 3.4e38f))
+    return fail(DG_ERR_INVALID_ARGUMENT, "scale must be finite and >= 0 (got %g)", (double)scale);
+  if (int s = check_strided(q, q_stride, q_head_stride, h_q, latent_dim, 8, "q")) return s;
+  if (int s = check_strided(q_rope, q_rope_stride, q_rope_head_stride, h_q, latent_dim / 8, 8, "q_rope")) return s;
+  if (int s = check_strided(out, out_stride, out_head_stride, h_q, latent_dim, 8, "out")) return s;
+  if (!aligned4(lse) || !aligned4(kv_lens) || !aligned4(cu_q))
+    return fail(DG_ERR_MISALIGNED, "lse and lengths must be 4-byte aligned");
+  if (batch == 0 || total == 0 || max_q == 0) return ok();
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  if (int s = ensure_latent_attributes()) return s;
+  p.q = q;
+  p.qr = q_rope;
+  p.q_stride = q_stride;
+  p.q_head_stride = q_head_stride;
+  p.qr_stride = q_rope_stride;
+  p.qr_head_stride = q_rope_head_stride;
+  p.kv_lens = kv_lens;
+  p.cu = cu_q;
+  p.out = out;
+  p.out_stride = out_stride;
+  p.out_head_stride = out_head_stride;
+  p.lse = lse;
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.causal = causal != 0;
+  p.batch = batch;
+  p.total = total;
+  p.most = max_q;
+  p.h_q = h_q;
+  p.workers = info->cus;
+  const int tiles = latent_row_tiles(max_q, h_q);
+  const LatentKernel k = latent_attn(latent_dim, cache_scales != nullptr, tiles);
+  char* base = nullptr;
+  if (int s = ensure_workspace(dev, (hipStream_t)stream,
+                               latent_part_floats(p.workers, tiles, latent_dim) * sizeof(float), &base)) return s;
+  p.arrived = (int*)base;
+  p.part_u = (float*)(base + kWsHeader);
+  p.part_ml = p.part_u + (size_t)p.workers * 2 * 16 * tiles * latent_dim;
+  void* args[] = {&p};
+  return launch_plain("latent_attention", k.fn, dim3(p.workers), 256, args, stream, k.smem);
+}
+
+int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint16_t* kv, int64_t kv_stride,
+                                 const uint16_t* k_rope, int64_t k_rope_stride, const int32_t* cu_q,
+                                 const int32_t* cu_kv, uint16_t* out, float* lse, float scale, int causal, int batch,
+                                 int total, int total_kv, int max_q, int heads, int head_dim, dg_stream_t stream) {
+  if (!cu_q || !cu_kv || (total > 0 && (!q || !out)) || (total_kv > 0 && (!kv || !k_rope)))
+    return fail(DG_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "head_dim must be 64 or 128 (got %d)", head_dim);
+  if (heads < 1 || heads > 32767) return fail(DG_ERR_INVALID_ARGUMENT, "heads must be 1..32767 (got %d)", heads);
+  if (int s = check_batch(batch, total, max_q)) return s;
+  if (total_kv < 0) return fail(DG_ERR_INVALID_ARGUMENT, "token counts must be >= 0");
+  if (!(scale >= 0.f && scale <= 3.4e38f))
+    return fail(DG_ERR_INVALID_ARGUMENT, "scale must be finite and >= 0 (got %g)", (double)scale);
+  if (int s = check_packed(q, q_stride, heads, head_dim / 2 * 3, "q")) return s;
+  if (int s = check_packed(kv, kv_stride, heads, 2 * head_dim, "kv")) return s;
+  if (int s = check_packed(k_rope, k_rope_stride, 1, head_dim / 2, "k_rope")) return s;
+  if (kv_stride >= (1 << 26) || k_rope_stride >= (1 << 26))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "kv and k_rope: strides must stay below 2^26 elements");
+  if (!aligned16(out) || !aligned4(lse) || !aligned4(cu_q) || !aligned4(cu_kv))
+    return fail(DG_ERR_MISALIGNED, "out must be 16-byte aligned, lse and lengths 4-byte");
+  if (batch == 0 || total == 0 || max_q == 0) return ok();
+  int dev;
+  DeviceInfo* info;
+  if (int s = current_device(&dev, &info)) return s;
+  if (int s = ensure_latent_attributes()) return s;
+  dg::LatentExpandedParams p{};
+  p.q = q;
+  p.kv = kv;
+  p.kr = k_rope;
+  p.q_stride = q_stride;
+  p.kv_stride = kv_stride;
+  p.kr_stride = k_rope_stride;
+  p.cu = cu_q;
+  p.cu_kv = cu_kv;
+  p.out = out;
+  p.lse = lse;
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.causal = causal != 0;
+  p.batch = batch;
+  p.total = total;
+  p.total_kv = total_kv;
+  p.most = max_q < total ? max_q : total;
+  p.h = heads;
+  constexpr int kRows = 128;
+  const long long tiles = ((long long)p.most + kRows - 1) / kRows;
+  if (tiles > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many queries per sequence (%d)", p.most);
+  const LatentKernel k = head_dim == 128 ? latent_expanded<128, 2>() : latent_expanded<64, 2>();
+  void* args[] = {&p};
+  return launch_plain("latent_expanded_attention", k.fn, dim3(heads, batch, (unsigned)tiles), 256, args, stream, k.smem);
 }
 
 }  // extern "C"

@@ -1,0 +1,1075 @@
+// Attention whose keys and values come from one shared latent vector a token,
+// the paged cache of those vectors, and the rotation of their rope parts.
+//
+// A token is a latent c of L values and a rope part r of P = L / 8 values,
+// both shared by all heads:
+//
+//   latent [num_blocks][block][L]   bf16, or e4m3 codes with
+//   scales [num_blocks][block][L / 128], powers of two, for each token and 128 values
+//   rope   [num_blocks][block][P]   bf16
+//
+// Absorbed, a head's key is (c, r) and its value c.  Expanded, an
+// up-projection gives each head a key part and a value of L / 4 values each.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_kernel.h"
+#include "kv8_kernel.h"
+#include "quant_kernel.h"
+#include "w4_kernel.h"
+
+namespace dg {
+
+
+
+struct LatentCache {
+  uint8_t* latent;  // bf16 or e4m3
+  uint16_t* rope;
+  float* scales;        // null: latents are bf16
+  const int32_t* table;  // [batch][max_blocks]
+  int block, block_log2, num_blocks, max_blocks;
+};
+
+// The block of sequence `seq` that holds token `token` >= 0, or -1 where the table has none.
+__device__ __forceinline__ int latent_page(const LatentCache& c, int seq, int token) {
+  if (c.max_blocks == 0) return -1;
+  const int j = token >> c.block_log2;
+  const int page = c.table[(size_t)seq * c.max_blocks + min(j, c.max_blocks - 1)];
+  return (j < c.max_blocks) & ((unsigned)page < (unsigned)c.num_blocks) ? page : -1;
+}
+
+// Which sequence packed row `row` is of, by the running sums cu: how many of
+// cu[1..batch] it has passed.  The wave's lanes look at 64 of them at a time.
+// batch: none.
+__device__ __forceinline__ int latent_seq_of(const int32_t* cu, int batch, int row) {
+  const int lane = threadIdx.x & 63;
+  int seq = 0;
+  for (int j = 0; j < batch; j += 64) {
+    const int end = cu[min(j + lane, batch - 1) + 1];
+    seq += __popcll(__ballot(j + lane < batch && end <= row));
+  }
+  return seq;
+}
+
+// ---- append
+
+struct LatentAppendParams {
+  const uint16_t* latent;  // bf16 rows, *_stride elements from token to token
+  const uint16_t* rope;
+  long long latent_stride, rope_stride;
+  LatentCache c;
+  const int32_t* ctx;
+  const int32_t* cu;
+  const float* angles;  // [positions][P]: P / 2 cosines, P / 2 sines
+  int positions;
+  const uint16_t* norm;  // bf16 [L] or null
+  float eps;
+  const uint16_t* q;  // rope parts of the queries, or null
+  uint16_t* q_out;
+  long long q_stride, q_head_stride, q_out_stride, q_out_head_stride;
+  int h_q, batch, total, most;
+};
+
+// Eight pairs (a, b) turned by their angles: (a cos - b sin, a sin + b cos) in
+// fp32, rounded once.  PAIRS: x[0], x[1] hold them as neighbours, else x[0]
+// the a's and x[1] the b's.
+template <bool PAIRS>
+__device__ __forceinline__ void latent_rotate(v4u (&x)[2], const v4f (&c)[2], const v4f (&n)[2]) {
+  if constexpr (PAIRS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = x[i / 4][i % 4];
+      const float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xFFFF0000u);
+      const float cs = c[i / 4][i % 4], sn = n[i / 4][i % 4];
+      x[i / 4][i % 4] = pack2_bf16(a * cs - b * sn, a * sn + b * cs);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t wa = x[0][i], wb = x[1][i];
+      const float a0 = __uint_as_float(wa << 16), a1 = __uint_as_float(wa & 0xFFFF0000u);
+      const float b0 = __uint_as_float(wb << 16), b1 = __uint_as_float(wb & 0xFFFF0000u);
+      const float c0 = c[i / 2][2 * i % 4], c1 = c[i / 2][2 * i % 4 + 1];
+      const float n0 = n[i / 2][2 * i % 4], n1 = n[i / 2][2 * i % 4 + 1];
+      x[0][i] = pack2_bf16(a0 * c0 - b0 * n0, a1 * c1 - b1 * n1);
+      x[1][i] = pack2_bf16(a0 * n0 + b0 * c0, a1 * n1 + b1 * c1);
+    }
+  }
+}
+
+// One wave takes one token: its latent, its rope part, and (blockIdx.y) some
+// of the queries' heads.  A lane turns eight pairs of a head; the cosines and
+// sines that it needs are the same for every head.
+constexpr int kLatentHeads = 32;  // query heads of one wave
+
+template <int L, bool F8, bool PAIRS>
+__global__ __launch_bounds__(256) void latent_append_kernel(LatentAppendParams p) {
+  constexpr int P = L / 8, kPer = P / 16;  // lanes of one head
+  const int lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
+  if (t >= p.total) return;
+  const int j = lane % kPer;
+  const bool first = blockIdx.y == 0;
+  // everything that does not hang on the token's place is on its way before it is known
+  v4u x = {0, 0, 0, 0};
+  if (first && lane * 8 < L) x = *(const v4u*)(p.latent + (long long)t * p.latent_stride + lane * 8);
+  const int seq = __builtin_amdgcn_readfirstlane(latent_seq_of(p.cu, p.batch, t));
+  if (seq >= p.batch) return;
+  const int i = t - p.cu[seq];
+  if (i < 0 || i >= p.most) return;
+  const long long pos64 = (long long)max(p.ctx[seq], 0) + i;
+  if (pos64 >= p.positions) return;
+  const int pos = (int)pos64;
+  const float* at = p.angles + (size_t)pos * P + j * 8;
+  const v4f cs[2] = {*(const v4f*)at, *(const v4f*)(at + 4)};
+  const v4f sn[2] = {*(const v4f*)(at + P / 2), *(const v4f*)(at + P / 2 + 4)};
+  const int o0 = PAIRS ? j * 16 : j * 8, o1 = PAIRS ? j * 16 + 8 : P / 2 + j * 8;
+  if (p.q) {
+    const int last = min((int)(blockIdx.y + 1) * kLatentHeads, p.h_q);
+#pragma unroll 2
+    for (int h = blockIdx.y * kLatentHeads + lane / kPer; h < last; h += 64 / kPer) {
+      const uint16_t* src = p.q + (long long)t * p.q_stride + (long long)h * p.q_head_stride;
+      uint16_t* dst = p.q_out + (long long)t * p.q_out_stride + (long long)h * p.q_out_head_stride;
+      v4u y[2] = {*(const v4u*)(src + o0), *(const v4u*)(src + o1)};
+      latent_rotate<PAIRS>(y, cs, sn);
+      *(v4u*)(dst + o0) = y[0];
+      *(v4u*)(dst + o1) = y[1];
+    }
+  }
+  if (!first) return;
+  const int page = latent_page(p.c, seq, pos);
+  if (page < 0) return;
+  const size_t row = ((size_t)page << p.c.block_log2) + (pos & (p.c.block - 1));
+  if (lane < kPer) {
+    const uint16_t* src = p.rope + (long long)t * p.rope_stride;
+    v4u y[2] = {*(const v4u*)(src + o0), *(const v4u*)(src + o1)};
+    latent_rotate<PAIRS>(y, cs, sn);
+    *(v4u*)(p.c.rope + row * P + o0) = y[0];
+    *(v4u*)(p.c.rope + row * P + o1) = y[1];
+  }
+  if (p.norm || F8) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(x[e] << 16);
+      v[2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u);
+    }
+    if (p.norm) {
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += v[e] * v[e];
+#pragma unroll
+      for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s, 64);
+      const float inv = 1.f / sqrtf(sum * (1.f / L) + p.eps);
+      const v4u w = *(const v4u*)(p.norm + lane * 8 % L);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = v[e] * inv * __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+    }
+    if constexpr (F8) {
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]) < __builtin_huge_valf() ? fabsf(v[e]) : 0.f);
+#pragma unroll
+      for (int s = 8; s >= 1; s >>= 1) amax = fmaxf(amax, __shfl_xor(amax, s, 64));
+      const float scale = kv8_scale(amax), inv = 1.f / scale;  // powers of two
+      if (lane * 8 < L) {
+        *(uint2*)(p.c.latent + row * L + lane * 8) =
+            make_uint2(kv8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                       kv8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+        if (lane % 16 == 0) p.c.scales[row * (L / 128) + lane / 16] = scale;
+      }
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = pack2_bf16(v[2 * e], v[2 * e + 1]);
+  }
+  if constexpr (!F8)
+    if (lane * 8 < L) *(v4u*)(p.c.latent + (row * L + lane * 8) * 2) = x;
+}
+
+// ---- gather
+
+struct LatentGatherParams {
+  LatentCache c;
+  const int32_t* starts;  // first token of each sequence, or null: 0
+  const int32_t* cu;
+  uint16_t* latent;  // bf16 [total][L]
+  uint16_t* rope;    // bf16 [total][P]
+  int batch, total;
+};
+
+// Eight codes times a power of two, as bf16: exact but for results outside bf16's range.
+__device__ __forceinline__ v4u latent_widen(uint32_t lo, uint32_t hi, float scale) {
+  v4u r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true));
+  return r;
+}
+
+// One wave takes one token.
+template <int L, bool F8>
+__global__ __launch_bounds__(256) void latent_gather_kernel(LatentGatherParams p) {
+  constexpr int P = L / 8;
+  const int lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
+  if (t >= p.total) return;
+  const int seq = __builtin_amdgcn_readfirstlane(latent_seq_of(p.cu, p.batch, t));
+  if (seq >= p.batch) return;
+  const int i = t - p.cu[seq];
+  const long long pos64 = (long long)(p.starts ? max(p.starts[seq], 0) : 0) + i;
+  if (i < 0 || pos64 > 0x7FFFFFFFLL) return;
+  const int pos = (int)pos64;
+  const int page = latent_page(p.c, seq, pos);
+  if (page < 0) return;
+  const size_t row = ((size_t)page << p.c.block_log2) + (pos & (p.c.block - 1));
+  if (lane * 8 < P) *(v4u*)(p.rope + (size_t)t * P + lane * 8) = *(const v4u*)(p.c.rope + row * P + lane * 8);
+  if (lane * 8 >= L) return;
+  v4u x;
+  if constexpr (F8) {
+    const uint2 w = *(const uint2*)(p.c.latent + row * L + lane * 8);
+    x = latent_widen(w.x, w.y, p.c.scales[row * (L / 128) + lane / 16]);
+  } else {
+    x = *(const v4u*)(p.c.latent + (row * L + lane * 8) * 2);
+  }
+  *(v4u*)(p.latent + (size_t)t * L + lane * 8) = x;
+}
+
+// ---- attention, absorbed
+//
+//   x[j] = scale * (ql . c[j] + qr . r[j])   over the tokens j that the row sees
+//   o    = sum_j e^(x[j] - lse) c[j],  lse = log sum_j e^x[j]
+//
+// Rows are (query, head) pairs of one sequence, row = query * h_q + head: all
+// of them read the same tokens, once.  Per row the kernel carries a reference
+// m, u = sum_j 2^(t[j] - m) c[j] and l = sum_j 2^(t[j] - m) in fp32, with
+// t[j] = log2(e) x[j].  m stands kLatentLead above the row's largest t when it
+// was set and moves when some t passes it: p never passes 1, and few steps pay
+// for scaling u.
+
+struct LatentAttnParams {
+  const uint16_t* q;   // bf16 latent parts of the queries
+  const uint16_t* qr;  // and their rope parts
+  long long q_stride, q_head_stride, qr_stride, qr_head_stride;
+  LatentCache c;
+  const int32_t* kv_lens;
+  const int32_t* cu;
+  uint16_t* out;  // bf16
+  long long out_stride, out_head_stride;
+  float* lse;  // [total][h_q] or null
+  float scale_log2;
+  int causal, batch, total, most, h_q;
+  // split work: workgroup w computes its share of the units below
+  float* part_u;   // [workers][2][rows of a tile][L], as the lanes hold it
+  float* part_ml;  // [workers][2][rows of a tile][2]
+  int* arrived;    // [workers] counters, zero between calls
+  int workers;
+};
+
+constexpr int kLatentStep = 64;       // tokens of one step
+constexpr float kLatentLead = 8.f;    // log2 of how far the reference is put above the largest score
+
+// How LDS rows of tokens are turned so that neither the 16 tokens of a row
+// fragment nor the 8 tokens that a transposing read covers at a time meet in a
+// bank: 16-byte piece s of token t lies in slot s ^ latent_turn(t).
+__device__ __forceinline__ int latent_turn(int t) { return (t & 3) << 1 | (t & 8) | (t >> 2 & 1); }
+
+struct LatentSeq {
+  int first, count;  // its queries
+  int kv;            // its tokens that the table has room for
+  int pos;           // where its first query stands (negative: before the cache)
+  int steps, tiles;
+};
+
+template <int ROWS>
+__device__ __forceinline__ LatentSeq latent_seq(const LatentAttnParams& p, int seq) {
+  LatentSeq s;
+  const int all = kv8_rows(p.cu, seq, p.total, p.most, &s.first, &s.count);
+  const long long room = (long long)p.c.max_blocks << p.c.block_log2;
+  const int kv = max(p.kv_lens[seq], 0);
+  s.kv = kv < room ? kv : (int)room;
+  s.pos = kv - all;
+  s.steps = (s.kv + kLatentStep - 1) / kLatentStep;
+  s.tiles = (s.count * p.h_q + ROWS - 1) / ROWS;
+  return s;
+}
+
+// The same in scalar registers, where `seq` is uniform.
+__device__ __forceinline__ int latent_uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+template <int ROWS>
+__device__ __forceinline__ LatentSeq latent_seq_uniform(const LatentAttnParams& p, int seq) {
+  const LatentSeq s = latent_seq<ROWS>(p, seq);
+  return LatentSeq{latent_uniform(s.first), latent_uniform(s.count), latent_uniform(s.kv),
+                   latent_uniform(s.pos), latent_uniform(s.steps), latent_uniform(s.tiles)};
+}
+
+// Tokens [0, hi) that query `i` of the sequence sees.
+__device__ __forceinline__ int latent_sees(const LatentAttnParams& p, const LatentSeq& s, int i) {
+  return p.causal ? max(min(s.pos + i + 1, s.kv), 0) : s.kv;
+}
+
+// The halves of a dword of two bf16 that are finite; the others become zero.
+__device__ __forceinline__ uint32_t bf16_finite(uint32_t w) {
+  w = (w & 0x7F80u) == 0x7F80u ? w & 0xFFFF0000u : w;
+  return (w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFFu : w;
+}
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// Four bf16 of one channel and four tokens, from token-major rows: lane i of
+// 16 gives the address of four channels of token i / 4 and gets channel i.
+__device__ __forceinline__ v2u lds_turned(const uint8_t* at) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(lds_u8*)at));
+}
+
+// A barrier that waits for this wave's LDS accesses, and not for the next
+// step's DMA as __syncthreads() would.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  block_barrier();
+}
+
+// Ends a run of LDS DMAs: the load under EXEC = 0 that each of them begins
+// with, so that the vector memory instruction behind the last one is such a
+// load too, whatever the compiler puts there (see lds_dma16).
+__device__ __forceinline__ void lds_dma_end(v4i_rsrc rs, uint32_t voff) {
+  uint64_t exec_save;
+  asm volatile("s_and_saveexec_b64 %0, 0\n\tbuffer_load_dword %1, %1, %2, 0 offen\n\ts_mov_b64 exec, %0"
+               : "=&s"(exec_save) : "v"(voff), "s"(rs) : "memory", "scc");
+}
+
+// LDS of the absorbed kernel, in bytes.
+template <int L, bool F8, int NT>
+struct LatentLds {
+  static constexpr int P = L / 8;
+  static constexpr int kRow = F8 ? L : 2 * L;                 // a token's latent as it lies in memory
+  static constexpr int kLatent = kLatentStep * kRow;
+  static constexpr int kRope = kLatentStep * P * 2;
+  static constexpr int kScales = F8 ? 4 * 256 : 0;
+  static constexpr int kBuffer = kLatent + kRope + kScales;   // two of them
+  static constexpr int kWide = 2 * kBuffer;                   // e4m3: the step's latents in bf16
+  static constexpr int kP = kWide + (F8 ? kLatentStep * L * 2 : 0);  // p [rows][64], bf16
+  // the second halves of p: [wave][rows][16]; for L = 512 each wave puts its
+  // own over its rope parts of the step, which nobody reads any more
+  static constexpr bool kRestOverRope = 16 * P * 2 >= 16 * NT * 32;
+  static constexpr int kRest = kP + 16 * NT * 128;
+  static constexpr int kMax = kRest + (kRestOverRope ? 0 : 4 * 16 * NT * 32);  // [4][rows] floats
+  static constexpr int kFlags = kMax + 4 * 16 * NT * 4;
+  static constexpr int kBytes = kFlags + 64;
+};
+
+// A workgroup of four waves takes an equal share of all (sequence, tile of 16
+// NT rows, 64-token step) units, in that order.  In a step wave w brings
+// tokens 16 w .. 16 w + 15 to LDS and computes all rows' scores with them; p
+// passes through LDS, and wave w adds up channels w L / 4 .. of every row.  So
+// each token's latent is fetched once, read from LDS once for the first product
+// and once for the second, and q and u stay in registers.
+template <int L, bool F8, int NT>
+__global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p) {
+  using Lds = LatentLds<L, F8, NT>;
+  constexpr int P = L / 8, kRows = 16 * NT, kJ = L / 64, kC = L / 64;  // kC column tiles of 16 a wave
+  constexpr int kRopeFrags = P / 32;
+  extern __shared__ __align__(1024) uint8_t lds[];  // all of it: a row's place has to be a multiple of its size
+  long long* const box = (long long*)(lds + Lds::kFlags + 16);
+  int& s_last = *(int*)(lds + Lds::kFlags + 8);
+  float* const s_max = (float*)(lds + Lds::kMax);
+  int* const s_flag = (int*)(lds + Lds::kFlags);
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
+
+  // rows of sequences without tokens
+  for (int i = blockIdx.x; i < p.batch; i += p.workers) {
+    const LatentSeq s = latent_seq<kRows>(p, i);
+    if (s.steps > 0) continue;
+    for (int r = tid / (L / 8); r < s.count * p.h_q; r += 256 / (L / 8)) {
+      const int token = s.first + r / p.h_q, head = r % p.h_q;
+      *(v4u*)(p.out + token * p.out_stride + head * p.out_head_stride + tid % (L / 8) * 8) = v4u{0, 0, 0, 0};
+      if (p.lse && tid % (L / 8) == 0) p.lse[(size_t)token * p.h_q + head] = -__builtin_huge_valf();
+    }
+  }
+  auto units_of = [&](const LatentSeq& s) { return (long long)s.tiles * s.steps; };
+  auto chunk_of = [&](int first) {
+    const int i = first + tid;
+    Kv8Chunk c;
+    c.units = i < p.batch ? units_of(latent_seq<kRows>(p, i)) : 0;
+    c.before = kv8_scan256(c.units, &c.total, box) - c.units;
+    return c;
+  };
+  Kv8Chunk chunk = chunk_of(0);
+  long long total = chunk.total;
+  for (int i = 256; i < p.batch; i += 256) total += chunk_of(i).total;
+  const long long share = max(kv8_div(total + p.workers - 1, p.workers), 1LL);
+  const long long begin = blockIdx.x * share, end = min(begin + share, total);
+  if (begin >= end) return;
+  // the sequence that the first unit is of
+  long long at = begin, seq0 = 0;
+  int seq;
+  {
+    long long carry = 0;
+    int from = 0;
+    while (at >= carry + chunk.total) {
+      carry += chunk.total;
+      from += 256;
+      chunk = chunk_of(from);
+    }
+    const long long mine = carry + chunk.before;
+    if (at >= mine && at < mine + chunk.units) {
+      box[4] = from + tid;
+      box[5] = mine;
+    }
+    __syncthreads();
+    seq = __builtin_amdgcn_readfirstlane((int)box[4]);
+    seq0 = box[5];
+  }
+  LatentSeq sq = latent_seq_uniform<kRows>(p, seq);
+  long long units = units_of(sq);
+  const __amdgpu_buffer_rsrc_t rs_ml =
+      __builtin_amdgcn_make_buffer_rsrc(p.part_ml, 0, p.workers * 2 * kRows * 2 * 4, kBufferRsrcWord3);
+  int zero = 0;
+  asm("" : "+v"(zero));  // loads of the table by vector loads, although they are uniform
+
+  while (at < end) {
+    while (at >= seq0 + units) {
+      seq0 += units;
+      ++seq;
+      sq = latent_seq_uniform<kRows>(p, seq);
+      units = units_of(sq);
+    }
+    const long long rel = at - seq0;
+    const int tile = latent_uniform((int)kv8_div(rel, sq.steps));
+    const int t0 = latent_uniform((int)(rel - (long long)tile * sq.steps));
+    const int t1 = latent_uniform((int)min((long long)sq.steps, t0 + (end - at)));
+    const int rows = sq.count * p.h_q, row0 = tile * kRows;
+
+    // B fragments of the rows, and how many tokens each sees
+    v8bf qf[NT][2 * kJ], qrf[NT][kRopeFrags];
+    int hi[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = min(row0 + 16 * n + a, rows - 1), i = row / p.h_q, head = row - i * p.h_q;
+      const uint16_t* src = p.q + (long long)(sq.first + i) * p.q_stride + (long long)head * p.q_head_stride + g * 16;
+      const uint16_t* srcr = p.qr + (long long)(sq.first + i) * p.qr_stride + (long long)head * p.qr_head_stride + g * (P / 4);
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        qf[n][2 * j] = __builtin_bit_cast(v8bf, *(const v4u*)(src + j * 64));
+        qf[n][2 * j + 1] = __builtin_bit_cast(v8bf, *(const v4u*)(src + j * 64 + 8));
+      }
+#pragma unroll
+      for (int j = 0; j < kRopeFrags; ++j) qrf[n][j] = __builtin_bit_cast(v8bf, *(const v4u*)(srcr + j * 8));
+      hi[n] = latent_sees(p, sq, i);
+    }
+    const int all_hi = latent_uniform(latent_sees(p, sq, row0 / p.h_q));
+    const int any_hi = latent_uniform(latent_sees(p, sq, (min(row0 + kRows, rows) - 1) / p.h_q));
+    v4f u[NT][kC];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < kC; ++c) u[n][c] = v4f{0.f, 0.f, 0.f, 0.f};
+      m[n] = -__builtin_huge_valf();
+      l[n] = 0.f;
+    }
+
+    const int last = min(t1, (any_hi + kLatentStep - 1) / kLatentStep);
+    if (t0 < last) {
+      int found;
+      auto look = [&](int step) {
+        found = p.c.table[(size_t)seq * p.c.max_blocks + min((step * kLatentStep + wave * 16) >> p.c.block_log2, p.c.max_blocks - 1) + zero];
+      };
+      // This wave's 16 tokens of a step, as they lie in memory; tokens past the
+      // sequence's end, or of a block that the table does not have, become zeros.
+      auto stage = [&](int step, int page, int buf) {
+        const int token = step * kLatentStep + wave * 16;
+        const int valid = page < 0 ? 0 : min(max(sq.kv - token, 0), 16);
+        const size_t row = ((size_t)max(page, 0) << p.c.block_log2) + (token & (p.c.block - 1));
+        uint8_t* const to = lds + buf * Lds::kBuffer;
+        int lane = tid & 63;
+        asm volatile("" : "+v"(lane));
+        const v4i_rsrc rl = make_rsrc(p.c.latent + row * Lds::kRow, valid * Lds::kRow);
+        constexpr int kPieces = Lds::kRow / 16, kPerDma = 64 / kPieces;  // tokens of one DMA
+#pragma unroll
+        for (int i = 0; i < 16 / kPerDma; ++i) {
+          const int t = i * kPerDma + lane / kPieces, s = lane % kPieces;
+          const int piece = s ^ (F8 ? t : latent_turn(t));
+          lds_dma16(rl, t * Lds::kRow + piece * 16, 0, to + wave * 16 * Lds::kRow + i * 1024);
+        }
+        const v4i_rsrc rr = make_rsrc(p.c.rope + row * P, valid * P * 2);
+#pragma unroll
+        for (int i = 0; i < P / 32; ++i) {
+          const int t = P == 64 ? i * 8 + lane / 8 : lane / 4, s = P == 64 ? lane % 8 : lane % 4;
+          const int piece = P == 64 ? s ^ (t >> 1 & 7) : s ^ (t >> 2 & 3);
+          lds_dma16(rr, t * P * 2 + piece * 16, 0, to + Lds::kLatent + wave * 16 * P * 2 + i * 1024);
+        }
+        if constexpr (F8)
+          lds_dma4(make_rsrc(p.c.scales + row * (L / 128), valid * (L / 128) * 4), lane * 4, 0,
+                   to + Lds::kLatent + Lds::kRope + wave * 256);
+        lds_dma_end(rr, lane);
+      };
+      auto page_of = [&](int step) {
+        const int f = __builtin_amdgcn_readfirstlane(found);
+        const int j = (step * kLatentStep + wave * 16) >> p.c.block_log2;
+        return (j < p.c.max_blocks) & ((unsigned)f < (unsigned)p.c.num_blocks) ? f : -1;
+      };
+      __syncthreads();  // the tile before is done with LDS
+      if (tid < 2) s_flag[tid] = 0;
+      look(t0);
+      int page0 = page_of(t0), page1;
+      look(t0 + 1);
+      page1 = page_of(t0 + 1);
+      look(t0 + 2);
+      stage(t0, page0, 0);
+      stage(t0 + 1, page1, 1);
+      int page2 = page_of(t0 + 2);
+      wait_vmem_all();
+      __syncthreads();
+
+      int s = t0;
+      auto steps = [&](int until, auto form) {
+        constexpr bool MASKED = decltype(form)::value;
+#pragma unroll 1
+        for (; s < until; ++s) {
+          const int buf = latent_uniform(s - t0) & 1;
+          uint8_t* const now = lds + buf * Lds::kBuffer;
+          uint8_t* const wide = F8 ? lds + Lds::kWide : now;
+          // addresses are worked out anew in every step: kept over the loop they
+          // would take the registers that q and u need
+          int here = lane;
+          asm volatile("" : "+v"(here));
+          const int a = here & 15, g = here >> 4;
+          // scores of this wave's 16 tokens
+          v4f x[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x[n] = v4f{0.f, 0.f, 0.f, 0.f};
+          if constexpr (F8) {
+            const uint8_t* const codes = now + (wave * 16 + a) * L;
+            const float* const sc = (const float*)(now + Lds::kLatent + Lds::kRope + wave * 256) + a * (L / 128);
+            uint8_t* const to = wide + (wave * 16 + a) * (2 * L);
+            const int turn = latent_turn(a);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+              const v4u w = *(const v4u*)(codes + (((4 * j + g) ^ a) << 4));
+              const float scale = sc[j / 2];
+              const v4u k0 = latent_widen(w[0], w[1], scale), k1 = latent_widen(w[2], w[3], scale);
+              *(v4u*)(to + (((8 * j + 2 * g) ^ turn) << 4)) = k0;
+              *(v4u*)(to + (((8 * j + 2 * g + 1) ^ turn) << 4)) = k1;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k0), qf[n][2 * j], x[n], 0, 0, 0);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k1), qf[n][2 * j + 1], x[n], 0, 0, 0);
+            }
+          } else {
+            const uint8_t* const from = now + (wave * 16 + a) * (2 * L);
+            const int turn = latent_turn(a);
+            v8bf k[2][2];
+            auto fetch = [&](int j) {
+              k[j & 1][0] = *(const v8bf*)(from + (((8 * j + 2 * g) ^ turn) << 4));
+              k[j & 1][1] = *(const v8bf*)(from + (((8 * j + 2 * g + 1) ^ turn) << 4));
+            };
+            fetch(0);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+              if (j + 1 < kJ) fetch(j + 1);
+              __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j & 1][h], qf[n][2 * j + h], x[n], 0, 0, 0);
+            }
+          }
+          {
+            const uint8_t* const from = now + Lds::kLatent + (wave * 16 + a) * (P * 2);
+#pragma unroll
+            for (int j = 0; j < kRopeFrags; ++j) {
+              const int slot = P == 64 ? (2 * g + j) ^ (a >> 1 & 7) : g ^ (a >> 2 & 3);
+              const v8bf k = *(const v8bf*)(from + slot * 16);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qrf[n][j], x[n], 0, 0, 0);
+            }
+          }
+          // t = log2(e) x; lane: row 16 n + a, tokens 4 g + e of the wave's 16
+          const int token = s * kLatentStep + wave * 16 + g * 4;
+          float t[NT][4];
+          bool moves = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int seen = MASKED ? (page0 < 0 ? 0 : hi[n] - token) : page0 < 0 ? 0 : 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              t[n][e] = x[n][e] * p.scale_log2;
+              if (MASKED || page0 < 0) t[n][e] = e < seen ? t[n][e] : -__builtin_huge_valf();
+              moves |= t[n][e] > m[n];
+            }
+          }
+          uint8_t* const s_rest = Lds::kRestOverRope ? now + Lds::kLatent : lds + Lds::kRest;
+          constexpr int kRestWave = Lds::kRestOverRope ? 16 * P * 2 : kRows * 32;
+          float sum[NT];
+          auto weigh = [&]() {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float ref = m[n] == -__builtin_huge_valf() ? 0.f : m[n];
+              float w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(t[n][e] - ref);
+              sum[n] = (w[0] + w[1]) + (w[2] + w[3]);
+              const v2u packed = {pack2_bf16(w[0], w[1]), pack2_bf16(w[2], w[3])};
+              const int row = 16 * n + a, piece = 2 * wave + (g >> 1);
+              *(v2u*)(lds + Lds::kP + row * 128 + ((piece ^ (row >> 1 & 7)) << 4) + (g & 1) * 8) = packed;
+              if constexpr (MASKED) {
+                const v2u rest = {pack2_bf16(w[0] - __uint_as_float(packed[0] << 16), w[1] - __uint_as_float(packed[0] & 0xFFFF0000u)),
+                                  pack2_bf16(w[2] - __uint_as_float(packed[1] << 16), w[3] - __uint_as_float(packed[1] & 0xFFFF0000u))};
+                *(v2u*)(s_rest + wave * kRestWave + row * 32 + g * 8) = rest;
+              }
+            }
+          };
+          weigh();
+          if (__any(moves) && lane == 0) s_flag[s & 1] = 1;
+          lds_barrier();
+          if (s_flag[s & 1]) {
+            // some row's score passed its reference: all waves move it alike
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float top = fmaxf(fmaxf(t[n][0], t[n][1]), fmaxf(t[n][2], t[n][3]));
+              top = fmaxf(top, __shfl_xor(top, 16, 64));
+              top = fmaxf(top, __shfl_xor(top, 32, 64));
+              if (g == 0) s_max[wave * kRows + 16 * n + a] = top;
+            }
+            lds_barrier();
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float top = s_max[16 * n + a];
+#pragma unroll
+              for (int w = 1; w < 4; ++w) top = fmaxf(top, s_max[w * kRows + 16 * n + a]);
+              if (top > m[n]) {
+                const float ref = top + kLatentLead;
+                const float shrink = __builtin_amdgcn_exp2f(m[n] - ref);
+                l[n] *= shrink;
+#pragma unroll
+                for (int c = 0; c < kC; ++c) u[n][c] *= shrink;
+                m[n] = ref;
+              }
+            }
+            weigh();
+            lds_barrier();
+          }
+          if (tid == 0) s_flag[(s & 1) ^ 1] = 0;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) l[n] += sum[n];
+          // u += c^T p^T, this wave's channels
+          const uint8_t* at_v[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int tk = 8 * g + 4 * h + (a >> 2);  // of 32; + 32 for the second half of the step
+            const int turn = latent_turn(tk & 15);
+            // piece 2 c + (a % 4) / 2 of the row, c = wave kC + i: i comes in by an exclusive or
+            at_v[h] = wide + tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ turn) << 4) + (a & 1) * 8;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            v8bf pf[NT], rest[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const int row = 16 * n + a;
+              pf[n] = *(const v8bf*)(lds + Lds::kP + row * 128 + (((4 * k + g) ^ (row >> 1 & 7)) << 4));
+              if constexpr (MASKED) rest[n] = *(const v8bf*)(s_rest + (2 * k + (g >> 1)) * kRestWave + row * 32 + (g & 1) * 16);
+            }
+            v4u v[2];
+            auto fetch = [&](int c) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t off = (uint32_t)(uintptr_t)(lds_u8*)at_v[h] ^ (c * 32);
+                const v2u w = lds_turned((const uint8_t*)(lds_u8*)(uintptr_t)(off + k * 32 * 2 * L));
+                v[c & 1][2 * h] = w[0];
+                v[c & 1][2 * h + 1] = w[1];
+              }
+            };
+            fetch(0);
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+              if (c + 1 < kC) fetch(c + 1);
+              __builtin_amdgcn_sched_barrier(0);
+              v4u w = v[c & 1];
+              if constexpr (MASKED) {
+                // a token that some rows see and others do not must reach the
+                // former only: what is not finite has made their sums NaN already
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = bf16_finite(w[e]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), rest[n], u[n][c], 0, 0, 0);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), pf[n], u[n][c], 0, 0, 0);
+            }
+          }
+          // the next step has landed, and everybody is done with this one
+          wait_vmem_all();
+          const int next = page_of(s + 3);
+          __syncthreads();
+          look(s + 4);
+          if (s + 2 < last) stage(s + 2, page2, buf);
+          page0 = page1;
+          page1 = page2;
+          page2 = next;
+        }
+      };
+      look(t0 + 3);
+      const int whole = max(min(all_hi / kLatentStep, last), t0);
+      steps(whole, std::false_type{});
+      steps(last, std::true_type{});
+    }
+    // l of the four lane groups and the four waves
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      l[n] += __shfl_xor(l[n], 16, 64);
+      l[n] += __shfl_xor(l[n], 32, 64);
+      if (g == 0) s_max[wave * kRows + 16 * n + a] = l[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float* const at_l = s_max + 16 * n + a;
+      l[n] = (at_l[0] + at_l[kRows]) + (at_l[2 * kRows] + at_l[3 * kRows]);
+    }
+    auto write = [&]() {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = row0 + 16 * n + a;
+        if (row >= rows) continue;
+        const int i = row / p.h_q, head = row - i * p.h_q;
+        const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];  // l == 0: the row sees no token
+        uint16_t* const to = p.out + (long long)(sq.first + i) * p.out_stride + (long long)head * p.out_head_stride + wave * (L / 4) + g * 4;
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          *(v2u*)(to + c * 16) = v2u{pack2_bf16(u[n][c][0] * inv, u[n][c][1] * inv), pack2_bf16(u[n][c][2] * inv, u[n][c][3] * inv)};
+        if (p.lse && wave == 0 && g == 0)
+          p.lse[(size_t)(sq.first + i) * p.h_q + head] = l[n] == 0.f ? -__builtin_huge_valf() : (m[n] + __builtin_amdgcn_logf(l[n])) * 0.69314718055994530942f;
+      }
+    };
+    if (t0 == 0 && t1 == sq.steps) {
+      write();
+    } else {
+      // As in the 8-bit cache's attention: parts pass between XCDs by stores
+      // and loads at agent scope, and the last workgroup of a tile joins them
+      // in workgroup order.
+      constexpr int kTile = kRows * L;  // floats of one part
+      const int slot = (int)blockIdx.x * 2 + (at == begin ? 0 : 1);
+      auto part = [&](int sl) { return __builtin_amdgcn_make_buffer_rsrc(p.part_u + (size_t)sl * kTile, 0, kTile * 4, kBufferRsrcWord3); };
+      {
+        const __amdgpu_buffer_rsrc_t rs = part(slot);
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, u[n][c]), rs, (((wave * kC + c) * NT + n) * 64 + lane) * 16, 0, kCpolSc1);
+        if (wave == 0 && g == 0)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, v2f{m[n], l[n]}), rs_ml, (slot * kRows + 16 * n + a) * 8, 0, kCpolSc1);
+      }
+      const long long s0 = seq0 + (long long)tile * sq.steps;
+      const int w0 = (int)kv8_div(s0, share), w1 = (int)kv8_div(s0 + sq.steps - 1, share);
+      wait_vmem_all();
+      __syncthreads();
+      if (tid == 0)
+        s_last = __hip_atomic_fetch_add(p.arrived + w0, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == w1 - w0;
+      __syncthreads();
+      if (s_last) {
+        if (tid == 0) __hip_atomic_store(p.arrived + w0, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+        const int slot0 = w0 * 2 + (s0 > w0 * share ? 1 : 0);  // only the first can have had another tile before
+        auto slot_of = [&](int w) { return w == w0 ? slot0 : w * 2; };
+        auto load_ml = [&](int w, int n) {
+          const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs_ml, (slot_of(w) * kRows + 16 * n + a) * 8, 0, kCpolSc1);
+          return __builtin_bit_cast(v2f, v);
+        };
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          m[n] = -__builtin_huge_valf();
+          l[n] = 0.f;
+#pragma unroll
+          for (int c = 0; c < kC; ++c) u[n][c] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+        for (int w = w0; w <= w1; ++w)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) m[n] = fmaxf(m[n], load_ml(w, n)[0]);
+        for (int w = w0; w <= w1; ++w) {
+          const __amdgpu_buffer_rsrc_t rs = part(slot_of(w));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const v2f ml = load_ml(w, n);
+            const float f = __builtin_amdgcn_exp2f(ml[0] - (m[n] == -__builtin_huge_valf() ? 0.f : m[n]));
+            l[n] += ml[1] * f;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+              const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, (((wave * kC + c) * NT + n) * 64 + lane) * 16, 0, kCpolSc1);
+              u[n][c] += __builtin_bit_cast(v4f, v) * f;
+            }
+          }
+        }
+        write();
+      }
+    }
+    at += t1 - t0;
+  }
+}
+
+// ---- attention, expanded
+//
+//   x[j] = scale * (qn . kn[j] + qr . r[j]),  o = sum_j e^(x[j] - lse) v[j]
+//
+// kn, v [D] are a head's own, r [D / 2] is shared by all heads.
+
+struct LatentExpandedParams {
+  const uint16_t* q;   // bf16 [total][h][3 D / 2]: key part, rope part
+  const uint16_t* kv;  // bf16 [total_kv][h][2 D]: key part, value
+  const uint16_t* kr;  // bf16 [total_kv][D / 2]
+  long long q_stride, kv_stride, kr_stride;
+  const int32_t* cu;
+  const int32_t* cu_kv;
+  uint16_t* out;  // bf16 [total][h][D]
+  float* lse;     // [total][h] or null
+  float scale_log2;
+  int causal, batch, total, total_kv, most, h;
+};
+
+// How the LDS rows are turned here: the 8 tokens of a transposing read are 4 g
+// .. 4 g + 3 of two lane groups.
+__device__ __forceinline__ int latent_turn8(int t) { return (t & 7) << 1 | (t >> 3 & 1); }
+
+// A workgroup of four waves takes 64 MT queries of one head, 16 MT of them a
+// wave, and walks all tokens that they see.  Keys and values come to LDS as
+// they lie in memory, two steps at a time in flight.  The scores' tiles are
+// dealt so that a lane ends up with p of tokens 32 k + 4 g .. and 32 k + 16 + 4
+// g .., which is what it wants as B operand if the values' transposing reads
+// take the tokens in that order: p stays in registers.
+template <int D, int MT>
+__global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(LatentExpandedParams p) {
+  constexpr int R = D / 2, kRows = 64 * MT, kRow = 4 * D, kPieces = kRow / 16;  // bytes and 16-byte pieces of a token's row
+  constexpr int kBuffer = kLatentStep * (kRow + 2 * R), kN = D / 32, kR = R / 32;
+  extern __shared__ __align__(1024) uint8_t lds[];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
+  const int head = blockIdx.x, seq = blockIdx.y;
+  int first, count, first_kv, kv;
+  const int all = latent_uniform(kv8_rows(p.cu, seq, p.total, p.most, &first, &count));
+  kv8_rows(p.cu_kv, seq, p.total_kv, p.total_kv, &first_kv, &kv);
+  first = latent_uniform(first);
+  count = latent_uniform(count);
+  first_kv = latent_uniform(first_kv);
+  kv = latent_uniform(kv);
+  // every sequence's last tile, which sees the most tokens, starts first
+  const int row0 = ((count + kRows - 1) / kRows - 1 - (int)blockIdx.z) * kRows;
+  if (row0 < 0) return;
+  const int pos = kv - all;
+  auto sees = [&](int i) { return p.causal ? max(min(pos + i + 1, kv), 0) : kv; };
+  const int wave0 = row0 + wave * 16 * MT;
+  const int any_hi = sees(min(row0 + kRows, count) - 1);
+  const int wave_hi = wave0 < count ? sees(min(wave0 + 16 * MT, count) - 1) : 0;
+
+  v8bf qf[MT][kN + kR];
+  int hi[MT];
+#pragma unroll
+  for (int n = 0; n < MT; ++n) {
+    const int i = min(wave0 + n * 16 + a, count - 1);
+    const uint16_t* src = p.q + (long long)(first + i) * p.q_stride + (long long)head * (D + R) + g * 8;
+#pragma unroll
+    for (int k = 0; k < kN + kR; ++k) qf[n][k] = __builtin_bit_cast(v8bf, *(const v4u*)(src + k * 32));
+    hi[n] = sees(i);
+  }
+  v4f u[MT][D / 16];
+  float m[MT], l[MT];
+#pragma unroll
+  for (int n = 0; n < MT; ++n) {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) u[n][c] = v4f{0.f, 0.f, 0.f, 0.f};
+    m[n] = -__builtin_huge_valf();
+    l[n] = 0.f;
+  }
+
+  // This wave's 16 tokens of a step.
+  auto stage = [&](int step, int buf) {
+    const int token = step * kLatentStep + wave * 16;
+    const int valid = min(max(kv - token, 0), 16);
+    const int at = first_kv + min(token, kv);
+    uint8_t* const to = lds + buf * kBuffer;
+    const uint32_t pitch = (uint32_t)p.kv_stride * 2, pitch_r = (uint32_t)p.kr_stride * 2;
+    const v4i_rsrc rk = make_rsrc(p.kv + (long long)at * p.kv_stride + (long long)head * (2 * D), valid ? (valid - 1) * pitch + kRow : 0);
+    constexpr int kPerDma = 64 / kPieces;
+#pragma unroll
+    for (int i = 0; i < 16 / kPerDma; ++i) {
+      const int t = i * kPerDma + lane / kPieces, piece = (lane % kPieces) ^ latent_turn8(t);
+      lds_dma16(rk, t * pitch + piece * 16, 0, to + wave * 16 * kRow + i * 1024);
+    }
+    const v4i_rsrc rr = make_rsrc(p.kr + (long long)at * p.kr_stride, valid ? (valid - 1) * pitch_r + 2 * R : 0);
+#pragma unroll
+    for (int i = 0; i < R / 32; ++i) {
+      const int t = R == 64 ? i * 8 + lane / 8 : lane / 4;
+      const int piece = R == 64 ? lane % 8 ^ (t >> 1 & 7) : lane % 4 ^ (t >> 2 & 3);
+      lds_dma16(rr, t * pitch_r + piece * 16, 0, to + kLatentStep * kRow + wave * 16 * R * 2 + i * 1024);
+    }
+    lds_dma_end(rr, lane);
+  };
+  constexpr int kEvents = (16 / (64 / kPieces) + R / 32) * kVmPerDma + 1;  // of one step, as vmcnt sees them
+
+  const int last = (any_hi + kLatentStep - 1) / kLatentStep;
+  if (last > 0) {
+    stage(0, 0);
+    stage(1, 1);  // past the last step: zeros
+    int s = 0;
+    auto steps = [&](int until, auto form) {
+      constexpr bool MASKED = decltype(form)::value;
+#pragma unroll 1
+      for (; s < until; ++s) {
+        const int base = s * kLatentStep, buf = s & 1;
+        const uint8_t* const now = lds + buf * kBuffer;
+        wait_vmem<kEvents>();  // this step has landed, the next may be under way
+        block_barrier();
+        if (base < wave_hi) {
+          float t[MT][16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v4f x[MT];
+#pragma unroll
+            for (int n = 0; n < MT; ++n) x[n] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kN + kR; ++k) {
+              const int row = 16 * j + a;
+              v8bf key;
+              if (k < kN) {
+                key = *(const v8bf*)(now + row * kRow + (((4 * k + g) ^ latent_turn8(a)) << 4));
+              } else {
+                const int piece = 4 * (k - kN) + g;
+                key = *(const v8bf*)(now + kLatentStep * kRow + row * 2 * R + ((R == 64 ? piece ^ (a >> 1 & 7) : piece ^ (a >> 2 & 3)) << 4));
+              }
+#pragma unroll
+              for (int n = 0; n < MT; ++n) x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key, qf[n][k], x[n], 0, 0, 0);
+            }
+#pragma unroll
+            for (int n = 0; n < MT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) t[n][4 * j + e] = x[n][e];
+          }
+          v4u pw[MT][2], rest[MT][2];
+          uint32_t seen[MT];
+          const float by = MASKED ? 1.f : p.scale_log2;  // what is masked is scaled before it is
+#pragma unroll
+          for (int n = 0; n < MT; ++n) {
+            // element 4 j + e: token 16 j + 4 g + e
+            if constexpr (MASKED) {
+              seen[n] = 0;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const bool is = base + 16 * (i / 4) + 4 * g + i % 4 < hi[n];
+                t[n][i] = is ? t[n][i] * p.scale_log2 : -__builtin_huge_valf();
+                seen[n] |= is ? 1u << i : 0u;
+              }
+            }
+            float top = t[n][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) top = fmaxf(top, t[n][i]);
+            top *= by;
+            if (__any(top > m[n])) {
+              top = fmaxf(top, __shfl_xor(top, 16, 64));
+              top = fmaxf(top, __shfl_xor(top, 32, 64));
+              if (top > m[n]) {
+                const float ref = top + kLatentLead, shrink = __builtin_amdgcn_exp2f(m[n] - ref);
+                l[n] *= shrink;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) u[n][c] *= shrink;
+                m[n] = ref;
+              }
+            }
+            const float ref = m[n] == -__builtin_huge_valf() ? 0.f : m[n];
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float p0 = __builtin_amdgcn_exp2f(t[n][i] * by - ref), p1 = __builtin_amdgcn_exp2f(t[n][i + 1] * by - ref);
+              sum[0] += p0;
+              sum[1] += p1;
+              const uint32_t both = pack2_bf16(p0, p1);
+              pw[n][i / 8][i / 2 & 3] = both;
+              if constexpr (MASKED)
+                rest[n][i / 8][i / 2 & 3] = pack2_bf16(p0 - __uint_as_float(both << 16), p1 - __uint_as_float(both & 0xFFFF0000u));
+            }
+            l[n] += sum[0] + sum[1];
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              v4u v;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int tk = 32 * k + 16 * h + 4 * g + (a >> 2);
+                const int piece = D / 8 + 2 * c + (a >> 1 & 1);
+                const v2u w = lds_turned(now + tk * kRow + ((piece ^ latent_turn8(tk & 15)) << 4) + (a & 1) * 8);
+                v[2 * h] = w[0];
+                v[2 * h + 1] = w[1];
+              }
+              if constexpr (MASKED) {
+                // What is not finite must reach the rows that see it only: it is
+                // zeroed, and a second product finds the rows that see some of it.
+                v4u ind, fin;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  fin[e] = bf16_finite(v[e]);
+                  const uint32_t lo = (v[e] & 0x7F80u) == 0x7F80u, up = (v[e] & 0x7F800000u) == 0x7F800000u;
+                  ind[e] = lo * 0x3F80u | up * 0x3F800000u;
+                }
+                if (__any((ind[0] | ind[1] | ind[2] | ind[3]) != 0)) {
+#pragma unroll
+                  for (int n = 0; n < MT; ++n) {
+                    v4u sw;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      sw[e] = (seen[n] >> (8 * k + 2 * e) & 1u) * 0x3F80u | (seen[n] >> (8 * k + 2 * e + 1) & 1u) * 0x3F800000u;
+                    const v4f cnt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, ind), __builtin_bit_cast(v8bf, sw),
+                                                                           v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) u[n][c][e] = cnt[e] > 0.f ? __builtin_nanf("") : u[n][c][e];
+                  }
+                }
+                v = fin;
+#pragma unroll
+                for (int n = 0; n < MT; ++n)
+                  u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, v), __builtin_bit_cast(v8bf, rest[n][k]), u[n][c], 0, 0, 0);
+              }
+#pragma unroll
+              for (int n = 0; n < MT; ++n)
+                u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, v), __builtin_bit_cast(v8bf, pw[n][k]), u[n][c], 0, 0, 0);
+            }
+          }
+        }
+        block_barrier();  // all are done with this buffer: their reads have returned, as products waited for them
+        stage(s + 2, buf);
+      }
+    };
+    // steps that every row of the workgroup sees wholly, and those with masks
+    steps(min(sees(row0) / kLatentStep, last), std::false_type{});
+    steps(last, std::true_type{});
+    wait_vmem_all();  // no LDS DMA may be in flight past this point
+  }
+#pragma unroll
+  for (int n = 0; n < MT; ++n) {
+    l[n] += __shfl_xor(l[n], 16, 64);
+    l[n] += __shfl_xor(l[n], 32, 64);
+    const int i = wave0 + n * 16 + a;
+    if (i >= count) continue;
+    const size_t row = (size_t)(first + i) * p.h + head;
+    const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];  // l == 0: the row sees no token
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+      *(v2u*)(p.out + row * D + c * 16 + g * 4) = v2u{pack2_bf16(u[n][c][0] * inv, u[n][c][1] * inv), pack2_bf16(u[n][c][2] * inv, u[n][c][3] * inv)};
+    if (p.lse && g == 0) p.lse[row] = l[n] == 0.f ? -__builtin_huge_valf() : (m[n] + __builtin_amdgcn_logf(l[n])) * 0.69314718055994530942f;
+  }
+}
+
+}  // namespace dg

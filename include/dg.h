@@ -41,7 +41,7 @@
  *   such a growth is refused with DG_ERR_WORKSPACE and nothing is enqueued:
  *   size the workspace first with dg_reserve_workspace(bytes, stream), bytes
  *   from dg_dense_workspace_size (dg_bf16_w4_workspace_size,
- *   dg_kv8_attention_workspace_size).  A captured call keeps using the workspace
+ *   dg_kv8_attention_workspace_size, dg_latent_attention_workspace_size).  A captured call keeps using the workspace
  *   its capture stream had; a replay must not overlap in time with other
  *   split-K work on that same workspace (replaying on the capture stream, or
  *   on any stream ordered with it, is safe).  dg_fp8_gemm_nt_noalloc uses a
@@ -449,6 +449,117 @@ int dg_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes
 
 /* Bytes of the stream's workspace that dg_kv8_attention takes on the current device. */
 int dg_kv8_attention_workspace_size(int d, size_t* bytes);
+
+/*
+ * ---- Latent attention: keys and values from one shared latent vector a token
+ *
+ * A token is a latent c of `latent` values (512 or 256) and a rope part r of
+ * P = latent / 8 values, shared by all heads.  Absorbed, a head's key is (c, r)
+ * and its value c; expanded, an up-projection of c gives each head a key part
+ * and a value of D = latent / 4 values each, and its key is (key part, r).
+ *
+ * A paged cache holds, for num_blocks blocks of `block` tokens (16, 32, 64 or 128):
+ *
+ *   latent [num_blocks][block][latent]       bf16 if scales is NULL, else e4m3
+ *   rope   [num_blocks][block][P]            bf16
+ *   scales [num_blocks][block][latent / 128] fp32 powers of two, or NULL
+ *
+ * block_table, lengths, running sums and packed rows are those of the 8-bit
+ * key/value cache above: tokens whose entry lies outside [0, num_blocks), or
+ * past max_blocks, are neither written nor seen; rows outside [0, total) and
+ * rows past the given longest sequence are ignored, and what would hold their
+ * results keeps what it held.  Cache arrays may pass 4 GiB; an array without
+ * elements may be NULL.
+ *
+ * dg_latent_append takes the latent and rope parts of new tokens, bf16 rows
+ * with *_stride elements (a multiple of 8) from token to token, so slices of
+ * one projection's output serve as they are.  Token i of sequence s stands at
+ * position ctx_lens[s] + i.  Into its place go
+ *
+ *   y = norm * c / sqrt(mean(c^2) + eps), or c if norm is NULL, in fp32: rounded
+ *       to bf16, or, for each 128 values, with s the smallest power of two with
+ *       amax <= 448 s (amax floored at 1e-4), e4m3(y / s), nearest even
+ *   r turned by its position: (a, b) -> (a cos - b sin, a sin + b cos) in fp32,
+ *       rounded to bf16, for pairs (r[2 i], r[2 i + 1]) if interleaved, else
+ *       (r[i], r[i + P / 2]); cos and sin are angles[pos][i], angles[pos][P / 2 + i]
+ *
+ * with norm bf16 [latent] and angles fp32 [positions][P].  If q is not NULL,
+ * the rope parts of the h_q query heads of each token (q_stride elements from
+ * token to token, q_head_stride from head to head) are turned alike and
+ * written to q_out, which may be q itself.  Tokens at positions outside [0,
+ * positions) are ignored.  amax counts finite values; infinities saturate, NaN
+ * is stored as NaN (with a norm either makes the whole token NaN).
+ */
+int dg_latent_append(const uint16_t* latent, int64_t latent_stride, const uint16_t* rope, int64_t rope_stride,
+                     void* cache_latent, uint16_t* cache_rope, float* cache_scales, const int32_t* block_table,
+                     const int32_t* ctx_lens, const int32_t* cu_new, const float* angles, int positions,
+                     const uint16_t* norm, float eps, const uint16_t* q, int64_t q_stride, int64_t q_head_stride,
+                     uint16_t* q_out, int64_t q_out_stride, int64_t q_out_head_stride, int interleaved, int batch,
+                     int total, int max_new, int h_q, int latent_dim, int block, int num_blocks, int max_blocks,
+                     dg_stream_t stream);
+
+/*
+ * Cached tokens as packed bf16 rows, latent [total][latent] and rope [total][P]:
+ * row cu[s] + i is token starts[s] + i of sequence s (starts NULL: from 0 on).
+ * e4m3 latents come out as the values they stand for.  Rows of tokens that the
+ * table has no block for keep what they held.
+ */
+int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const float* cache_scales,
+                     const int32_t* block_table, const int32_t* starts, const int32_t* cu, uint16_t* latent,
+                     uint16_t* rope, int batch, int total, int latent_dim, int block, int num_blocks, int max_blocks,
+                     dg_stream_t stream);
+
+/*
+ * Absorbed attention of packed queries over the cache: for query i of the n_i of
+ * sequence s, standing at position kv_lens[s] - n_i + i (its own token is in the
+ * cache already), and each of the h_q heads,
+ *
+ *   x[j] = scale * (q . c[j] + q_rope . r[j]),  out = sum_j softmax(x)[j] c[j],  lse = log sum_j e^x[j]
+ *
+ * with scale >= 0, over the tokens j up to its own position if causal, all
+ * kv_lens[s] otherwise.  A row that sees no token gets out = 0 and lse = -inf.
+ * q [total][h_q][latent], q_rope [total][h_q][P] and out [total][h_q][latent]
+ * are bf16 with any strides (multiples of 8, 4 for out) from token to token and head to head;
+ * lse is fp32 [total][h_q] or NULL; max_q is the most queries of one sequence.
+ * A token whose latent or rope part is not finite makes the rows that see it
+ * not finite and no others; what the cache holds past kv_lens[s] reaches none.
+ * Scores, the softmax's running reference and sums and the output's
+ * accumulator are fp32; for the second product each probability is rounded to
+ * bf16, in steps of 64 tokens that some row does not see wholly to two bf16
+ * pieces.  The same call gives the same bits.  Needs
+ * dg_latent_attention_workspace_size bytes of the stream's workspace (reserve
+ * it before capturing); the work is shared out on the device from the lengths
+ * it finds there.
+ */
+int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stride, const uint16_t* q_rope,
+                        int64_t q_rope_stride, int64_t q_rope_head_stride, const void* cache_latent,
+                        const uint16_t* cache_rope, const float* cache_scales, const int32_t* block_table,
+                        const int32_t* kv_lens, const int32_t* cu_q, uint16_t* out, int64_t out_stride,
+                        int64_t out_head_stride, float* lse, float scale, int causal, int batch, int total, int max_q,
+                        int h_q, int latent_dim, int block, int num_blocks, int max_blocks, dg_stream_t stream);
+
+/* Bytes of the stream's workspace that dg_latent_attention takes on the current device. */
+int dg_latent_attention_workspace_size(int latent_dim, int max_q, int h_q, size_t* bytes);
+
+/*
+ * Expanded attention of packed prompts: for query i of the n_i of sequence s,
+ * which has m_i tokens, standing at position m_i - n_i + i, and each head,
+ *
+ *   x[j] = scale * (q[0..D) . k[j] + q[D..D + P) . r[j]),  out = sum_j softmax(x)[j] v[j]
+ *
+ * q bf16 [total][heads][D + P] and kv bf16 [total_kv][heads][2 D] (key part,
+ * then value; an up-projection's output as it stands), k_rope bf16 [total_kv][P],
+ * with *_stride elements (a multiple of 8, less than 2^26) from token to token;
+ * cu_q, cu_kv int32 [batch + 1] running sums; out bf16 [total][heads][D], lse
+ * fp32 [total][heads] or NULL; head_dim D is 128 or 64, P = D / 2.  Masks, rows
+ * that see nothing, precision and determinism as in dg_latent_attention; a
+ * value that is not finite makes that dimension of the rows that see it not
+ * finite and nothing else.  Needs no workspace.
+ */
+int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint16_t* kv, int64_t kv_stride,
+                                 const uint16_t* k_rope, int64_t k_rope_stride, const int32_t* cu_q,
+                                 const int32_t* cu_kv, uint16_t* out, float* lse, float scale, int causal, int batch,
+                                 int total, int total_kv, int max_q, int heads, int head_dim, dg_stream_t stream);
 
 /*
  * Size the split-K workspace of `stream` on the current device to hold at

@@ -30,6 +30,7 @@ gemm   dense, contiguous-grouped, masked-grouped and K-grouped reference GEMMs i
        the BF16 and FP4 NT GEMMs; FC1 + SwiGLU on the masked and contiguous layouts
 w4     4-bit weights with group scales: quantiser, inverse, product
 kv8    the paged 8-bit key/value cache: append and attention
+latent latent attention, absorbed and expanded, its cache and the rotation of rope parts
 check  the element-wise acceptance rule
 """
 
@@ -54,4 +55,4 @@ from .gemm import (  # noqa: F401
 )
 from .check import tolerance_check, bf16_bits_to_float, bf16_round  # noqa: F401
 from .w4 import dequantize_w4, quantize_w4, w4_gemm_ref  # noqa: F401
-from . import kv8  # noqa: F401
+from . import kv8, latent  # noqa: F401
