@@ -1118,6 +1118,9 @@ int latent_row_tiles(int max_q, int h_q) {
   return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
 size_t latent_part_floats(int workers, int tiles, int latent) { return (size_t)workers * 2 * 16 * tiles * (latent + 2); }
+size_t latent_part_bytes(int workers, int tiles, int latent) {
+  return latent_part_floats(workers, tiles, latent) * sizeof(float) + workers * sizeof(dg::LatentCut);
+}
 
 int check_latent_rows(int max_q, int h_q) {
   if (h_q < 1 || h_q > 32767) return fail(DG_ERR_INVALID_ARGUMENT, "h_q must be 1..32767 (got %d)", h_q);
@@ -1129,11 +1132,13 @@ int check_latent_rows(int max_q, int h_q) {
 struct LatentKernel {
   const void* fn;
   int smem;
+  const void* join;
 };
 
 template <int L, bool F8, int NT>
 LatentKernel latent_attn() {
-  return {reinterpret_cast<const void*>(&dg::latent_attn_kernel<L, F8, NT>), dg::LatentLds<L, F8, NT>::kBytes};
+  return {reinterpret_cast<const void*>(&dg::latent_attn_kernel<L, F8, NT>), dg::LatentLds<L, F8, NT>::kBytes,
+          reinterpret_cast<const void*>(&dg::latent_join_kernel<L, NT>)};
 }
 template <int L, bool F8>
 LatentKernel latent_attn(int tiles) {
@@ -1146,7 +1151,7 @@ LatentKernel latent_attn(int latent, bool f8, int tiles) {
 
 template <int D, int MT>
 LatentKernel latent_expanded() {
-  return {reinterpret_cast<const void*>(&dg::latent_expanded_kernel<D, MT>), 2 * dg::kLatentStep * (4 * D + D)};
+  return {reinterpret_cast<const void*>(&dg::latent_expanded_kernel<D, MT>), 2 * dg::kLatentStep * (4 * D + D), nullptr};
 }
 
 std::once_flag g_latent_once;
@@ -1900,7 +1905,7 @@ int dg_latent_attention_workspace_size(int latent_dim, int max_q, int h_q, size_
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
-  *bytes = latent_part_floats(info->cus, latent_row_tiles(max_q, h_q), latent_dim) * sizeof(float);
+  *bytes = latent_part_bytes(info->cus, latent_row_tiles(max_q, h_q), latent_dim);
   return ok();
 }
 
@@ -1951,13 +1956,13 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   const int tiles = latent_row_tiles(max_q, h_q);
   const LatentKernel k = latent_attn(latent_dim, cache_scales != nullptr, tiles);
   char* base = nullptr;
-  if (int s = ensure_workspace(dev, (hipStream_t)stream,
-                               latent_part_floats(p.workers, tiles, latent_dim) * sizeof(float), &base)) return s;
-  p.arrived = (int*)base;
+  if (int s = ensure_workspace(dev, (hipStream_t)stream, latent_part_bytes(p.workers, tiles, latent_dim), &base)) return s;
   p.part_u = (float*)(base + kWsHeader);
   p.part_ml = p.part_u + (size_t)p.workers * 2 * 16 * tiles * latent_dim;
+  p.cut = (dg::LatentCut*)(p.part_ml + (size_t)p.workers * 2 * 16 * tiles * 2);
   void* args[] = {&p};
-  return launch_plain("latent_attention", k.fn, dim3(p.workers), 256, args, stream, k.smem);
+  if (int s = launch_plain("latent_attention", k.fn, dim3(p.workers), 256, args, stream, k.smem)) return s;
+  return launch_plain("latent_join", k.join, dim3(p.workers, 16), 256, args, stream);
 }
 
 int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint16_t* kv, int64_t kv_stride,

@@ -251,6 +251,12 @@ __global__ __launch_bounds__(256) void latent_gather_kernel(LatentGatherParams p
 // was set and moves when some t passes it: p never passes 1, and few steps pay
 // for scaling u.
 
+// A tile that a workgroup began and did not finish: how many parts it has, and
+// where the first lies.
+struct LatentCut {
+  int seq, tile, parts, slot;
+};
+
 struct LatentAttnParams {
   const uint16_t* q;   // bf16 latent parts of the queries
   const uint16_t* qr;  // and their rope parts
@@ -265,8 +271,8 @@ struct LatentAttnParams {
   int causal, batch, total, most, h_q;
   // split work: workgroup w computes its share of the units below
   float* part_u;   // [workers][2][rows of a tile][L], as the lanes hold it
-  float* part_ml;  // [workers][2][rows of a tile][2]
-  int* arrived;    // [workers] counters, zero between calls
+  float* part_ml;  // [workers][2][rows of a tile][2]: m and l
+  LatentCut* cut;  // [workers]
   int workers;
 };
 
@@ -312,6 +318,27 @@ __device__ __forceinline__ int latent_sees(const LatentAttnParams& p, const Late
   return p.causal ? max(min(s.pos + i + 1, s.kv), 0) : s.kv;
 }
 
+// Consecutive shares go to one XCD, so that the tiles of one sequence find its
+// tokens in that XCD's L2.
+__device__ __forceinline__ int latent_worker(int block, int workers) {
+  return workers % kNumXcd == 0 ? block % kNumXcd * (workers / kNumXcd) + block / kNumXcd : block;
+}
+
+// Channels col + 16 c .. + 3 of one row: u / l; l == 0: the row sees no token.
+template <int L, int C>
+__device__ __forceinline__ void latent_write(const LatentAttnParams& p, const LatentSeq& sq, int row, int col,
+                                             const v4f (&u)[C], float m, float l, bool with_lse) {
+  const int i = row / p.h_q, head = row - i * p.h_q;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* const to = p.out + (long long)(sq.first + i) * p.out_stride + (long long)head * p.out_head_stride + col;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    *(v2u*)(to + c * 16) = v2u{pack2_bf16(u[c][0] * inv, u[c][1] * inv), pack2_bf16(u[c][2] * inv, u[c][3] * inv)};
+  if (p.lse && with_lse)
+    p.lse[(size_t)(sq.first + i) * p.h_q + head] =
+        l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+}
+
 // The halves of a dword of two bf16 that are finite; the others become zero.
 __device__ __forceinline__ uint32_t bf16_finite(uint32_t w) {
   w = (w & 0x7F80u) == 0x7F80u ? w & 0xFFFF0000u : w;
@@ -355,32 +382,39 @@ struct LatentLds {
   static constexpr int kBuffer = kLatent + kRope + kScales;   // two of them
   static constexpr int kWide = 2 * kBuffer;                   // e4m3: the step's latents in bf16
   static constexpr int kP = kWide + (F8 ? kLatentStep * L * 2 : 0);  // p [rows][64], bf16
-  // the second halves of p: [wave][rows][16]; for L = 512 each wave puts its
-  // own over its rope parts of the step, which nobody reads any more
+  // the second pieces of p: [4][rows][16]; for L = 512 they go over the step's
+  // rope parts once all waves are done with those
   static constexpr bool kRestOverRope = 16 * P * 2 >= 16 * NT * 32;
   static constexpr int kRest = kP + 16 * NT * 128;
   static constexpr int kMax = kRest + (kRestOverRope ? 0 : 4 * 16 * NT * 32);  // [4][rows] floats
-  static constexpr int kFlags = kMax + 4 * 16 * NT * 4;
-  static constexpr int kBytes = kFlags + 64;
+  static constexpr int kFlags = kMax + 4 * 16 * NT * 4;       // [2] a reference moves, [2][4] a group's block is there
+  static constexpr int kBox = kFlags + 64;
+  static constexpr int kBytes = kBox + 64;
 };
 
-// A workgroup of four waves takes an equal share of all (sequence, tile of 16
-// NT rows, 64-token step) units, in that order.  In a step wave w brings
-// tokens 16 w .. 16 w + 15 to LDS and computes all rows' scores with them; p
-// passes through LDS, and wave w adds up channels w L / 4 .. of every row.  So
-// each token's latent is fetched once, read from LDS once for the first product
-// and once for the second, and q and u stay in registers.
+// A unit of work is a 64-token step of a tile of 16 NT rows; a workgroup of
+// four waves takes an equal share of all units, in the order (sequence, tile,
+// step).  In a step wave w brings tokens 16 w .. 16 w + 15 to LDS, two steps
+// ahead of their use.  For the scores the waves share out the tokens, and for
+// more than 32 rows (RW = 2) tokens and rows, each half of both, as q for all
+// rows would not fit in the registers beside u.  p passes through LDS, and
+// wave w adds up channels w L / 4 .. of every row.  So a token's latent is
+// fetched once for all heads, and q and u never leave the registers.
+//
+// Tiles that a share's end cuts leave their parts in the workspace, and
+// latent_join_kernel adds them up.
 template <int L, bool F8, int NT>
 __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p) {
   using Lds = LatentLds<L, F8, NT>;
   constexpr int P = L / 8, kRows = 16 * NT, kJ = L / 64, kC = L / 64;  // kC column tiles of 16 a wave
-  constexpr int kRopeFrags = P / 32;
+  constexpr int kRopeFrags = P / 32, RW = NT > 2 ? 2 : 1, kN = NT / RW;  // kN row tiles and RW token tiles of a wave's scores
   extern __shared__ __align__(1024) uint8_t lds[];  // all of it: a row's place has to be a multiple of its size
-  long long* const box = (long long*)(lds + Lds::kFlags + 16);
-  int& s_last = *(int*)(lds + Lds::kFlags + 8);
   float* const s_max = (float*)(lds + Lds::kMax);
   int* const s_flag = (int*)(lds + Lds::kFlags);
+  int* const s_there = s_flag + 2;
+  long long* const box = (long long*)(lds + Lds::kBox);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
+  const int rw = wave / (4 / RW), tw = wave % (4 / RW);
 
   // rows of sequences without tokens
   for (int i = blockIdx.x; i < p.batch; i += p.workers) {
@@ -392,6 +426,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
       if (p.lse && tid % (L / 8) == 0) p.lse[(size_t)token * p.h_q + head] = -__builtin_huge_valf();
     }
   }
+  if (tid == 0) p.cut[latent_worker(blockIdx.x, p.workers)] = LatentCut{0, 0, 0, 0};
   auto units_of = [&](const LatentSeq& s) { return (long long)s.tiles * s.steps; };
   auto chunk_of = [&](int first) {
     const int i = first + tid;
@@ -404,7 +439,8 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
   long long total = chunk.total;
   for (int i = 256; i < p.batch; i += 256) total += chunk_of(i).total;
   const long long share = max(kv8_div(total + p.workers - 1, p.workers), 1LL);
-  const long long begin = blockIdx.x * share, end = min(begin + share, total);
+  const int worker = latent_worker(blockIdx.x, p.workers);
+  const long long begin = worker * share, end = min(begin + share, total);
   if (begin >= end) return;
   // the sequence that the first unit is of
   long long at = begin, seq0 = 0;
@@ -428,8 +464,6 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
   }
   LatentSeq sq = latent_seq_uniform<kRows>(p, seq);
   long long units = units_of(sq);
-  const __amdgpu_buffer_rsrc_t rs_ml =
-      __builtin_amdgcn_make_buffer_rsrc(p.part_ml, 0, p.workers * 2 * kRows * 2 * 4, kBufferRsrcWord3);
   int zero = 0;
   asm("" : "+v"(zero));  // loads of the table by vector loads, although they are uniform
 
@@ -446,12 +480,12 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
     const int t1 = latent_uniform((int)min((long long)sq.steps, t0 + (end - at)));
     const int rows = sq.count * p.h_q, row0 = tile * kRows;
 
-    // B fragments of the rows, and how many tokens each sees
-    v8bf qf[NT][2 * kJ], qrf[NT][kRopeFrags];
-    int hi[NT];
+    // B fragments of this wave's rows, and how many tokens each sees
+    v8bf qf[kN][2 * kJ], qrf[kN][kRopeFrags];
+    int hi[kN];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = min(row0 + 16 * n + a, rows - 1), i = row / p.h_q, head = row - i * p.h_q;
+    for (int n = 0; n < kN; ++n) {
+      const int row = min(row0 + 16 * (rw * kN + n) + a, rows - 1), i = row / p.h_q, head = row - i * p.h_q;
       const uint16_t* src = p.q + (long long)(sq.first + i) * p.q_stride + (long long)head * p.q_head_stride + g * 16;
       const uint16_t* srcr = p.qr + (long long)(sq.first + i) * p.qr_stride + (long long)head * p.qr_head_stride + g * (P / 4);
 #pragma unroll
@@ -465,21 +499,30 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
     }
     const int all_hi = latent_uniform(latent_sees(p, sq, row0 / p.h_q));
     const int any_hi = latent_uniform(latent_sees(p, sq, (min(row0 + kRows, rows) - 1) / p.h_q));
+    // every row's u in this wave's channels, and reference; l of this wave's rows and tokens
     v4f u[NT][kC];
-    float m[NT], l[NT];
+    float m[NT], l[kN];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int c = 0; c < kC; ++c) u[n][c] = v4f{0.f, 0.f, 0.f, 0.f};
       m[n] = -__builtin_huge_valf();
-      l[n] = 0.f;
     }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) l[n] = 0.f;
+    // the n-th of this wave's row tiles, of what is kept for all
+    auto of_wave = [&](const float (&v)[NT], int n) { return RW == 1 || rw == 0 ? v[n] : v[(kN + n) % NT]; };
 
     const int last = min(t1, (any_hi + kLatentStep - 1) / kLatentStep);
     if (t0 < last) {
       int found;
       auto look = [&](int step) {
         found = p.c.table[(size_t)seq * p.c.max_blocks + min((step * kLatentStep + wave * 16) >> p.c.block_log2, p.c.max_blocks - 1) + zero];
+      };
+      auto page_of = [&](int step) {
+        const int f = __builtin_amdgcn_readfirstlane(found);
+        const int j = (step * kLatentStep + wave * 16) >> p.c.block_log2;
+        return (j < p.c.max_blocks) & ((unsigned)f < (unsigned)p.c.num_blocks) ? f : -1;
       };
       // This wave's 16 tokens of a step, as they lie in memory; tokens past the
       // sequence's end, or of a block that the table does not have, become zeros.
@@ -509,24 +552,21 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           lds_dma4(make_rsrc(p.c.scales + row * (L / 128), valid * (L / 128) * 4), lane * 4, 0,
                    to + Lds::kLatent + Lds::kRope + wave * 256);
         lds_dma_end(rr, lane);
-      };
-      auto page_of = [&](int step) {
-        const int f = __builtin_amdgcn_readfirstlane(found);
-        const int j = (step * kLatentStep + wave * 16) >> p.c.block_log2;
-        return (j < p.c.max_blocks) & ((unsigned)f < (unsigned)p.c.num_blocks) ? f : -1;
+        if (lane == 0) s_there[buf * 4 + wave] = page >= 0;
       };
       __syncthreads();  // the tile before is done with LDS
       if (tid < 2) s_flag[tid] = 0;
       look(t0);
-      int page0 = page_of(t0), page1;
+      const int page0 = page_of(t0);
       look(t0 + 1);
-      page1 = page_of(t0 + 1);
-      look(t0 + 2);
       stage(t0, page0, 0);
+      const int page1 = page_of(t0 + 1);
+      look(t0 + 2);
       stage(t0 + 1, page1, 1);
       int page2 = page_of(t0 + 2);
       wait_vmem_all();
       __syncthreads();
+      look(t0 + 3);
 
       int s = t0;
       auto steps = [&](int until, auto form) {
@@ -541,36 +581,57 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           int here = lane;
           asm volatile("" : "+v"(here));
           const int a = here & 15, g = here >> 4;
-          // scores of this wave's 16 tokens
-          v4f x[NT];
+          // scores: tokens 16 (tw RW + r) + a of the step with rows 16 (rw kN + n) + a
+          v4f x[RW][kN];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) x[n] = v4f{0.f, 0.f, 0.f, 0.f};
+          for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int n = 0; n < kN; ++n) x[r][n] = v4f{0.f, 0.f, 0.f, 0.f};
+          const int turn = F8 ? a : latent_turn(a);
           if constexpr (F8) {
-            const uint8_t* const codes = now + (wave * 16 + a) * L;
-            const float* const sc = (const float*)(now + Lds::kLatent + Lds::kRope + wave * 256) + a * (L / 128);
-            uint8_t* const to = wide + (wave * 16 + a) * (2 * L);
-            const int turn = latent_turn(a);
+            v4u w[2][RW];
+            float scale[RW][L / 128];
+            auto fetch = [&](int j) {
+#pragma unroll
+              for (int r = 0; r < RW; ++r) w[j & 1][r] = *(const v4u*)(now + (16 * (tw * RW + r) + a) * L + (((4 * j + g) ^ turn) << 4));
+            };
+#pragma unroll
+            for (int r = 0; r < RW; ++r) {
+              const float* const sc = (const float*)(now + Lds::kLatent + Lds::kRope + (tw * RW + r) * 256) + a * (L / 128);
+#pragma unroll
+              for (int b = 0; b < L / 128; ++b) scale[r][b] = sc[b];
+            }
+            fetch(0);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
-              const v4u w = *(const v4u*)(codes + (((4 * j + g) ^ a) << 4));
-              const float scale = sc[j / 2];
-              const v4u k0 = latent_widen(w[0], w[1], scale), k1 = latent_widen(w[2], w[3], scale);
-              *(v4u*)(to + (((8 * j + 2 * g) ^ turn) << 4)) = k0;
-              *(v4u*)(to + (((8 * j + 2 * g + 1) ^ turn) << 4)) = k1;
+              if (j + 1 < kJ) fetch(j + 1);
+              __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-                x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k0), qf[n][2 * j], x[n], 0, 0, 0);
+              for (int r = 0; r < RW; ++r) {
+                const v4u c = w[j & 1][r];
+                const v4u k0 = latent_widen(c[0], c[1], scale[r][j / 2]), k1 = latent_widen(c[2], c[3], scale[r][j / 2]);
+                if (RW == 1 || r == rw) {  // one of the waves that widen them keeps them for the second product
+                  uint8_t* const to = wide + (16 * (tw * RW + r) + a) * (2 * L);
+                  *(v4u*)(to + (((8 * j + 2 * g) ^ latent_turn(a)) << 4)) = k0;
+                  *(v4u*)(to + (((8 * j + 2 * g + 1) ^ latent_turn(a)) << 4)) = k1;
+                }
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-                x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k1), qf[n][2 * j + 1], x[n], 0, 0, 0);
+                for (int n = 0; n < kN; ++n)
+                  x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k0), qf[n][2 * j], x[r][n], 0, 0, 0);
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+                  x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k1), qf[n][2 * j + 1], x[r][n], 0, 0, 0);
+              }
             }
           } else {
-            const uint8_t* const from = now + (wave * 16 + a) * (2 * L);
-            const int turn = latent_turn(a);
-            v8bf k[2][2];
+            v8bf k[2][2][RW];
             auto fetch = [&](int j) {
-              k[j & 1][0] = *(const v8bf*)(from + (((8 * j + 2 * g) ^ turn) << 4));
-              k[j & 1][1] = *(const v8bf*)(from + (((8 * j + 2 * g + 1) ^ turn) << 4));
+#pragma unroll
+              for (int r = 0; r < RW; ++r) {
+                const uint8_t* const from = now + (16 * (tw * RW + r) + a) * (2 * L);
+                k[j & 1][0][r] = *(const v8bf*)(from + (((8 * j + 2 * g) ^ turn) << 4));
+                k[j & 1][1][r] = *(const v8bf*)(from + (((8 * j + 2 * g + 1) ^ turn) << 4));
+              }
             };
             fetch(0);
 #pragma unroll
@@ -580,96 +641,110 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j & 1][h], qf[n][2 * j + h], x[n], 0, 0, 0);
+                for (int r = 0; r < RW; ++r)
+#pragma unroll
+                  for (int n = 0; n < kN; ++n)
+                    x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j & 1][h][r], qf[n][2 * j + h], x[r][n], 0, 0, 0);
             }
           }
-          {
-            const uint8_t* const from = now + Lds::kLatent + (wave * 16 + a) * (P * 2);
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const uint8_t* const from = now + Lds::kLatent + (16 * (tw * RW + r) + a) * (P * 2);
 #pragma unroll
             for (int j = 0; j < kRopeFrags; ++j) {
               const int slot = P == 64 ? (2 * g + j) ^ (a >> 1 & 7) : g ^ (a >> 2 & 3);
               const v8bf k = *(const v8bf*)(from + slot * 16);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qrf[n][j], x[n], 0, 0, 0);
+              for (int n = 0; n < kN; ++n) x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qrf[n][j], x[r][n], 0, 0, 0);
             }
           }
-          // t = log2(e) x; lane: row 16 n + a, tokens 4 g + e of the wave's 16
-          const int token = s * kLatentStep + wave * 16 + g * 4;
-          float t[NT][4];
+          // t = log2(e) x; lane: row 16 (rw kN + n) + a, tokens 4 g + e of a group of 16
           bool moves = false;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int seen = MASKED ? (page0 < 0 ? 0 : hi[n] - token) : page0 < 0 ? 0 : 4;
+          for (int r = 0; r < RW; ++r) {
+            const int token = s * kLatentStep + 16 * (tw * RW + r) + 4 * g;
+            const bool there = __builtin_amdgcn_readfirstlane(s_there[buf * 4 + tw * RW + r]) != 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              t[n][e] = x[n][e] * p.scale_log2;
-              if (MASKED || page0 < 0) t[n][e] = e < seen ? t[n][e] : -__builtin_huge_valf();
-              moves |= t[n][e] > m[n];
+            for (int n = 0; n < kN; ++n) {
+              x[r][n] *= p.scale_log2;
+              const int seen = !there ? 0 : MASKED ? hi[n] - token : 4;
+              if (MASKED || !there)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[r][n][e] = e < seen ? x[r][n][e] : -__builtin_huge_valf();
+#pragma unroll
+              for (int e = 0; e < 4; ++e) moves |= x[r][n][e] > of_wave(m, n);
             }
           }
           uint8_t* const s_rest = Lds::kRestOverRope ? now + Lds::kLatent : lds + Lds::kRest;
-          constexpr int kRestWave = Lds::kRestOverRope ? 16 * P * 2 : kRows * 32;
-          float sum[NT];
+          constexpr int kRestGroup = Lds::kRestOverRope ? 16 * P * 2 : kRows * 32;
+          if constexpr (MASKED && Lds::kRestOverRope) lds_barrier();
+          float sum[kN];
           auto weigh = [&]() {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const float ref = m[n] == -__builtin_huge_valf() ? 0.f : m[n];
-              float w[4];
+            for (int n = 0; n < kN; ++n) {
+              const int row = 16 * (rw * kN + n) + a;
+              const float mine = of_wave(m, n), ref = mine == -__builtin_huge_valf() ? 0.f : mine;
+              sum[n] = 0.f;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(t[n][e] - ref);
-              sum[n] = (w[0] + w[1]) + (w[2] + w[3]);
-              const v2u packed = {pack2_bf16(w[0], w[1]), pack2_bf16(w[2], w[3])};
-              const int row = 16 * n + a, piece = 2 * wave + (g >> 1);
-              *(v2u*)(lds + Lds::kP + row * 128 + ((piece ^ (row >> 1 & 7)) << 4) + (g & 1) * 8) = packed;
-              if constexpr (MASKED) {
-                const v2u rest = {pack2_bf16(w[0] - __uint_as_float(packed[0] << 16), w[1] - __uint_as_float(packed[0] & 0xFFFF0000u)),
-                                  pack2_bf16(w[2] - __uint_as_float(packed[1] << 16), w[3] - __uint_as_float(packed[1] & 0xFFFF0000u))};
-                *(v2u*)(s_rest + wave * kRestWave + row * 32 + g * 8) = rest;
+              for (int r = 0; r < RW; ++r) {
+                const int group = tw * RW + r;
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(x[r][n][e] - ref);
+                sum[n] += (w[0] + w[1]) + (w[2] + w[3]);
+                const v2u packed = {pack2_bf16(w[0], w[1]), pack2_bf16(w[2], w[3])};
+                const int piece = 2 * group + (g >> 1);
+                *(v2u*)(lds + Lds::kP + row * 128 + ((piece ^ (row >> 1 & 7)) << 4) + (g & 1) * 8) = packed;
+                if constexpr (MASKED) {
+                  const v2u rest = {pack2_bf16(w[0] - __uint_as_float(packed[0] << 16), w[1] - __uint_as_float(packed[0] & 0xFFFF0000u)),
+                                    pack2_bf16(w[2] - __uint_as_float(packed[1] << 16), w[3] - __uint_as_float(packed[1] & 0xFFFF0000u))};
+                  *(v2u*)(s_rest + group * kRestGroup + row * 32 + g * 8) = rest;
+                }
               }
             }
           };
           weigh();
-          if (__any(moves) && lane == 0) s_flag[s & 1] = 1;
+          if (__any(moves) && here == 0) s_flag[s & 1] = 1;
           lds_barrier();
           if (s_flag[s & 1]) {
             // some row's score passed its reference: all waves move it alike
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float top = fmaxf(fmaxf(t[n][0], t[n][1]), fmaxf(t[n][2], t[n][3]));
+            for (int n = 0; n < kN; ++n) {
+              float top = -__builtin_huge_valf();
+#pragma unroll
+              for (int r = 0; r < RW; ++r) top = fmaxf(top, fmaxf(fmaxf(x[r][n][0], x[r][n][1]), fmaxf(x[r][n][2], x[r][n][3])));
               top = fmaxf(top, __shfl_xor(top, 16, 64));
               top = fmaxf(top, __shfl_xor(top, 32, 64));
-              if (g == 0) s_max[wave * kRows + 16 * n + a] = top;
+              if (g == 0) s_max[tw * kRows + 16 * (rw * kN + n) + a] = top;
             }
             lds_barrier();
+            float shrinks[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               float top = s_max[16 * n + a];
 #pragma unroll
-              for (int w = 1; w < 4; ++w) top = fmaxf(top, s_max[w * kRows + 16 * n + a]);
-              if (top > m[n]) {
-                const float ref = top + kLatentLead;
-                const float shrink = __builtin_amdgcn_exp2f(m[n] - ref);
-                l[n] *= shrink;
+              for (int w = 1; w < 4 / RW; ++w) top = fmaxf(top, s_max[w * kRows + 16 * n + a]);
+              const float ref = top > m[n] ? top + kLatentLead : m[n];
+              shrinks[n] = top > m[n] ? __builtin_amdgcn_exp2f(m[n] - ref) : 1.f;
+              m[n] = ref;
 #pragma unroll
-                for (int c = 0; c < kC; ++c) u[n][c] *= shrink;
-                m[n] = ref;
-              }
+              for (int c = 0; c < kC; ++c) u[n][c] *= shrinks[n];
             }
+#pragma unroll
+            for (int n = 0; n < kN; ++n) l[n] *= of_wave(shrinks, n);
             weigh();
             lds_barrier();
           }
           if (tid == 0) s_flag[(s & 1) ^ 1] = 0;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) l[n] += sum[n];
+          for (int n = 0; n < kN; ++n) l[n] += sum[n];
           // u += c^T p^T, this wave's channels
           const uint8_t* at_v[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int tk = 8 * g + 4 * h + (a >> 2);  // of 32; + 32 for the second half of the step
-            const int turn = latent_turn(tk & 15);
             // piece 2 c + (a % 4) / 2 of the row, c = wave kC + i: i comes in by an exclusive or
-            at_v[h] = wide + tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ turn) << 4) + (a & 1) * 8;
+            at_v[h] = wide + tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ latent_turn(tk & 15)) << 4) + (a & 1) * 8;
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -678,7 +753,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             for (int n = 0; n < NT; ++n) {
               const int row = 16 * n + a;
               pf[n] = *(const v8bf*)(lds + Lds::kP + row * 128 + (((4 * k + g) ^ (row >> 1 & 7)) << 4));
-              if constexpr (MASKED) rest[n] = *(const v8bf*)(s_rest + (2 * k + (g >> 1)) * kRestWave + row * 32 + (g & 1) * 16);
+              if constexpr (MASKED) rest[n] = *(const v8bf*)(s_rest + (2 * k + (g >> 1)) * kRestGroup + row * 32 + (g & 1) * 16);
             }
             v4u v[2];
             auto fetch = [&](int c) {
@@ -716,109 +791,81 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           __syncthreads();
           look(s + 4);
           if (s + 2 < last) stage(s + 2, page2, buf);
-          page0 = page1;
-          page1 = page2;
           page2 = next;
         }
       };
-      look(t0 + 3);
       const int whole = max(min(all_hi / kLatentStep, last), t0);
       steps(whole, std::false_type{});
       steps(last, std::true_type{});
     }
-    // l of the four lane groups and the four waves
+    // l of the lane groups and of the waves that share the tokens
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < kN; ++n) {
       l[n] += __shfl_xor(l[n], 16, 64);
       l[n] += __shfl_xor(l[n], 32, 64);
-      if (g == 0) s_max[wave * kRows + 16 * n + a] = l[n];
+      if (g == 0) s_max[tw * kRows + 16 * (rw * kN + n) + a] = l[n];
     }
     __syncthreads();
+    const bool whole_tile = t0 == 0 && t1 == sq.steps;
+    // a part that does not start its tile is its workgroup's first; one that does may have another tile before it
+    const int slot = worker * 2 + (at == begin ? 0 : 1);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float* const at_l = s_max + 16 * n + a;
-      l[n] = (at_l[0] + at_l[kRows]) + (at_l[2 * kRows] + at_l[3 * kRows]);
-    }
-    auto write = [&]() {
+      float sum = s_max[16 * n + a];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int w = 1; w < 4 / RW; ++w) sum += s_max[w * kRows + 16 * n + a];
+      if (whole_tile) {
         const int row = row0 + 16 * n + a;
         if (row >= rows) continue;
-        const int i = row / p.h_q, head = row - i * p.h_q;
-        const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];  // l == 0: the row sees no token
-        uint16_t* const to = p.out + (long long)(sq.first + i) * p.out_stride + (long long)head * p.out_head_stride + wave * (L / 4) + g * 4;
+        latent_write<L, kC>(p, sq, row, wave * (L / 4) + g * 4, u[n], m[n], sum, wave == 0 && g == 0);
+      } else {
+        // as the lanes hold it: whole kilobytes
+        v4f* const to = (v4f*)(p.part_u + (size_t)slot * (kRows * L)) + lane;
 #pragma unroll
-        for (int c = 0; c < kC; ++c)
-          *(v2u*)(to + c * 16) = v2u{pack2_bf16(u[n][c][0] * inv, u[n][c][1] * inv), pack2_bf16(u[n][c][2] * inv, u[n][c][3] * inv)};
-        if (p.lse && wave == 0 && g == 0)
-          p.lse[(size_t)(sq.first + i) * p.h_q + head] = l[n] == 0.f ? -__builtin_huge_valf() : (m[n] + __builtin_amdgcn_logf(l[n])) * 0.69314718055994530942f;
-      }
-    };
-    if (t0 == 0 && t1 == sq.steps) {
-      write();
-    } else {
-      // As in the 8-bit cache's attention: parts pass between XCDs by stores
-      // and loads at agent scope, and the last workgroup of a tile joins them
-      // in workgroup order.
-      constexpr int kTile = kRows * L;  // floats of one part
-      const int slot = (int)blockIdx.x * 2 + (at == begin ? 0 : 1);
-      auto part = [&](int sl) { return __builtin_amdgcn_make_buffer_rsrc(p.part_u + (size_t)sl * kTile, 0, kTile * 4, kBufferRsrcWord3); };
-      {
-        const __amdgpu_buffer_rsrc_t rs = part(slot);
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, u[n][c]), rs, (((wave * kC + c) * NT + n) * 64 + lane) * 16, 0, kCpolSc1);
-        if (wave == 0 && g == 0)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, v2f{m[n], l[n]}), rs_ml, (slot * kRows + 16 * n + a) * 8, 0, kCpolSc1);
-      }
-      const long long s0 = seq0 + (long long)tile * sq.steps;
-      const int w0 = (int)kv8_div(s0, share), w1 = (int)kv8_div(s0 + sq.steps - 1, share);
-      wait_vmem_all();
-      __syncthreads();
-      if (tid == 0)
-        s_last = __hip_atomic_fetch_add(p.arrived + w0, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == w1 - w0;
-      __syncthreads();
-      if (s_last) {
-        if (tid == 0) __hip_atomic_store(p.arrived + w0, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
-        const int slot0 = w0 * 2 + (s0 > w0 * share ? 1 : 0);  // only the first can have had another tile before
-        auto slot_of = [&](int w) { return w == w0 ? slot0 : w * 2; };
-        auto load_ml = [&](int w, int n) {
-          const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs_ml, (slot_of(w) * kRows + 16 * n + a) * 8, 0, kCpolSc1);
-          return __builtin_bit_cast(v2f, v);
-        };
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          m[n] = -__builtin_huge_valf();
-          l[n] = 0.f;
-#pragma unroll
-          for (int c = 0; c < kC; ++c) u[n][c] = v4f{0.f, 0.f, 0.f, 0.f};
-        }
-        for (int w = w0; w <= w1; ++w)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) m[n] = fmaxf(m[n], load_ml(w, n)[0]);
-        for (int w = w0; w <= w1; ++w) {
-          const __amdgpu_buffer_rsrc_t rs = part(slot_of(w));
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const v2f ml = load_ml(w, n);
-            const float f = __builtin_amdgcn_exp2f(ml[0] - (m[n] == -__builtin_huge_valf() ? 0.f : m[n]));
-            l[n] += ml[1] * f;
-#pragma unroll
-            for (int c = 0; c < kC; ++c) {
-              const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, (((wave * kC + c) * NT + n) * 64 + lane) * 16, 0, kCpolSc1);
-              u[n][c] += __builtin_bit_cast(v4f, v) * f;
-            }
-          }
-        }
-        write();
+        for (int c = 0; c < kC; ++c) to[((wave * kC + c) * NT + n) * 64] = u[n][c];
+        if (wave == 0 && g == 0) *(v2f*)(p.part_ml + (size_t)(slot * kRows + 16 * n + a) * 2) = v2f{m[n], sum};
       }
     }
+    if (!whole_tile && t0 == 0 && tid == 0) {
+      const int w1 = (int)kv8_div(seq0 + (long long)tile * sq.steps + sq.steps - 1, share);
+      p.cut[worker] = LatentCut{seq, tile, w1 - worker + 1, slot};
+    }
     at += t1 - t0;
+  }
+}
+
+// Adds up the parts of the tiles that shares cut, in workgroup order: tile w is
+// the one that workgroup w began and did not finish, if there is one.  A wave
+// takes 16 rows by 16 channels at a time.
+template <int L, int NT>
+__global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
+  constexpr int kRows = 16 * NT, kBlocks = L / 16 * NT;
+  const LatentCut cut = p.cut[blockIdx.x];
+  if (cut.parts == 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+  const LatentSeq sq = latent_seq_uniform<kRows>(p, cut.seq);
+  // the parts after the first are their workgroups' first
+  auto slot_of = [&](int i) { return i == 0 ? cut.slot : ((int)blockIdx.x + i) * 2; };
+  for (int b = blockIdx.y * 4 + wave; b < kBlocks; b += gridDim.y * 4) {
+    const int n = b % NT, c = b / NT, row = cut.tile * kRows + 16 * n + a;
+    const float* const ml = p.part_ml + (16 * n + a) * 2;
+    float m = -__builtin_huge_valf();
+#pragma unroll 4
+    for (int i = 0; i < cut.parts; ++i) m = fmaxf(m, ml[(size_t)slot_of(i) * kRows * 2]);
+    const float ref = m == -__builtin_huge_valf() ? 0.f : m;
+    float l = 0.f;
+    v4f u[1] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 4
+    for (int i = 0; i < cut.parts; ++i) {
+      const size_t slot = slot_of(i);
+      const v2f at = *(const v2f*)(ml + slot * kRows * 2);
+      const v4f x = *((const v4f*)(p.part_u + slot * (kRows * L)) + b * 64 + lane);
+      const float f = __builtin_amdgcn_exp2f(at[0] - ref);
+      l += at[1] * f;
+      u[0] += x * f;
+    }
+    if (row < sq.count * p.h_q) latent_write<L, 1>(p, sq, row, c * 16 + g * 4, u, m, l, c == 0 && g == 0);
   }
 }
 
