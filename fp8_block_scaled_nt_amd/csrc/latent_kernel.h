@@ -408,6 +408,9 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
   using Lds = LatentLds<L, F8, NT>;
   constexpr int P = L / 8, kRows = 16 * NT, kJ = L / 64, kC = L / 64;  // kC column tiles of 16 a wave
   constexpr int kRopeFrags = P / 32, RW = NT > 2 ? 2 : 1, kN = NT / RW;  // kN row tiles and RW token tiles of a wave's scores
+  // u and q together pass the 256 registers that vector instructions reach: q
+  // goes to the accumulation registers, where matrix instructions read it
+  constexpr bool kQInAcc = NT * L >= 1024;
   extern __shared__ __align__(1024) uint8_t lds[];  // all of it: a row's place has to be a multiple of its size
   float* const s_max = (float*)(lds + Lds::kMax);
   int* const s_flag = (int*)(lds + Lds::kFlags);
@@ -496,6 +499,12 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 #pragma unroll
       for (int j = 0; j < kRopeFrags; ++j) qrf[n][j] = __builtin_bit_cast(v8bf, *(const v4u*)(srcr + j * 8));
       hi[n] = latent_sees(p, sq, i);
+      if constexpr (kQInAcc) {
+#pragma unroll
+        for (int j = 0; j < 2 * kJ; ++j) asm("" : "+a"(qf[n][j]));
+#pragma unroll
+        for (int j = 0; j < kRopeFrags; ++j) asm("" : "+a"(qrf[n][j]));
+      }
     }
     const int all_hi = latent_uniform(latent_sees(p, sq, row0 / p.h_q));
     const int any_hi = latent_uniform(latent_sees(p, sq, (min(row0 + kRows, rows) - 1) / p.h_q));
@@ -524,49 +533,49 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
         const int j = (step * kLatentStep + wave * 16) >> p.c.block_log2;
         return (j < p.c.max_blocks) & ((unsigned)f < (unsigned)p.c.num_blocks) ? f : -1;
       };
-      // This wave's 16 tokens of a step, as they lie in memory; tokens past the
-      // sequence's end, or of a block that the table does not have, become zeros.
-      auto stage = [&](int step, int page, int buf) {
+      // This wave's 16 tokens of a step, as they lie in memory, in kDmas
+      // pieces; tokens past the sequence's end, or of a block that the table
+      // does not have, become zeros.  Where a lane's bytes lie is linear in the
+      // bits of the piece's number and the lane, so that one exclusive or tells.
+      constexpr int kPieces = Lds::kRow / 16, kPerDma = 64 / kPieces;  // tokens of one DMA
+      constexpr int kLatentDmas = 16 / kPerDma, kDmas = kLatentDmas + P / 32 + F8;
+      const int lane_l = lane / kPieces * Lds::kRow + ((lane % kPieces ^ (F8 ? lane / kPieces : latent_turn(lane / kPieces))) << 4);
+      const int lane_r = P == 64 ? lane / 8 * 128 + ((lane % 8 ^ lane / 16) << 4) : lane / 4 * 64 + ((lane % 4 ^ (lane / 16 & 3)) << 4);
+      v4i_rsrc rl, rr, rs;
+      uint8_t* to;
+      auto stage_at = [&](int step, int page, int buf) {
         const int token = step * kLatentStep + wave * 16;
         const int valid = page < 0 ? 0 : min(max(sq.kv - token, 0), 16);
         const size_t row = ((size_t)max(page, 0) << p.c.block_log2) + (token & (p.c.block - 1));
-        uint8_t* const to = lds + buf * Lds::kBuffer;
-        int lane = tid & 63;
-        asm volatile("" : "+v"(lane));
-        const v4i_rsrc rl = make_rsrc(p.c.latent + row * Lds::kRow, valid * Lds::kRow);
-        constexpr int kPieces = Lds::kRow / 16, kPerDma = 64 / kPieces;  // tokens of one DMA
-#pragma unroll
-        for (int i = 0; i < 16 / kPerDma; ++i) {
-          const int t = i * kPerDma + lane / kPieces, s = lane % kPieces;
-          const int piece = s ^ (F8 ? t : latent_turn(t));
-          lds_dma16(rl, t * Lds::kRow + piece * 16, 0, to + wave * 16 * Lds::kRow + i * 1024);
-        }
-        const v4i_rsrc rr = make_rsrc(p.c.rope + row * P, valid * P * 2);
-#pragma unroll
-        for (int i = 0; i < P / 32; ++i) {
-          const int t = P == 64 ? i * 8 + lane / 8 : lane / 4, s = P == 64 ? lane % 8 : lane % 4;
-          const int piece = P == 64 ? s ^ (t >> 1 & 7) : s ^ (t >> 2 & 3);
-          lds_dma16(rr, t * P * 2 + piece * 16, 0, to + Lds::kLatent + wave * 16 * P * 2 + i * 1024);
-        }
-        if constexpr (F8)
-          lds_dma4(make_rsrc(p.c.scales + row * (L / 128), valid * (L / 128) * 4), lane * 4, 0,
-                   to + Lds::kLatent + Lds::kRope + wave * 256);
-        lds_dma_end(rr, lane);
+        to = lds + buf * Lds::kBuffer;
+        rl = make_rsrc(p.c.latent + row * Lds::kRow, valid * Lds::kRow);
+        rr = make_rsrc(p.c.rope + row * P, valid * P * 2);
+        if constexpr (F8) rs = make_rsrc(p.c.scales + row * (L / 128), valid * (L / 128) * 4);
         if (lane == 0) s_there[buf * 4 + wave] = page >= 0;
+      };
+      auto stage = [&](int i) {
+        if (i < kLatentDmas) {
+          const int t = i * kPerDma;
+          lds_dma16(rl, lane_l ^ (i * 1024 | (F8 ? t : latent_turn(t)) << 4), 0, to + wave * 16 * Lds::kRow + i * 1024);
+        } else if (i < kLatentDmas + P / 32) {
+          const int r = i - kLatentDmas;
+          lds_dma16(rr, lane_r ^ (r * 1024 | (P == 64 ? r * 4 : 0) << 4), 0, to + Lds::kLatent + wave * 16 * P * 2 + r * 1024);
+        } else {
+          lds_dma4(rs, lane * 4, 0, to + Lds::kLatent + Lds::kRope + wave * 256);
+        }
+        if (i == kDmas - 1) lds_dma_end(rr, lane);
       };
       __syncthreads();  // the tile before is done with LDS
       if (tid < 2) s_flag[tid] = 0;
       look(t0);
-      const int page0 = page_of(t0);
+      stage_at(t0, page_of(t0), 0);
       look(t0 + 1);
-      stage(t0, page0, 0);
-      const int page1 = page_of(t0 + 1);
+#pragma unroll
+      for (int i = 0; i < kDmas; ++i) stage(i);
+      int page1 = page_of(t0 + 1);
       look(t0 + 2);
-      stage(t0 + 1, page1, 1);
-      int page2 = page_of(t0 + 2);
       wait_vmem_all();
       __syncthreads();
-      look(t0 + 3);
 
       int s = t0;
       auto steps = [&](int until, auto form) {
@@ -581,6 +590,14 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           int here = lane;
           asm volatile("" : "+v"(here));
           const int a = here & 15, g = here >> 4;
+          // The next step's tokens set out while the scores are worked out:
+          // piece by piece between the products, which leave room for them.
+          stage_at(s + 1, s + 1 < last ? page1 : -1, buf ^ 1);
+          constexpr int kPerJ = (kDmas + kJ - 1) / kJ;
+          auto stage_of = [&](int j) {
+#pragma unroll
+            for (int i = j * kPerJ; i < (j + 1) * kPerJ && i < kDmas; ++i) stage(i);
+          };
           // scores: tokens 16 (tw RW + r) + a of the step with rows 16 (rw kN + n) + a
           v4f x[RW][kN];
 #pragma unroll
@@ -589,11 +606,11 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             for (int n = 0; n < kN; ++n) x[r][n] = v4f{0.f, 0.f, 0.f, 0.f};
           const int turn = F8 ? a : latent_turn(a);
           if constexpr (F8) {
-            v4u w[2][RW];
+            v4u w[3][RW];
             float scale[RW][L / 128];
             auto fetch = [&](int j) {
 #pragma unroll
-              for (int r = 0; r < RW; ++r) w[j & 1][r] = *(const v4u*)(now + (16 * (tw * RW + r) + a) * L + (((4 * j + g) ^ turn) << 4));
+              for (int r = 0; r < RW; ++r) w[j % 3][r] = *(const v4u*)(now + (16 * (tw * RW + r) + a) * L + (((4 * j + g) ^ turn) << 4));
             };
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
@@ -602,13 +619,15 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
               for (int b = 0; b < L / 128; ++b) scale[r][b] = sc[b];
             }
             fetch(0);
+            fetch(1);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
-              if (j + 1 < kJ) fetch(j + 1);
+              if (j + 2 < kJ) fetch(j + 2);
+              stage_of(j);
               __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
               for (int r = 0; r < RW; ++r) {
-                const v4u c = w[j & 1][r];
+                const v4u c = w[j % 3][r];
                 const v4u k0 = latent_widen(c[0], c[1], scale[r][j / 2]), k1 = latent_widen(c[2], c[3], scale[r][j / 2]);
                 if (RW == 1 || r == rw) {  // one of the waves that widen them keeps them for the second product
                   uint8_t* const to = wide + (16 * (tw * RW + r) + a) * (2 * L);
@@ -624,19 +643,21 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
               }
             }
           } else {
-            v8bf k[2][2][RW];
+            v8bf k[3][2][RW];
             auto fetch = [&](int j) {
 #pragma unroll
               for (int r = 0; r < RW; ++r) {
                 const uint8_t* const from = now + (16 * (tw * RW + r) + a) * (2 * L);
-                k[j & 1][0][r] = *(const v8bf*)(from + (((8 * j + 2 * g) ^ turn) << 4));
-                k[j & 1][1][r] = *(const v8bf*)(from + (((8 * j + 2 * g + 1) ^ turn) << 4));
+                k[j % 3][0][r] = *(const v8bf*)(from + (((8 * j + 2 * g) ^ turn) << 4));
+                k[j % 3][1][r] = *(const v8bf*)(from + (((8 * j + 2 * g + 1) ^ turn) << 4));
               }
             };
             fetch(0);
+            fetch(1);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
-              if (j + 1 < kJ) fetch(j + 1);
+              if (j + 2 < kJ) fetch(j + 2);
+              stage_of(j);
               __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
               for (int h = 0; h < 2; ++h)
@@ -644,7 +665,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
                 for (int r = 0; r < RW; ++r)
 #pragma unroll
                   for (int n = 0; n < kN; ++n)
-                    x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j & 1][h][r], qf[n][2 * j + h], x[r][n], 0, 0, 0);
+                    x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j % 3][h][r], qf[n][2 * j + h], x[r][n], 0, 0, 0);
             }
           }
 #pragma unroll
@@ -755,22 +776,23 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
               pf[n] = *(const v8bf*)(lds + Lds::kP + row * 128 + (((4 * k + g) ^ (row >> 1 & 7)) << 4));
               if constexpr (MASKED) rest[n] = *(const v8bf*)(s_rest + (2 * k + (g >> 1)) * kRestGroup + row * 32 + (g & 1) * 16);
             }
-            v4u v[2];
+            v4u v[3];
             auto fetch = [&](int c) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t off = (uint32_t)(uintptr_t)(lds_u8*)at_v[h] ^ (c * 32);
                 const v2u w = lds_turned((const uint8_t*)(lds_u8*)(uintptr_t)(off + k * 32 * 2 * L));
-                v[c & 1][2 * h] = w[0];
-                v[c & 1][2 * h + 1] = w[1];
+                v[c % 3][2 * h] = w[0];
+                v[c % 3][2 * h + 1] = w[1];
               }
             };
             fetch(0);
+            fetch(1);
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
-              if (c + 1 < kC) fetch(c + 1);
+              if (c + 2 < kC) fetch(c + 2);
               __builtin_amdgcn_sched_barrier(0);
-              v4u w = v[c & 1];
+              v4u w = v[c % 3];
               if constexpr (MASKED) {
                 // a token that some rows see and others do not must reach the
                 // former only: what is not finite has made their sums NaN already
@@ -787,11 +809,9 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           }
           // the next step has landed, and everybody is done with this one
           wait_vmem_all();
-          const int next = page_of(s + 3);
+          page1 = page_of(s + 2);
           __syncthreads();
-          look(s + 4);
-          if (s + 2 < last) stage(s + 2, page2, buf);
-          page2 = next;
+          look(s + 3);
         }
       };
       const int whole = max(min(all_hi / kLatentStep, last), t0);
