@@ -1955,6 +1955,8 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   p.workers = info->cus;
   const int tiles = latent_row_tiles(max_q, h_q);
   const LatentKernel k = latent_attn(latent_dim, cache_scales != nullptr, tiles);
+  const int row_tiles = (int)(((long long)max_q * h_q + 16 * tiles - 1) / (16 * tiles));
+  p.together = (long long)max_q * batch == total && row_tiles <= 8 ? row_tiles : 1;
   char* base = nullptr;
   if (int s = ensure_workspace(dev, (hipStream_t)stream, latent_part_bytes(p.workers, tiles, latent_dim), &base)) return s;
   p.part_u = (float*)(base + kWsHeader);
@@ -1962,7 +1964,7 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   p.cut = (dg::LatentCut*)(p.part_ml + (size_t)p.workers * 2 * 16 * tiles * 2);
   void* args[] = {&p};
   if (int s = launch_plain("latent_attention", k.fn, dim3(p.workers), 256, args, stream, k.smem)) return s;
-  return launch_plain("latent_join", k.join, dim3(p.workers, 16), 256, args, stream);
+  return launch_plain("latent_join", k.join, dim3(p.workers, dg::kLatentJoiners), 256, args, stream);
 }
 
 int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint16_t* kv, int64_t kv_stride,

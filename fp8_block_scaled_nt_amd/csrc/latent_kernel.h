@@ -274,6 +274,7 @@ struct LatentAttnParams {
   float* part_ml;  // [workers][2][rows of a tile][2]: m and l
   LatentCut* cut;  // [workers]
   int workers;
+  int together;  // > 1: every sequence has so many tiles, and as many neighbouring workgroups take the same steps of each
 };
 
 constexpr int kLatentStep = 64;       // tokens of one step
@@ -430,7 +431,8 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
     }
   }
   if (tid == 0) p.cut[latent_worker(blockIdx.x, p.workers)] = LatentCut{0, 0, 0, 0};
-  auto units_of = [&](const LatentSeq& s) { return (long long)s.tiles * s.steps; };
+  // together > 1: a unit is a step of all tiles, shared out to groups of workgroups that read the same tokens at a time
+  auto units_of = [&](const LatentSeq& s) { return p.together > 1 ? (s.count > 0 ? (long long)s.steps : 0) : (long long)s.tiles * s.steps; };
   auto chunk_of = [&](int first) {
     const int i = first + tid;
     Kv8Chunk c;
@@ -441,10 +443,11 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
   Kv8Chunk chunk = chunk_of(0);
   long long total = chunk.total;
   for (int i = 256; i < p.batch; i += 256) total += chunk_of(i).total;
-  const long long share = max(kv8_div(total + p.workers - 1, p.workers), 1LL);
-  const int worker = latent_worker(blockIdx.x, p.workers);
-  const long long begin = worker * share, end = min(begin + share, total);
-  if (begin >= end) return;
+  const int groups = p.workers / p.together;
+  const long long share = max(kv8_div(total + groups - 1, groups), 1LL);
+  const int worker = latent_worker(blockIdx.x, p.workers), group = worker / p.together;
+  const long long begin = group * share, end = min(begin + share, total);
+  if (group >= groups || begin >= end) return;
   // the sequence that the first unit is of
   long long at = begin, seq0 = 0;
   int seq;
@@ -478,8 +481,9 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
       units = units_of(sq);
     }
     const long long rel = at - seq0;
-    const int tile = latent_uniform((int)kv8_div(rel, sq.steps));
-    const int t0 = latent_uniform((int)(rel - (long long)tile * sq.steps));
+    const int past = latent_uniform((int)kv8_div(rel, sq.steps));  // tiles before this one
+    const int tile = p.together > 1 ? worker % p.together : past;
+    const int t0 = latent_uniform((int)(rel - (long long)past * sq.steps));
     const int t1 = latent_uniform((int)min((long long)sq.steps, t0 + (end - at)));
     const int rows = sq.count * p.h_q, row0 = tile * kRows;
 
@@ -848,44 +852,88 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
       }
     }
     if (!whole_tile && t0 == 0 && tid == 0) {
-      const int w1 = (int)kv8_div(seq0 + (long long)tile * sq.steps + sq.steps - 1, share);
-      p.cut[worker] = LatentCut{seq, tile, w1 - worker + 1, slot};
+      const int g1 = (int)kv8_div(seq0 + (long long)past * sq.steps + sq.steps - 1, share);
+      p.cut[worker] = LatentCut{seq, tile, g1 - group + 1, slot};
     }
     at += t1 - t0;
   }
 }
 
-// Adds up the parts of the tiles that shares cut, in workgroup order: tile w is
-// the one that workgroup w began and did not finish, if there is one.  A wave
-// takes 16 rows by 16 channels at a time.
+// Adds up the parts of the tiles that shares cut, in an order of their own
+// that does not change from call to call.  blockIdx.x: the workgroup that began
+// the tile and did not finish it, if there is one; blockIdx.y: the pieces of 16
+// rows by 16 channels that this workgroup adds up, each wave every fourth part.
+constexpr int kLatentJoiners = 16;  // workgroups of a tile
+
 template <int L, int NT>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
-  constexpr int kRows = 16 * NT, kBlocks = L / 16 * NT;
+  constexpr int kRows = 16 * NT, kPer = L / 16 * NT / kLatentJoiners, kChunk = 64;
+  __shared__ float s_f[kChunk][kRows], s_ml[4][2][kRows];
+  __shared__ v4f s_u[4][kPer][64];
   const LatentCut cut = p.cut[blockIdx.x];
   if (cut.parts == 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
   const LatentSeq sq = latent_seq_uniform<kRows>(p, cut.seq);
   // the parts after the first are their workgroups' first
-  auto slot_of = [&](int i) { return i == 0 ? cut.slot : ((int)blockIdx.x + i) * 2; };
-  for (int b = blockIdx.y * 4 + wave; b < kBlocks; b += gridDim.y * 4) {
-    const int n = b % NT, c = b / NT, row = cut.tile * kRows + 16 * n + a;
-    const float* const ml = p.part_ml + (16 * n + a) * 2;
-    float m = -__builtin_huge_valf();
+  auto slot_of = [&](int i) { return (size_t)(i == 0 ? cut.slot : ((int)blockIdx.x + i * p.together) * 2); };
+  auto ml_of = [&](int i, int n) { return *(const v2f*)(p.part_ml + (slot_of(i) * kRows + 16 * n + a) * 2); };
+  const int i0 = wave + 4 * g;  // this lane's parts, for references and sums: every 16th
+  float m[NT], l[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) m[n] = -__builtin_huge_valf(), l[n] = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < cut.parts; ++i) m = fmaxf(m, ml[(size_t)slot_of(i) * kRows * 2]);
-    const float ref = m == -__builtin_huge_valf() ? 0.f : m;
-    float l = 0.f;
-    v4f u[1] = {{0.f, 0.f, 0.f, 0.f}};
+  for (int i = i0; i < cut.parts; i += 16)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) m[n] = fmaxf(m[n], ml_of(i, n)[0]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m[n] = fmaxf(m[n], __shfl_xor(m[n], 16, 64));
+    m[n] = fmaxf(m[n], __shfl_xor(m[n], 32, 64));
+    if (g == 0) s_ml[wave][0][16 * n + a] = m[n];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    m[n] = fmaxf(fmaxf(s_ml[0][0][16 * n + a], s_ml[1][0][16 * n + a]), fmaxf(s_ml[2][0][16 * n + a], s_ml[3][0][16 * n + a]));
+  v4f u[kPer];
+#pragma unroll
+  for (int b = 0; b < kPer; ++b) u[b] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int first = 0; first < cut.parts; first += kChunk) {
+    const int stop = min(cut.parts - first, kChunk);
+    if (first) __syncthreads();
 #pragma unroll 4
-    for (int i = 0; i < cut.parts; ++i) {
-      const size_t slot = slot_of(i);
-      const v2f at = *(const v2f*)(ml + slot * kRows * 2);
-      const v4f x = *((const v4f*)(p.part_u + slot * (kRows * L)) + b * 64 + lane);
-      const float f = __builtin_amdgcn_exp2f(at[0] - ref);
-      l += at[1] * f;
-      u[0] += x * f;
+    for (int i = i0; i < stop; i += 16)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const v2f ml = ml_of(first + i, n);
+        const float f = __builtin_amdgcn_exp2f(ml[0] - (m[n] == -__builtin_huge_valf() ? 0.f : m[n]));
+        l[n] += ml[1] * f;
+        s_f[i][16 * n + a] = f;
+      }
+    __syncthreads();
+#pragma unroll 2
+    for (int i = wave; i < stop; i += 4) {
+      const v4f* const from = (const v4f*)(p.part_u + slot_of(first + i) * (kRows * L)) + blockIdx.y * kPer * 64 + lane;
+#pragma unroll
+      for (int b = 0; b < kPer; ++b) u[b] += from[b * 64] * s_f[i][(blockIdx.y * kPer + b) % NT * 16 + a];
     }
-    if (row < sq.count * p.h_q) latent_write<L, 1>(p, sq, row, c * 16 + g * 4, u, m, l, c == 0 && g == 0);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    l[n] += __shfl_xor(l[n], 16, 64);
+    l[n] += __shfl_xor(l[n], 32, 64);
+    if (g == 0) s_ml[wave][1][16 * n + a] = l[n];
+  }
+#pragma unroll
+  for (int b = 0; b < kPer; ++b) s_u[wave][b][lane] = u[b];
+  __syncthreads();
+  for (int b = wave; b < kPer; b += 4) {
+    const int block = blockIdx.y * kPer + b, n = block % NT, c = block / NT, r = 16 * n + a, row = cut.tile * kRows + r;
+    if (row >= sq.count * p.h_q) continue;
+    const v4f sum[1] = {(s_u[0][b][lane] + s_u[1][b][lane]) + (s_u[2][b][lane] + s_u[3][b][lane])};
+    const float top = fmaxf(fmaxf(s_ml[0][0][r], s_ml[1][0][r]), fmaxf(s_ml[2][0][r], s_ml[3][0][r]));
+    const float all = (s_ml[0][1][r] + s_ml[1][1][r]) + (s_ml[2][1][r] + s_ml[3][1][r]);
+    latent_write<L, 1>(p, sq, row, c * 16 + g * 4, sum, top, all, c == 0 && g == 0);
   }
 }
 
