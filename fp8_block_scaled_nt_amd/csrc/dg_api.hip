@@ -1964,7 +1964,7 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   p.cut = (dg::LatentCut*)(p.part_ml + (size_t)p.workers * 2 * 16 * tiles * 2);
   void* args[] = {&p};
   if (int s = launch_plain("latent_attention", k.fn, dim3(p.workers), 256, args, stream, k.smem)) return s;
-  return launch_plain("latent_join", k.join, dim3(p.workers, dg::kLatentJoiners), 256, args, stream);
+  return launch_plain("latent_join", k.join, dim3(4 * p.workers), 256, args, stream);
 }
 
 int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint16_t* kv, int64_t kv_stride,

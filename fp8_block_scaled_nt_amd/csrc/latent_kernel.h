@@ -859,81 +859,88 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
   }
 }
 
-// Adds up the parts of the tiles that shares cut, in an order of their own
-// that does not change from call to call.  blockIdx.x: the workgroup that began
-// the tile and did not finish it, if there is one; blockIdx.y: the pieces of 16
-// rows by 16 channels that this workgroup adds up, each wave every fourth part.
-constexpr int kLatentJoiners = 16;  // workgroups of a tile
-
+// Adds up the parts of the tiles that shares cut, in an order that does not
+// change from call to call.  The workgroups share out all pieces of such tiles:
+// kPer times 16 rows by 16 channels, of which each wave takes every fourth part.
 template <int L, int NT>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
-  constexpr int kRows = 16 * NT, kPer = L / 16 * NT / kLatentJoiners, kChunk = 64;
-  __shared__ float s_f[kChunk][kRows], s_ml[4][2][kRows];
+  constexpr int kRows = 16 * NT, kPer = 4, kPieces = L / 16 * NT / kPer;
+  __shared__ int s_tile[256], s_count[4];
+  __shared__ float s_ml[4][2][kRows];
   __shared__ v4f s_u[4][kPer][64];
-  const LatentCut cut = p.cut[blockIdx.x];
-  if (cut.parts == 0) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
-  const LatentSeq sq = latent_seq_uniform<kRows>(p, cut.seq);
-  // the parts after the first are their workgroups' first
-  auto slot_of = [&](int i) { return (size_t)(i == 0 ? cut.slot : ((int)blockIdx.x + i * p.together) * 2); };
-  auto ml_of = [&](int i, int n) { return *(const v2f*)(p.part_ml + (slot_of(i) * kRows + 16 * n + a) * 2); };
-  const int i0 = wave + 4 * g;  // this lane's parts, for references and sums: every 16th
-  float m[NT], l[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) m[n] = -__builtin_huge_valf(), l[n] = 0.f;
-#pragma unroll 4
-  for (int i = i0; i < cut.parts; i += 16)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) m[n] = fmaxf(m[n], ml_of(i, n)[0]);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    m[n] = fmaxf(m[n], __shfl_xor(m[n], 16, 64));
-    m[n] = fmaxf(m[n], __shfl_xor(m[n], 32, 64));
-    if (g == 0) s_ml[wave][0][16 * n + a] = m[n];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-    m[n] = fmaxf(fmaxf(s_ml[0][0][16 * n + a], s_ml[1][0][16 * n + a]), fmaxf(s_ml[2][0][16 * n + a], s_ml[3][0][16 * n + a]));
-  v4f u[kPer];
-#pragma unroll
-  for (int b = 0; b < kPer; ++b) u[b] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int first = 0; first < cut.parts; first += kChunk) {
-    const int stop = min(cut.parts - first, kChunk);
-    if (first) __syncthreads();
-#pragma unroll 4
-    for (int i = i0; i < stop; i += 16)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const v2f ml = ml_of(first + i, n);
-        const float f = __builtin_amdgcn_exp2f(ml[0] - (m[n] == -__builtin_huge_valf() ? 0.f : m[n]));
-        l[n] += ml[1] * f;
-        s_f[i][16 * n + a] = f;
-      }
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
+  int item = blockIdx.x;  // among all pieces, less those of the 256 workgroups before `base`
+  for (int base = 0; base < p.workers; base += 256) {
+    // the workgroups that began a tile and did not finish it
+    const bool cuts = base + tid < p.workers && p.cut[min(base + tid, p.workers - 1)].parts > 0;
+    const uint64_t all = __ballot(cuts);
     __syncthreads();
-#pragma unroll 2
-    for (int i = wave; i < stop; i += 4) {
-      const v4f* const from = (const v4f*)(p.part_u + slot_of(first + i) * (kRows * L)) + blockIdx.y * kPer * 64 + lane;
+    if (lane == 0) s_count[wave] = __popcll(all);
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < wave; ++w) before += s_count[w];
+    if (cuts) s_tile[before + __popcll(all & ((1ull << lane) - 1))] = base + tid;
+    const int tiles = s_count[0] + s_count[1] + s_count[2] + s_count[3];
+    __syncthreads();
+    for (; item < tiles * kPieces; item += gridDim.x) {
+      const int worker = s_tile[item / kPieces], b0 = item % kPieces * kPer;
+      const LatentCut cut = p.cut[worker];
+      // the parts after the first are their workgroups' first
+      auto slot_of = [&](int i) { return (size_t)(i == 0 ? cut.slot : (worker + i * p.together) * 2); };
+      float m[NT], l[NT];
+      v4f u[kPer];
 #pragma unroll
-      for (int b = 0; b < kPer; ++b) u[b] += from[b * 64] * s_f[i][(blockIdx.y * kPer + b) % NT * 16 + a];
+      for (int n = 0; n < NT; ++n) m[n] = -__builtin_huge_valf(), l[n] = 0.f;
+#pragma unroll
+      for (int b = 0; b < kPer; ++b) u[b] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int i = wave; i < cut.parts; i += 4) {
+        const size_t slot = slot_of(i);
+        const v4f* const from = (const v4f*)(p.part_u + slot * (kRows * L)) + b0 * 64 + lane;
+        v4f x[kPer];
+        v2f ml[NT];
+#pragma unroll
+        for (int b = 0; b < kPer; ++b) x[b] = from[b * 64];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) ml[n] = *(const v2f*)(p.part_ml + (slot * kRows + 16 * n + a) * 2);
+        float was[NT], is[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float top = fmaxf(m[n], ml[n][0]), ref = top == -__builtin_huge_valf() ? 0.f : top;
+          was[n] = __builtin_amdgcn_exp2f(m[n] - ref);
+          is[n] = __builtin_amdgcn_exp2f(ml[n][0] - ref);
+          l[n] = l[n] * was[n] + ml[n][1] * is[n];
+          m[n] = top;
+        }
+#pragma unroll
+        for (int b = 0; b < kPer; ++b) u[b] = u[b] * was[b % NT] + x[b] * is[b % NT];
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (g == 0) {
+          s_ml[wave][0][16 * n + a] = m[n];
+          s_ml[wave][1][16 * n + a] = l[n];
+        }
+#pragma unroll
+      for (int b = 0; b < kPer; ++b) s_u[wave][b][lane] = u[b];
+      __syncthreads();
+      {
+        const LatentSeq sq = latent_seq_uniform<kRows>(p, cut.seq);
+        const int block = b0 + wave, n = block % NT, c = block / NT, r = 16 * n + a, row = cut.tile * kRows + r;
+        const float top = fmaxf(fmaxf(s_ml[0][0][r], s_ml[1][0][r]), fmaxf(s_ml[2][0][r], s_ml[3][0][r]));
+        float sum = 0.f;
+        v4f out[1] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = __builtin_amdgcn_exp2f(s_ml[w][0][r] - (top == -__builtin_huge_valf() ? 0.f : top));
+          sum += s_ml[w][1][r] * f;
+          out[0] += s_u[w][wave][lane] * f;
+        }
+        if (row < sq.count * p.h_q) latent_write<L, 1>(p, sq, row, c * 16 + g * 4, out, top, sum, c == 0 && g == 0);
+      }
+      __syncthreads();
     }
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    l[n] += __shfl_xor(l[n], 16, 64);
-    l[n] += __shfl_xor(l[n], 32, 64);
-    if (g == 0) s_ml[wave][1][16 * n + a] = l[n];
-  }
-#pragma unroll
-  for (int b = 0; b < kPer; ++b) s_u[wave][b][lane] = u[b];
-  __syncthreads();
-  for (int b = wave; b < kPer; b += 4) {
-    const int block = blockIdx.y * kPer + b, n = block % NT, c = block / NT, r = 16 * n + a, row = cut.tile * kRows + r;
-    if (row >= sq.count * p.h_q) continue;
-    const v4f sum[1] = {(s_u[0][b][lane] + s_u[1][b][lane]) + (s_u[2][b][lane] + s_u[3][b][lane])};
-    const float top = fmaxf(fmaxf(s_ml[0][0][r], s_ml[1][0][r]), fmaxf(s_ml[2][0][r], s_ml[3][0][r]));
-    const float all = (s_ml[0][1][r] + s_ml[1][1][r]) + (s_ml[2][1][r] + s_ml[3][1][r]);
-    latent_write<L, 1>(p, sq, row, c * 16 + g * 4, sum, top, all, c == 0 && g == 0);
+    item -= tiles * kPieces;
   }
 }
 
