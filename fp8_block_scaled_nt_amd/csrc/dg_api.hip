@@ -1068,6 +1068,12 @@ size_t kv8_part_floats(int workers, int d) { return (size_t)workers * 2 * 16 * (
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// The scale in units of log2, and not 0: 0 times what is masked would be no mask.
+float latent_scale(float scale) {
+  const float s = scale * 1.44269504088896340736f;
+  return s > 1.17549435e-38f ? s : 1.17549435e-38f;
+}
+
 int check_latent_dim(int latent) {
   if (latent != 256 && latent != 512)
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "the latent must have 256 or 512 values (got %d)", latent);
@@ -1946,7 +1952,7 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   p.out_stride = out_stride;
   p.out_head_stride = out_head_stride;
   p.lse = lse;
-  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.scale_log2 = latent_scale(scale);
   p.causal = causal != 0;
   p.batch = batch;
   p.total = total;
@@ -2003,7 +2009,7 @@ int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint
   p.cu_kv = cu_kv;
   p.out = out;
   p.lse = lse;
-  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.scale_log2 = latent_scale(scale);
   p.causal = causal != 0;
   p.batch = batch;
   p.total = total;

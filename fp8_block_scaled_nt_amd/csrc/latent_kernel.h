@@ -279,6 +279,7 @@ struct LatentAttnParams {
 
 constexpr int kLatentStep = 64;       // tokens of one step
 constexpr float kLatentLead = 8.f;    // log2 of how far the reference is put above the largest score
+constexpr float kLatentLow = -3e38f;  // the reference of a row that has seen no token: any score passes it
 
 // How LDS rows of tokens are turned so that neither the 16 tokens of a row
 // fragment nor the 8 tokens that a transposing read covers at a time meet in a
@@ -346,13 +347,13 @@ __device__ __forceinline__ uint32_t bf16_finite(uint32_t w) {
   return (w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFFu : w;
 }
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) v4u lds_v4u;
 
 // Four bf16 of one channel and four tokens, from token-major rows: lane i of
 // 16 gives the address of four channels of token i / 4 and gets channel i.
-__device__ __forceinline__ v2u lds_turned(const uint8_t* at) {
+__device__ __forceinline__ v2u lds_turned(uint32_t at) {
   typedef short v4s __attribute__((ext_vector_type(4)));
-  return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(lds_u8*)at));
+  return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(uintptr_t)at));
 }
 
 // A barrier that waits for this wave's LDS accesses, and not for the next
@@ -519,7 +520,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int c = 0; c < kC; ++c) u[n][c] = v4f{0.f, 0.f, 0.f, 0.f};
-      m[n] = -__builtin_huge_valf();
+      m[n] = kLatentLow;
     }
 #pragma unroll
     for (int n = 0; n < kN; ++n) l[n] = 0.f;
@@ -593,84 +594,77 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           // would take the registers that q and u need
           int here = lane;
           asm volatile("" : "+v"(here));
-          const int a = here & 15, g = here >> 4;
-          // The next step's tokens set out while the scores are worked out:
-          // piece by piece between the products, which leave room for them.
-          stage_at(s + 1, s + 1 < last ? page1 : -1, buf ^ 1);
-          constexpr int kPerJ = (kDmas + kJ - 1) / kJ;
-          auto stage_of = [&](int j) {
-#pragma unroll
-            for (int i = j * kPerJ; i < (j + 1) * kPerJ && i < kDmas; ++i) stage(i);
-          };
-          // scores: tokens 16 (tw RW + r) + a of the step with rows 16 (rw kN + n) + a
+          const int a = here & 15, g = here >> 4, turn = latent_turn(a);
+          // Scores: tokens 16 (tw RW + r) + a of the step with rows 16 (rw kN + n)
+          // + a, 64 channels at a time.  The next step's tokens set out
+          // meanwhile, piece by piece between the products, which leave room.
           v4f x[RW][kN];
 #pragma unroll
           for (int r = 0; r < RW; ++r)
 #pragma unroll
             for (int n = 0; n < kN; ++n) x[r][n] = v4f{0.f, 0.f, 0.f, 0.f};
-          const int turn = F8 ? a : latent_turn(a);
-          if constexpr (F8) {
-            v4u w[3][RW];
-            float scale[RW][L / 128];
-            auto fetch = [&](int j) {
+          constexpr int kPerJ = (kDmas + kJ - 1) / kJ;
+          auto stage_of = [&](int j, int i) {
+            if (i < kPerJ && j * kPerJ + i < kDmas) stage(j * kPerJ + i);
+          };
+          // piece 8 j + 2 g + h of a bf16 row, 4 j + g of a row of codes
+          const uint32_t at_k = lds_addr(now) + (16 * tw * RW + a) * Lds::kRow + (F8 ? (g ^ a) << 4 : (2 * g ^ turn) << 4);
+          auto key_at = [&](int j, int h, int r) {
+            const uint32_t bits = F8 ? (j & 3) * 64 : (j & 1) * 128 + h * 16;
+            return *(const lds_v4u*)(uintptr_t)((at_k ^ bits) + (F8 ? j / 4 : j / 2) * 256 + r * 16 * Lds::kRow);
+          };
+          v4u k[3][F8 ? 1 : 2][RW];
+          auto fetch_k = [&](int j) {
 #pragma unroll
-              for (int r = 0; r < RW; ++r) w[j % 3][r] = *(const v4u*)(now + (16 * (tw * RW + r) + a) * L + (((4 * j + g) ^ turn) << 4));
-            };
+            for (int r = 0; r < RW; ++r)
+#pragma unroll
+              for (int h = 0; h < (F8 ? 1 : 2); ++h) k[j % 3][h][r] = key_at(j, h, r);
+          };
+          fetch_k(0);
+          fetch_k(1);
+          float scale[RW][F8 ? L / 128 : 1];
+          if constexpr (F8)
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
               const float* const sc = (const float*)(now + Lds::kLatent + Lds::kRope + (tw * RW + r) * 256) + a * (L / 128);
 #pragma unroll
               for (int b = 0; b < L / 128; ++b) scale[r][b] = sc[b];
             }
-            fetch(0);
-            fetch(1);
+          stage_at(s + 1, s + 1 < last ? page1 : -1, buf ^ 1);
+          const uint32_t at_w = lds_addr(wide) + (16 * tw * RW + a) * (2 * L) + ((2 * g ^ turn) << 4);
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-              if (j + 2 < kJ) fetch(j + 2);
-              stage_of(j);
-              __builtin_amdgcn_sched_barrier(0);
+          for (int j = 0; j < kJ; ++j) {
+            if (j + 2 < kJ) fetch_k(j + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            v4u kk[2][RW];
 #pragma unroll
-              for (int r = 0; r < RW; ++r) {
-                const v4u c = w[j % 3][r];
-                const v4u k0 = latent_widen(c[0], c[1], scale[r][j / 2]), k1 = latent_widen(c[2], c[3], scale[r][j / 2]);
+            for (int r = 0; r < RW; ++r) {
+              if constexpr (F8) {
+                const v4u c = k[j % 3][0][r];
+                kk[0][r] = latent_widen(c[0], c[1], scale[r][j / 2]);
+                kk[1][r] = latent_widen(c[2], c[3], scale[r][j / 2]);
                 if (RW == 1 || r == rw) {  // one of the waves that widen them keeps them for the second product
-                  uint8_t* const to = wide + (16 * (tw * RW + r) + a) * (2 * L);
-                  *(v4u*)(to + (((8 * j + 2 * g) ^ latent_turn(a)) << 4)) = k0;
-                  *(v4u*)(to + (((8 * j + 2 * g + 1) ^ latent_turn(a)) << 4)) = k1;
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    *(lds_v4u*)(uintptr_t)((at_w ^ ((j & 1) * 128 + h * 16)) + j / 2 * 256 + r * 16 * 2 * L) = kk[h][r];
                 }
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-                  x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k0), qf[n][2 * j], x[r][n], 0, 0, 0);
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-                  x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k1), qf[n][2 * j + 1], x[r][n], 0, 0, 0);
+              } else {
+                kk[0][r] = k[j % 3][0][r];
+                kk[1][r] = k[j % 3][1][r];
               }
             }
-          } else {
-            v8bf k[3][2][RW];
-            auto fetch = [&](int j) {
+            int i = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int r = 0; r < RW; ++r) {
-                const uint8_t* const from = now + (16 * (tw * RW + r) + a) * (2 * L);
-                k[j % 3][0][r] = *(const v8bf*)(from + (((8 * j + 2 * g) ^ turn) << 4));
-                k[j % 3][1][r] = *(const v8bf*)(from + (((8 * j + 2 * g + 1) ^ turn) << 4));
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+                  x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, kk[h][r]), qf[n][2 * j + h], x[r][n], 0, 0, 0);
+                stage_of(j, i++);
+                if constexpr (!F8) __builtin_amdgcn_sched_barrier(0);
               }
-            };
-            fetch(0);
-            fetch(1);
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-              if (j + 2 < kJ) fetch(j + 2);
-              stage_of(j);
-              __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int r = 0; r < RW; ++r)
-#pragma unroll
-                  for (int n = 0; n < kN; ++n)
-                    x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j % 3][h][r], qf[n][2 * j + h], x[r][n], 0, 0, 0);
-            }
+            for (; i < kPerJ; ++i) stage_of(j, i);
           }
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
@@ -678,44 +672,45 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 #pragma unroll
             for (int j = 0; j < kRopeFrags; ++j) {
               const int slot = P == 64 ? (2 * g + j) ^ (a >> 1 & 7) : g ^ (a >> 2 & 3);
-              const v8bf k = *(const v8bf*)(from + slot * 16);
+              const v8bf kr = *(const v8bf*)(from + slot * 16);
 #pragma unroll
-              for (int n = 0; n < kN; ++n) x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qrf[n][j], x[r][n], 0, 0, 0);
+              for (int n = 0; n < kN; ++n) x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr, qrf[n][j], x[r][n], 0, 0, 0);
             }
           }
-          // t = log2(e) x; lane: row 16 (rw kN + n) + a, tokens 4 g + e of a group of 16
-          bool moves = false;
+          // lane: row 16 (rw kN + n) + a, tokens 4 g + e of a group of 16
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
             const int token = s * kLatentStep + 16 * (tw * RW + r) + 4 * g;
             const bool there = __builtin_amdgcn_readfirstlane(s_there[buf * 4 + tw * RW + r]) != 0;
+            if (MASKED || !there) {
+              asm volatile("");  // a branch: most steps leave it out
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-              x[r][n] *= p.scale_log2;
-              const int seen = !there ? 0 : MASKED ? hi[n] - token : 4;
-              if (MASKED || !there)
+              for (int n = 0; n < kN; ++n) {
+                const int seen = there ? hi[n] - token : 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[r][n][e] = e < seen ? x[r][n][e] : -__builtin_huge_valf();
-#pragma unroll
-              for (int e = 0; e < 4; ++e) moves |= x[r][n][e] > of_wave(m, n);
+              }
             }
           }
           uint8_t* const s_rest = Lds::kRestOverRope ? now + Lds::kLatent : lds + Lds::kRest;
           constexpr int kRestGroup = Lds::kRestOverRope ? 16 * P * 2 : kRows * 32;
           if constexpr (MASKED && Lds::kRestOverRope) lds_barrier();
-          float sum[kN];
+          float sum[kN], most = -__builtin_huge_valf();
           auto weigh = [&]() {
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
               const int row = 16 * (rw * kN + n) + a;
-              const float mine = of_wave(m, n), ref = mine == -__builtin_huge_valf() ? 0.f : mine;
+              const float ref = of_wave(m, n);
               sum[n] = 0.f;
 #pragma unroll
               for (int r = 0; r < RW; ++r) {
                 const int group = tw * RW + r;
                 float w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(x[r][n][e] - ref);
+                for (int e = 0; e < 4; ++e) w[e] = x[r][n][e] * p.scale_log2 - ref;  // what is masked is -inf: the scale is not 0
+                most = fmaxf(most, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(w[e]);
                 sum[n] += (w[0] + w[1]) + (w[2] + w[3]);
                 const v2u packed = {pack2_bf16(w[0], w[1]), pack2_bf16(w[2], w[3])};
                 const int piece = 2 * group + (g >> 1);
@@ -729,9 +724,40 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             }
           };
           weigh();
-          if (__any(moves) && here == 0) s_flag[s & 1] = 1;
+          if (__any(most > 0.f) && here == 0) s_flag[s & 1] = 1;
           lds_barrier();
-          if (s_flag[s & 1]) {
+          // u += c^T p^T, this wave's channels; the first operands are on their
+          // way before it is known that p stays
+          v8bf pf[NT], rest[NT];
+          auto fetch_p = [&](int k) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const int row = 16 * n + a;
+              pf[n] = *(const v8bf*)(lds + Lds::kP + row * 128 + (((4 * k + g) ^ (row >> 1 & 7)) << 4));
+              if constexpr (MASKED) rest[n] = *(const v8bf*)(s_rest + (2 * k + (g >> 1)) * kRestGroup + row * 32 + (g & 1) * 16);
+            }
+          };
+          uint32_t at_v[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int tk = 8 * g + 4 * h + (a >> 2);  // of 32; + 32 for the second half of the step
+            // piece 2 c + (a % 4) / 2 of the row, c = wave kC + i: i comes in by an exclusive or
+            at_v[h] = lds_addr(wide) + tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ latent_turn(tk & 15)) << 4) + (a & 1) * 8;
+          }
+          v4u v[3];
+          auto fetch_v = [&](int k, int c) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const v2u w = lds_turned((at_v[h] ^ (c * 32)) + k * 32 * 2 * L);
+              v[c % 3][2 * h] = w[0];
+              v[c % 3][2 * h + 1] = w[1];
+            }
+          };
+          const int moved = s_flag[s & 1];
+          fetch_p(0);
+          fetch_v(0, 0);
+          fetch_v(0, 1);
+          if (moved) {
             // some row's score passed its reference: all waves move it alike
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
@@ -739,7 +765,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 #pragma unroll
               for (int r = 0; r < RW; ++r) top = fmaxf(top, fmaxf(fmaxf(x[r][n][0], x[r][n][1]), fmaxf(x[r][n][2], x[r][n][3])));
               top = fmaxf(top, __shfl_xor(top, 16, 64));
-              top = fmaxf(top, __shfl_xor(top, 32, 64));
+              top = fmaxf(top, __shfl_xor(top, 32, 64)) * p.scale_log2;
               if (g == 0) s_max[tw * kRows + 16 * (rw * kN + n) + a] = top;
             }
             lds_barrier();
@@ -759,42 +785,21 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             for (int n = 0; n < kN; ++n) l[n] *= of_wave(shrinks, n);
             weigh();
             lds_barrier();
+            fetch_p(0);
           }
           if (tid == 0) s_flag[(s & 1) ^ 1] = 0;
 #pragma unroll
           for (int n = 0; n < kN; ++n) l[n] += sum[n];
-          // u += c^T p^T, this wave's channels
-          const uint8_t* at_v[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int tk = 8 * g + 4 * h + (a >> 2);  // of 32; + 32 for the second half of the step
-            // piece 2 c + (a % 4) / 2 of the row, c = wave kC + i: i comes in by an exclusive or
-            at_v[h] = wide + tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ latent_turn(tk & 15)) << 4) + (a & 1) * 8;
-          }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            v8bf pf[NT], rest[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const int row = 16 * n + a;
-              pf[n] = *(const v8bf*)(lds + Lds::kP + row * 128 + (((4 * k + g) ^ (row >> 1 & 7)) << 4));
-              if constexpr (MASKED) rest[n] = *(const v8bf*)(s_rest + (2 * k + (g >> 1)) * kRestGroup + row * 32 + (g & 1) * 16);
+            if (k) {
+              fetch_p(k);
+              fetch_v(k, 0);
+              fetch_v(k, 1);
             }
-            v4u v[3];
-            auto fetch = [&](int c) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t off = (uint32_t)(uintptr_t)(lds_u8*)at_v[h] ^ (c * 32);
-                const v2u w = lds_turned((const uint8_t*)(lds_u8*)(uintptr_t)(off + k * 32 * 2 * L));
-                v[c % 3][2 * h] = w[0];
-                v[c % 3][2 * h + 1] = w[1];
-              }
-            };
-            fetch(0);
-            fetch(1);
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
-              if (c + 2 < kC) fetch(c + 2);
+              if (c + 2 < kC) fetch_v(k, c + 2);
               __builtin_amdgcn_sched_barrier(0);
               v4u w = v[c % 3];
               if constexpr (MASKED) {
@@ -890,7 +895,7 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
       float m[NT], l[NT];
       v4f u[kPer];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) m[n] = -__builtin_huge_valf(), l[n] = 0.f;
+      for (int n = 0; n < NT; ++n) m[n] = kLatentLow, l[n] = 0.f;
 #pragma unroll
       for (int b = 0; b < kPer; ++b) u[b] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -906,9 +911,9 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
         float was[NT], is[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float top = fmaxf(m[n], ml[n][0]), ref = top == -__builtin_huge_valf() ? 0.f : top;
-          was[n] = __builtin_amdgcn_exp2f(m[n] - ref);
-          is[n] = __builtin_amdgcn_exp2f(ml[n][0] - ref);
+          const float top = fmaxf(m[n], ml[n][0]);
+          was[n] = __builtin_amdgcn_exp2f(m[n] - top);
+          is[n] = __builtin_amdgcn_exp2f(ml[n][0] - top);
           l[n] = l[n] * was[n] + ml[n][1] * is[n];
           m[n] = top;
         }
@@ -932,7 +937,7 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
         v4f out[1] = {{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float f = __builtin_amdgcn_exp2f(s_ml[w][0][r] - (top == -__builtin_huge_valf() ? 0.f : top));
+          const float f = __builtin_amdgcn_exp2f(s_ml[w][0][r] - top);
           sum += s_ml[w][1][r] * f;
           out[0] += s_u[w][wave][lane] * f;
         }
@@ -1012,7 +1017,7 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
   for (int n = 0; n < MT; ++n) {
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) u[n][c] = v4f{0.f, 0.f, 0.f, 0.f};
-    m[n] = -__builtin_huge_valf();
+    m[n] = kLatentLow;
     l[n] = 0.f;
   }
 
@@ -1081,7 +1086,6 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
           }
           v4u pw[MT][2], rest[MT][2];
           uint32_t seen[MT];
-          const float by = MASKED ? 1.f : p.scale_log2;  // what is masked is scaled before it is
 #pragma unroll
           for (int n = 0; n < MT; ++n) {
             // element 4 j + e: token 16 j + 4 g + e
@@ -1090,14 +1094,14 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const bool is = base + 16 * (i / 4) + 4 * g + i % 4 < hi[n];
-                t[n][i] = is ? t[n][i] * p.scale_log2 : -__builtin_huge_valf();
+                t[n][i] = is ? t[n][i] : -__builtin_huge_valf();
                 seen[n] |= is ? 1u << i : 0u;
               }
             }
             float top = t[n][0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) top = fmaxf(top, t[n][i]);
-            top *= by;
+            top *= p.scale_log2;  // what is masked is -inf: the scale is not 0
             if (__any(top > m[n])) {
               top = fmaxf(top, __shfl_xor(top, 16, 64));
               top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -1109,11 +1113,11 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
                 m[n] = ref;
               }
             }
-            const float ref = m[n] == -__builtin_huge_valf() ? 0.f : m[n];
+            const float ref = m[n];
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              const float p0 = __builtin_amdgcn_exp2f(t[n][i] * by - ref), p1 = __builtin_amdgcn_exp2f(t[n][i + 1] * by - ref);
+              const float p0 = __builtin_amdgcn_exp2f(t[n][i] * p.scale_log2 - ref), p1 = __builtin_amdgcn_exp2f(t[n][i + 1] * p.scale_log2 - ref);
               sum[0] += p0;
               sum[1] += p1;
               const uint32_t both = pack2_bf16(p0, p1);
@@ -1132,7 +1136,7 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
               for (int h = 0; h < 2; ++h) {
                 const int tk = 32 * k + 16 * h + 4 * g + (a >> 2);
                 const int piece = D / 8 + 2 * c + (a >> 1 & 1);
-                const v2u w = lds_turned(now + tk * kRow + ((piece ^ latent_turn8(tk & 15)) << 4) + (a & 1) * 8);
+                const v2u w = lds_turned(lds_addr(now) + tk * kRow + ((piece ^ latent_turn8(tk & 15)) << 4) + (a & 1) * 8);
                 v[2 * h] = w[0];
                 v[2 * h + 1] = w[1];
               }
