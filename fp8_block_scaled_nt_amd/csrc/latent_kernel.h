@@ -577,9 +577,12 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
       look(t0 + 1);
 #pragma unroll
       for (int i = 0; i < kDmas; ++i) stage(i);
-      int page1 = page_of(t0 + 1);
+      const int page1 = page_of(t0 + 1);
       look(t0 + 2);
       wait_vmem_all();
+      int page2 = page_of(t0 + 2);
+      look(t0 + 3);
+      stage_at(t0 + 1, t0 + 1 < last ? page1 : -1, 1);
       __syncthreads();
 
       int s = t0;
@@ -603,10 +606,15 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           for (int r = 0; r < RW; ++r)
 #pragma unroll
             for (int n = 0; n < kN; ++n) x[r][n] = v4f{0.f, 0.f, 0.f, 0.f};
-          constexpr int kPerJ = (kDmas + kJ - 1) / kJ;
+          // two pieces every 128 channels and then one, the rest beside the second product
+          constexpr int kEarly = kJ + kJ / 2 < kDmas ? kJ + kJ / 2 : kDmas;
           auto stage_of = [&](int j, int i) {
-            if (i < kPerJ && j * kPerJ + i < kDmas) stage(j * kPerJ + i);
+            const int piece = j + j / 2 + i;
+            if (i < 1 + j % 2 && piece < kEarly) stage(piece);
           };
+          bool there[RW];
+#pragma unroll
+          for (int r = 0; r < RW; ++r) there[r] = s_there[buf * 4 + tw * RW + r] != 0;
           // piece 8 j + 2 g + h of a bf16 row, 4 j + g of a row of codes
           const uint32_t at_k = lds_addr(now) + (16 * tw * RW + a) * Lds::kRow + (F8 ? (g ^ a) << 4 : (2 * g ^ turn) << 4);
           auto key_at = [&](int j, int h, int r) {
@@ -630,7 +638,6 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 #pragma unroll
               for (int b = 0; b < L / 128; ++b) scale[r][b] = sc[b];
             }
-          stage_at(s + 1, s + 1 < last ? page1 : -1, buf ^ 1);
           const uint32_t at_w = lds_addr(wide) + (16 * tw * RW + a) * (2 * L) + ((2 * g ^ turn) << 4);
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
@@ -664,7 +671,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
                 stage_of(j, i++);
                 if constexpr (!F8) __builtin_amdgcn_sched_barrier(0);
               }
-            for (; i < kPerJ; ++i) stage_of(j, i);
+            if constexpr (RW == 1) stage_of(j, i);
           }
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
@@ -681,12 +688,12 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
             const int token = s * kLatentStep + 16 * (tw * RW + r) + 4 * g;
-            const bool there = __builtin_amdgcn_readfirstlane(s_there[buf * 4 + tw * RW + r]) != 0;
-            if (MASKED || !there) {
+            const bool is = __builtin_amdgcn_readfirstlane(there[r]);
+            if (MASKED || !is) {
               asm volatile("");  // a branch: most steps leave it out
 #pragma unroll
               for (int n = 0; n < kN; ++n) {
-                const int seen = there ? hi[n] - token : 0;
+                const int seen = is ? hi[n] - token : 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[r][n][e] = e < seen ? x[r][n][e] : -__builtin_huge_valf();
               }
@@ -728,12 +735,13 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           lds_barrier();
           // u += c^T p^T, this wave's channels; the first operands are on their
           // way before it is known that p stays
-          v8bf pf[NT], rest[NT];
+          constexpr int kAhead = 4, kPf = MASKED ? 1 : 2;  // steps with masks have two pieces of p: half of the tokens at a time
+          v8bf pf[kPf][NT], rest[NT];
           auto fetch_p = [&](int k) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const int row = 16 * n + a;
-              pf[n] = *(const v8bf*)(lds + Lds::kP + row * 128 + (((4 * k + g) ^ (row >> 1 & 7)) << 4));
+              pf[k % kPf][n] = *(const v8bf*)(lds + Lds::kP + row * 128 + (((4 * k + g) ^ (row >> 1 & 7)) << 4));
               if constexpr (MASKED) rest[n] = *(const v8bf*)(s_rest + (2 * k + (g >> 1)) * kRestGroup + row * 32 + (g & 1) * 16);
             }
           };
@@ -744,19 +752,20 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             // piece 2 c + (a % 4) / 2 of the row, c = wave kC + i: i comes in by an exclusive or
             at_v[h] = lds_addr(wide) + tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ latent_turn(tk & 15)) << 4) + (a & 1) * 8;
           }
-          v4u v[3];
-          auto fetch_v = [&](int k, int c) {
+          v4u v[kAhead + 1];
+          auto fetch_v = [&](int i) {  // column tile i % kC, tokens 32 (i / kC) ..
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const v2u w = lds_turned((at_v[h] ^ (c * 32)) + k * 32 * 2 * L);
-              v[c % 3][2 * h] = w[0];
-              v[c % 3][2 * h + 1] = w[1];
+              const v2u w = lds_turned((at_v[h] ^ (i % kC * 32)) + i / kC * 32 * 2 * L);
+              v[i % (kAhead + 1)][2 * h] = w[0];
+              v[i % (kAhead + 1)][2 * h + 1] = w[1];
             }
           };
           const int moved = s_flag[s & 1];
           fetch_p(0);
-          fetch_v(0, 0);
-          fetch_v(0, 1);
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) fetch_v(i);
+          if constexpr (!MASKED) fetch_p(1);
           if (moved) {
             // some row's score passed its reference: all waves move it alike
 #pragma unroll
@@ -786,41 +795,39 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             weigh();
             lds_barrier();
             fetch_p(0);
+            if constexpr (!MASKED) fetch_p(1);
           }
           if (tid == 0) s_flag[(s & 1) ^ 1] = 0;
 #pragma unroll
           for (int n = 0; n < kN; ++n) l[n] += sum[n];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (k) {
-              fetch_p(k);
-              fetch_v(k, 0);
-              fetch_v(k, 1);
-            }
+          for (int i = 0; i < 2 * kC; ++i) {
+            const int c = i % kC, k = i / kC;
+            if (MASKED && i == kC) fetch_p(1);
+            if (i + kAhead < 2 * kC) fetch_v(i + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+            v4u w = v[i % (kAhead + 1)];
+            if constexpr (MASKED) {
+              // a token that some rows see and others do not must reach the
+              // former only: what is not finite has made their sums NaN already
 #pragma unroll
-            for (int c = 0; c < kC; ++c) {
-              if (c + 2 < kC) fetch_v(k, c + 2);
-              __builtin_amdgcn_sched_barrier(0);
-              v4u w = v[c % 3];
-              if constexpr (MASKED) {
-                // a token that some rows see and others do not must reach the
-                // former only: what is not finite has made their sums NaN already
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = bf16_finite(w[e]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), rest[n], u[n][c], 0, 0, 0);
-              }
+              for (int e = 0; e < 4; ++e) w[e] = bf16_finite(w[e]);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), pf[n], u[n][c], 0, 0, 0);
+                u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), rest[n], u[n][c], 0, 0, 0);
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), pf[k % kPf][n], u[n][c], 0, 0, 0);
+            if (kEarly + i < kDmas) stage(kEarly + i);
+            if (i == (kDmas - kEarly < kC ? kC : 2 * kC - 1)) stage_at(s + 2, s + 2 < last ? page2 : -1, buf);  // for the next step to send for
           }
+          static_assert(kDmas - kEarly < 2 * kC, "all pieces have set out before the next ones' places are worked out");
           // the next step has landed, and everybody is done with this one
           wait_vmem_all();
-          page1 = page_of(s + 2);
+          page2 = page_of(s + 3);
           __syncthreads();
-          look(s + 3);
+          look(s + 4);
         }
       };
       const int whole = max(min(all_hi / kLatentStep, last), t0);
