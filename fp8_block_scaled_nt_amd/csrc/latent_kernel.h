@@ -598,7 +598,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           int here = lane;
           asm volatile("" : "+v"(here));
           const int a = here & 15, g = here >> 4, turn = latent_turn(a);
-          // Scores: tokens 16 (tw RW + r) + a of the step with rows 16 (rw kN + n)
+          // Scores: tokens 16 group[r] + a of the step with rows 16 (rw kN + n)
           // + a, 64 channels at a time.  The next step's tokens set out
           // meanwhile, piece by piece between the products, which leave room.
           v4f x[RW][kN];
@@ -612,14 +612,19 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             const int piece = j + j / 2 + i;
             if (i < 1 + j % 2 && piece < kEarly) stage(piece);
           };
+          // this wave's groups of 16 tokens; where two waves widen a group, it is the first of one of them
+          int group[RW];
           bool there[RW];
+          uint32_t at_k[RW];  // piece 2 g of a bf16 row, g of a row of codes
 #pragma unroll
-          for (int r = 0; r < RW; ++r) there[r] = s_there[buf * 4 + tw * RW + r] != 0;
-          // piece 8 j + 2 g + h of a bf16 row, 4 j + g of a row of codes
-          const uint32_t at_k = lds_addr(now) + (16 * tw * RW + a) * Lds::kRow + (F8 ? (g ^ a) << 4 : (2 * g ^ turn) << 4);
+          for (int r = 0; r < RW; ++r) {
+            group[r] = RW == 1 ? wave : tw * 2 + (r ^ rw);
+            there[r] = s_there[buf * 4 + group[r]] != 0;
+            at_k[r] = lds_addr(now) + (16 * group[r] + a) * Lds::kRow + (F8 ? (g ^ a) << 4 : (2 * g ^ turn) << 4);
+          }
           auto key_at = [&](int j, int h, int r) {
             const uint32_t bits = F8 ? (j & 3) * 64 : (j & 1) * 128 + h * 16;
-            return *(const lds_v4u*)(uintptr_t)((at_k ^ bits) + (F8 ? j / 4 : j / 2) * 256 + r * 16 * Lds::kRow);
+            return *(const lds_v4u*)(uintptr_t)((at_k[r] ^ bits) + (F8 ? j / 4 : j / 2) * 256);
           };
           v4u k[3][F8 ? 1 : 2][RW];
           auto fetch_k = [&](int j) {
@@ -634,11 +639,11 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           if constexpr (F8)
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
-              const float* const sc = (const float*)(now + Lds::kLatent + Lds::kRope + (tw * RW + r) * 256) + a * (L / 128);
+              const float* const sc = (const float*)(now + Lds::kLatent + Lds::kRope + group[r] * 256) + a * (L / 128);
 #pragma unroll
               for (int b = 0; b < L / 128; ++b) scale[r][b] = sc[b];
             }
-          const uint32_t at_w = lds_addr(wide) + (16 * tw * RW + a) * (2 * L) + ((2 * g ^ turn) << 4);
+          const uint32_t at_w = lds_addr(wide) + (16 * group[0] + a) * (2 * L) + ((2 * g ^ turn) << 4);
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             if (j + 2 < kJ) fetch_k(j + 2);
@@ -650,11 +655,10 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
                 const v4u c = k[j % 3][0][r];
                 kk[0][r] = latent_widen(c[0], c[1], scale[r][j / 2]);
                 kk[1][r] = latent_widen(c[2], c[3], scale[r][j / 2]);
-                if (RW == 1 || r == rw) {  // one of the waves that widen them keeps them for the second product
+                if (r == 0)  // kept for the second product
 #pragma unroll
                   for (int h = 0; h < 2; ++h)
-                    *(lds_v4u*)(uintptr_t)((at_w ^ ((j & 1) * 128 + h * 16)) + j / 2 * 256 + r * 16 * 2 * L) = kk[h][r];
-                }
+                    *(lds_v4u*)(uintptr_t)((at_w ^ ((j & 1) * 128 + h * 16)) + j / 2 * 256) = kk[h][r];
               } else {
                 kk[0][r] = k[j % 3][0][r];
                 kk[1][r] = k[j % 3][1][r];
@@ -675,7 +679,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           }
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
-            const uint8_t* const from = now + Lds::kLatent + (16 * (tw * RW + r) + a) * (P * 2);
+            const uint8_t* const from = now + Lds::kLatent + (16 * group[r] + a) * (P * 2);
 #pragma unroll
             for (int j = 0; j < kRopeFrags; ++j) {
               const int slot = P == 64 ? (2 * g + j) ^ (a >> 1 & 7) : g ^ (a >> 2 & 3);
@@ -687,7 +691,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           // lane: row 16 (rw kN + n) + a, tokens 4 g + e of a group of 16
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
-            const int token = s * kLatentStep + 16 * (tw * RW + r) + 4 * g;
+            const int token = s * kLatentStep + 16 * group[r] + 4 * g;
             const bool is = __builtin_amdgcn_readfirstlane(there[r]);
             if (MASKED || !is) {
               asm volatile("");  // a branch: most steps leave it out
@@ -711,7 +715,6 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
               sum[n] = 0.f;
 #pragma unroll
               for (int r = 0; r < RW; ++r) {
-                const int group = tw * RW + r;
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = x[r][n][e] * p.scale_log2 - ref;  // what is masked is -inf: the scale is not 0
@@ -720,12 +723,12 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
                 for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(w[e]);
                 sum[n] += (w[0] + w[1]) + (w[2] + w[3]);
                 const v2u packed = {pack2_bf16(w[0], w[1]), pack2_bf16(w[2], w[3])};
-                const int piece = 2 * group + (g >> 1);
+                const int piece = 2 * group[r] + (g >> 1);
                 *(v2u*)(lds + Lds::kP + row * 128 + ((piece ^ (row >> 1 & 7)) << 4) + (g & 1) * 8) = packed;
                 if constexpr (MASKED) {
                   const v2u rest = {pack2_bf16(w[0] - __uint_as_float(packed[0] << 16), w[1] - __uint_as_float(packed[0] & 0xFFFF0000u)),
                                     pack2_bf16(w[2] - __uint_as_float(packed[1] << 16), w[3] - __uint_as_float(packed[1] & 0xFFFF0000u))};
-                  *(v2u*)(s_rest + group * kRestGroup + row * 32 + g * 8) = rest;
+                  *(v2u*)(s_rest + group[r] * kRestGroup + row * 32 + g * 8) = rest;
                 }
               }
             }
