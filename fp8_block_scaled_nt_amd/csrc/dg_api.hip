@@ -243,6 +243,8 @@ constexpr const char* kW4RowsName = "w4_rows";
 constexpr const char* kW4TileName = "w4_tile";
 constexpr const char* kKv8Split = "kv8_split";
 constexpr const char* kKv8Prompt = "kv8_prompt";
+// rows of a tile of absorbed attention over latents
+constexpr const char* kLatentRows[] = {"latent_rows16", "latent_rows32", "latent_rows64"};
 
 // DG_FORCE_CONFIG=<name> pins the configuration of the variant it names (for
 // tuning sweeps); an unknown name is an error rather than silently ignored.
@@ -256,6 +258,7 @@ int forced_name(const char** name) {
   for (int i = 0; i < cnt; ++i) known = known || strcmp(t[i].name, e) == 0;
   known = known || find_skinny(e) != nullptr || strcmp(e, kKv8Split) == 0 || strcmp(e, kKv8Prompt) == 0 ||
           strcmp(e, kW4RowsName) == 0 || strcmp(e, kW4TileName) == 0;
+  for (const char* rows : kLatentRows) known = known || strcmp(e, rows) == 0;
   if (!known) return fail(DG_ERR_INVALID_ARGUMENT, "DG_FORCE_CONFIG names no configuration: %s", e);
   *name = e;
   return DG_OK;
@@ -1117,11 +1120,25 @@ int check_strided(const void* x, int64_t stride, int64_t head_stride, int heads,
   return DG_OK;
 }
 
-// Tiles of 16 rows that a workgroup of absorbed attention takes at once: as
-// many as one sequence's queries fill, at most four.
-int latent_row_tiles(int max_q, int h_q) {
+// Tiles of 16 rows that a workgroup of absorbed attention takes at once: as many as one sequence's queries fill, up to four, if there are more
+// than four 64-token steps of such tiles for each workgroup; else one, as a
+// large tile's only step and part then cost more than reading the tokens again
+// (us with 16 / 32 / 64 rows, bf16, latents of 512, 128 heads: 1 x 4096 20 / 30 / 32,
+// 8 x 1024 23 / 28 / 33, 1 x 16384 30 / 34 / 40, 32 x 1024 35 / 35 / 38, 4 x 65536
+// 244 / 148 / 112; 64 heads: 64 x 512 24 / 29 / 34; 32 heads: 1 x 8192 23 / 32, 16 x
+// 8192 49 / 47; e4m3, 128 heads: 32 x up to 4096 94 / 72 / 70; 16 heads, 256 new
+// of 2048 61 / 50 / 50).  How many steps there are the host knows from the table and
+// the pool only: with tables much wider than the sequences it takes more rows.
+int latent_row_tiles(int max_q, int h_q, long long tokens, int workers, int* tiles) {
   const long long rows = (long long)max_q * h_q;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  *tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const long long each = (rows + 16 * *tiles - 1) / (16 * *tiles);
+  if ((tokens + 63) / 64 <= 4LL * workers / each) *tiles = 1;
+  const char* name;
+  if (int s = forced_name(&name)) return s;
+  for (int i = 0; name && i < 3; ++i)
+    if (strcmp(name, kLatentRows[i]) == 0) *tiles = 1 << i;
+  return DG_OK;
 }
 size_t latent_part_floats(int workers, int tiles, int latent) { return (size_t)workers * 2 * 16 * tiles * (latent + 2); }
 size_t latent_part_bytes(int workers, int tiles, int latent) {
@@ -1911,7 +1928,9 @@ int dg_latent_attention_workspace_size(int latent_dim, int max_q, int h_q, size_
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
-  *bytes = latent_part_bytes(info->cus, latent_row_tiles(max_q, h_q), latent_dim);
+  int tiles;
+  if (int s = latent_row_tiles(max_q, h_q, LLONG_MAX / 4096, info->cus, &tiles)) return s;  // the most that any tokens take
+  *bytes = latent_part_bytes(info->cus, tiles, latent_dim);
   return ok();
 }
 
@@ -1959,7 +1978,10 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   p.most = max_q;
   p.h_q = h_q;
   p.workers = info->cus;
-  const int tiles = latent_row_tiles(max_q, h_q);
+  int tiles;
+  const long long all_blocks = (long long)batch * max_blocks;
+  const long long tokens = (all_blocks < num_blocks ? all_blocks : num_blocks) * block;
+  if (int s = latent_row_tiles(max_q, h_q, tokens, p.workers, &tiles)) return s;
   const LatentKernel k = latent_attn(latent_dim, cache_scales != nullptr, tiles);
   const int row_tiles = (int)(((long long)max_q * h_q + 16 * tiles - 1) / (16 * tiles));
   p.together = (long long)max_q * batch == total && row_tiles <= 8 ? row_tiles : 1;

@@ -900,6 +900,7 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
     for (; item < tiles * kPieces; item += gridDim.x) {
       const int worker = s_tile[item / kPieces], b0 = item % kPieces * kPer;
       const LatentCut cut = p.cut[worker];
+      const LatentSeq sq = latent_seq_uniform<kRows>(p, cut.seq);
       // the parts after the first are their workgroups' first
       auto slot_of = [&](int i) { return (size_t)(i == 0 ? cut.slot : (worker + i * p.together) * 2); };
       float m[NT], l[NT];
@@ -940,7 +941,6 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
       for (int b = 0; b < kPer; ++b) s_u[wave][b][lane] = u[b];
       __syncthreads();
       {
-        const LatentSeq sq = latent_seq_uniform<kRows>(p, cut.seq);
         const int block = b0 + wave, n = block % NT, c = block / NT, r = 16 * n + a, row = cut.tile * kRows + r;
         const float top = fmaxf(fmaxf(s_ml[0][0][r], s_ml[1][0][r]), fmaxf(s_ml[2][0][r], s_ml[3][0][r]));
         float sum = 0.f;
