@@ -717,7 +717,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
               for (int r = 0; r < RW; ++r) {
                 float w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = x[r][n][e] * p.scale_log2 - ref;  // what is masked is -inf: the scale is not 0
+                for (int e = 0; e < 4; ++e) w[e] = __builtin_fmaf(x[r][n][e], p.scale_log2, -ref);  // what is masked is -inf: the scale is not 0
                 most = fmaxf(most, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(w[e]);
@@ -1031,6 +1031,14 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
     l[n] = 0.f;
   }
 
+  // Where a lane finds its pieces in a step's rows: of a key (token a, channels 8
+  // g ..), of a rope part, and of four values (token 4 g + a / 4, channels 4 (a %
+  // 4) ..); other channels come in by an exclusive or, other tokens by an offset.
+  const uint32_t lane_k = a * kRow + ((g ^ latent_turn8(a)) << 4);
+  const uint32_t lane_r = kLatentStep * kRow + a * 2 * R + ((R == 64 ? g ^ (a >> 1 & 7) : g ^ (a >> 2 & 3)) << 4);
+  const int tk = 4 * g + (a >> 2);
+  const uint32_t lane_v = tk * kRow + (((D / 8 + (a >> 1 & 1)) ^ latent_turn8(tk)) << 4) + (a & 1) * 8;
+
   // This wave's 16 tokens of a step.
   auto stage = [&](int step, int buf) {
     const int token = step * kLatentStep + wave * 16;
@@ -1071,6 +1079,7 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
         block_barrier();
         if (base < wave_hi) {
           float t[MT][16];
+          const uint32_t at = lds_addr(now);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             v4f x[MT];
@@ -1078,16 +1087,11 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
             for (int n = 0; n < MT; ++n) x[n] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < kN + kR; ++k) {
-              const int row = 16 * j + a;
-              v8bf key;
-              if (k < kN) {
-                key = *(const v8bf*)(now + row * kRow + (((4 * k + g) ^ latent_turn8(a)) << 4));
-              } else {
-                const int piece = 4 * (k - kN) + g;
-                key = *(const v8bf*)(now + kLatentStep * kRow + row * 2 * R + ((R == 64 ? piece ^ (a >> 1 & 7) : piece ^ (a >> 2 & 3)) << 4));
-              }
+              const v4u key = k < kN ? *(const lds_v4u*)(uintptr_t)(((at + lane_k) ^ (k * 64)) + j * 16 * kRow)
+                                     : *(const lds_v4u*)(uintptr_t)(((at + lane_r) ^ ((k - kN) * 64)) + j * 32 * R);
 #pragma unroll
-              for (int n = 0; n < MT; ++n) x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key, qf[n][k], x[n], 0, 0, 0);
+              for (int n = 0; n < MT; ++n)
+                x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, key), qf[n][k], x[n], 0, 0, 0);
             }
 #pragma unroll
             for (int n = 0; n < MT; ++n)
@@ -1104,30 +1108,35 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const bool is = base + 16 * (i / 4) + 4 * g + i % 4 < hi[n];
-                t[n][i] = is ? t[n][i] : -__builtin_huge_valf();
+                t[n][i] = is ? t[n][i] : -__builtin_huge_valf();  // the scale is not 0: it stays so
                 seen[n] |= is ? 1u << i : 0u;
               }
             }
-            float top = t[n][0];
+            // how far the scores are from the reference; the largest is taken of
+            // these, as products' results would be made canonical for it first
+            float d[16], top = -__builtin_huge_valf();
 #pragma unroll
-            for (int i = 1; i < 16; ++i) top = fmaxf(top, t[n][i]);
-            top *= p.scale_log2;  // what is masked is -inf: the scale is not 0
-            if (__any(top > m[n])) {
+            for (int i = 0; i < 16; ++i) d[i] = __builtin_fmaf(t[n][i], p.scale_log2, -m[n]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, d[i]);
+            if (__any(top > 0.f)) {
+              top = -__builtin_huge_valf();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) top = fmaxf(top, t[n][i]);
               top = fmaxf(top, __shfl_xor(top, 16, 64));
-              top = fmaxf(top, __shfl_xor(top, 32, 64));
-              if (top > m[n]) {
-                const float ref = top + kLatentLead, shrink = __builtin_amdgcn_exp2f(m[n] - ref);
-                l[n] *= shrink;
+              top = fmaxf(top, __shfl_xor(top, 32, 64)) * p.scale_log2;
+              const float ref = top > m[n] ? top + kLatentLead : m[n], shrink = top > m[n] ? __builtin_amdgcn_exp2f(m[n] - ref) : 1.f;
+              l[n] *= shrink;
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) u[n][c] *= shrink;
-                m[n] = ref;
-              }
+              for (int c = 0; c < D / 16; ++c) u[n][c] *= shrink;
+              m[n] = ref;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) d[i] = __builtin_fmaf(t[n][i], p.scale_log2, -ref);
             }
-            const float ref = m[n];
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              const float p0 = __builtin_amdgcn_exp2f(t[n][i] * p.scale_log2 - ref), p1 = __builtin_amdgcn_exp2f(t[n][i + 1] * p.scale_log2 - ref);
+              const float p0 = __builtin_amdgcn_exp2f(d[i]), p1 = __builtin_amdgcn_exp2f(d[i + 1]);
               sum[0] += p0;
               sum[1] += p1;
               const uint32_t both = pack2_bf16(p0, p1);
@@ -1138,15 +1147,14 @@ __global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(La
             l[n] += sum[0] + sum[1];
           }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int c = 0; c < D / 16; ++c) {
+            const uint32_t at_v = (at + lane_v) ^ (c * 32);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
+            for (int k = 0; k < 2; ++k) {
               v4u v;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int tk = 32 * k + 16 * h + 4 * g + (a >> 2);
-                const int piece = D / 8 + 2 * c + (a >> 1 & 1);
-                const v2u w = lds_turned(lds_addr(now) + tk * kRow + ((piece ^ latent_turn8(tk & 15)) << 4) + (a & 1) * 8);
+                const v2u w = lds_turned(at_v + (32 * k + 16 * h) * kRow);
                 v[2 * h] = w[0];
                 v[2 * h + 1] = w[1];
               }
