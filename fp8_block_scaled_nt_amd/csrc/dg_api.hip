@@ -1916,7 +1916,8 @@ int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const
   const bool f8 = cache_scales != nullptr;
   const void* fn = latent_dim == 512 ? latent_gather_fn<512>(f8) : latent_gather_fn<256>(f8);
   void* args[] = {&p};
-  return launch_plain("latent_gather", fn, dim3((total + 3) / 4), 256, args, stream);
+  constexpr int kRows = 4 * dg::kLatentGather;
+  return launch_plain("latent_gather", fn, dim3((total + kRows - 1) / kRows), 256, args, stream);
 }
 
 int dg_latent_attention_workspace_size(int latent_dim, int max_q, int h_q, size_t* bytes) {

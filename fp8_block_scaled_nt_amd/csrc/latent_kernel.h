@@ -211,32 +211,58 @@ __device__ __forceinline__ v4u latent_widen(uint32_t lo, uint32_t hi, float scal
   return r;
 }
 
-// One wave takes one token.
+// One wave takes eight rows; a lane takes 16 bytes of a token at a time, so
+// that a load brings 1 KB of one to four tokens, and all of them are on their
+// way together.
+constexpr int kLatentGather = 8;  // rows of a wave
+
 template <int L, bool F8>
 __global__ __launch_bounds__(256) void latent_gather_kernel(LatentGatherParams p) {
-  constexpr int P = L / 8;
+  constexpr int P = L / 8, kLanes = F8 ? L / 16 : L / 8, kAt = 64 / kLanes;  // lanes of a token, tokens of a load
   const int lane = threadIdx.x & 63;
-  const int t = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
-  if (t >= p.total) return;
-  const int seq = __builtin_amdgcn_readfirstlane(latent_seq_of(p.cu, p.batch, t));
-  if (seq >= p.batch) return;
-  const int i = t - p.cu[seq];
-  const long long pos64 = (long long)(p.starts ? max(p.starts[seq], 0) : 0) + i;
-  if (i < 0 || pos64 > 0x7FFFFFFFLL) return;
-  const int pos = (int)pos64;
-  const int page = latent_page(p.c, seq, pos);
-  if (page < 0) return;
-  const size_t row = ((size_t)page << p.c.block_log2) + (pos & (p.c.block - 1));
-  if (lane * 8 < P) *(v4u*)(p.rope + (size_t)t * P + lane * 8) = *(const v4u*)(p.c.rope + row * P + lane * 8);
-  if (lane * 8 >= L) return;
-  v4u x;
-  if constexpr (F8) {
-    const uint2 w = *(const uint2*)(p.c.latent + row * L + lane * 8);
-    x = latent_widen(w.x, w.y, p.c.scales[row * (L / 128) + lane / 16]);
-  } else {
-    x = *(const v4u*)(p.c.latent + (row * L + lane * 8) * 2);
+  const int row0 = __builtin_amdgcn_readfirstlane(((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6)) * kLatentGather);
+  if (row0 >= p.total) return;
+  const int seq0 = __builtin_amdgcn_readfirstlane(latent_seq_of(p.cu, p.batch, row0));
+  // where row t lies in the cache, or -1
+  auto place = [&](int t) -> long long {
+    int seq = seq0;
+    while (seq < p.batch && p.cu[seq + 1] <= t) ++seq;  // as a rule none: t is of the wave's first sequence
+    if (t >= p.total || seq >= p.batch) return -1;
+    const int i = t - p.cu[seq];
+    const long long pos = (long long)(p.starts ? max(p.starts[seq], 0) : 0) + i;
+    if (i < 0 || pos > 0x7FFFFFFFLL) return -1;
+    const int page = latent_page(p.c, seq, (int)pos);
+    return page < 0 ? -1 : ((long long)page << p.c.block_log2) + ((int)pos & (p.c.block - 1));
+  };
+  // lane t of the first eight finds row t's place for all
+  const long long mine = place(row0 + lane % kLatentGather);
+  auto place_of = [&](int t) { return __shfl(mine, t, 64); };
+  v4u x[kLatentGather / kAt];
+  float scale[kLatentGather / kAt];
+  const int part = lane % kLanes;
+#pragma unroll
+  for (int i = 0; i < kLatentGather / kAt; ++i) {
+    const long long at = max(place_of(i * kAt + lane / kLanes), 0LL);  // some token there is: its bytes are not kept
+    x[i] = *(const v4u*)(p.c.latent + at * (F8 ? L : 2 * L) + part * 16);
+    if constexpr (F8) scale[i] = p.c.scales[at * (L / 128) + part / 8];
   }
-  *(v4u*)(p.latent + (size_t)t * L + lane * 8) = x;
+  constexpr int kRopeLanes = P / 8, kRopeAt = 64 / kRopeLanes < kLatentGather ? 64 / kRopeLanes : kLatentGather;
+  const int r = lane / kRopeLanes % kRopeAt;
+  const long long rope_at = place_of(r);
+  const v4u rope = *(const v4u*)(p.c.rope + max(rope_at, 0LL) * P + lane % kRopeLanes * 8);
+  if (rope_at >= 0 && lane < kRopeAt * kRopeLanes) *(v4u*)(p.rope + (size_t)(row0 + r) * P + lane % kRopeLanes * 8) = rope;
+#pragma unroll
+  for (int i = 0; i < kLatentGather / kAt; ++i) {
+    const int t = i * kAt + lane / kLanes;
+    if (place_of(t) < 0) continue;
+    uint16_t* const to = p.latent + (size_t)(row0 + t) * L + part * (F8 ? 16 : 8);
+    if constexpr (F8) {
+      *(v4u*)to = latent_widen(x[i][0], x[i][1], scale[i]);
+      *(v4u*)(to + 8) = latent_widen(x[i][2], x[i][3], scale[i]);
+    } else {
+      *(v4u*)to = x[i];
+    }
+  }
 }
 
 // ---- attention, absorbed
