@@ -639,53 +639,67 @@ def empty_latent_cache(num_blocks, latent=512, block=64, fmt="e4m3", device="cud
             torch.empty((num_blocks, block, latent // 128), dtype=torch.float32, device=device) if fmt == "e4m3" else None)
 
 
+_Tensor, _BF16, _F32, _I32, _E4M3 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+
+
+def _plain(t, name, dtype, ndim):
+    """_need for one dtype, in one expression where it passes."""
+    if type(t) is not _Tensor or t.dtype is not dtype or t.ndim != ndim or not t.is_cuda or not t.is_contiguous():
+        _need(t, name, (dtype,), ndim)
+
+
 def _latent_shape(cache, block_table, cu):
     """(latent, rope, scales pointers, L, block, num_blocks, max_blocks, batch) of a cache and its tables, checked."""
     latent, rope, scales = cache
-    _need(latent, "latent", (torch.bfloat16,) if scales is None else _FP8, 3)
-    _need(rope, "rope", (torch.bfloat16,), 3)
-    _need(block_table, "block_table", (torch.int32,), 2)
-    _need(cu, "cu", (torch.int32,), 1)
+    if scales is None:
+        _plain(latent, "latent", _BF16, 3)
+    else:
+        if type(latent) is not _Tensor or latent.dtype is not _E4M3 or not latent.is_cuda or not latent.is_contiguous():
+            _need(latent, "latent", _FP8, 3)
+        _plain(scales, "scales", _F32, 3)
+    _plain(rope, "rope", _BF16, 3)
+    _plain(block_table, "block_table", _I32, 2)
+    _plain(cu, "cu", _I32, 1)
     num_blocks, block, dim = latent.shape
     if rope.shape != (num_blocks, block, dim // 8):
         raise ValueError(f"rope {tuple(rope.shape)} does not fit latent {tuple(latent.shape)}")
-    if scales is not None:
-        _need(scales, "scales", (torch.float32,), 3)
-        if scales.shape != (num_blocks, block, dim // 128):
-            raise ValueError(f"scales {tuple(scales.shape)} do not fit latent {tuple(latent.shape)}")
+    if scales is not None and scales.shape != (num_blocks, block, dim // 128):
+        raise ValueError(f"scales {tuple(scales.shape)} do not fit latent {tuple(latent.shape)}")
     batch, max_blocks = block_table.shape
-    if cu.shape[0] != batch + 1:
+    if len(cu) != batch + 1:
         raise ValueError("the block table and cu (batch + 1) disagree on the batch")
     return (latent.data_ptr(), rope.data_ptr(), None if scales is None else scales.data_ptr(), dim, block, num_blocks,
             max_blocks, batch)
 
 
 def _lengths(x, name, batch):
-    _need(x, name, (torch.int32,), 1)
-    if x.shape[0] != batch:
-        raise ValueError(f"{name} must hold {batch} lengths, got {x.shape[0]}")
+    _plain(x, name, _I32, 1)
+    if len(x) != batch:
+        raise ValueError(f"{name} must hold {batch} lengths, got {len(x)}")
     return x.data_ptr()
 
 
 def _rows(x, name, d):
     """Checks bf16 [total, d] with packed values; returns (total, elements from token to token)."""
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
+    if not isinstance(x, _Tensor) or x.dtype is not _BF16 or x.ndim != 2 or not x.is_cuda:
         raise TypeError(f"{name} must be a bf16 device tensor [tokens, d]")
     total, dim = x.shape
-    if dim != d or (x.stride(1) != 1 and d > 1):
+    stride, s1 = x.stride()
+    if dim != d or (s1 != 1 and d > 1):
         raise ValueError(f"{name} must be [tokens, {d}] with packed values, got {tuple(x.shape)}")
-    return total, x.stride(0) if total > 1 else -(-d // 8) * 8
+    return total, stride if total > 1 else -(-d // 8) * 8
 
 
 def _heads(x, name, heads, d):
-    """Checks bf16 [total, heads, d] with packed values; returns (total, elements from token to token, from head to head)."""
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 3 or not x.is_cuda:
+    """Checks bf16 [total, heads, d] with packed values; returns (total, heads, elements from token to token, from head to head)."""
+    if not isinstance(x, _Tensor) or x.dtype is not _BF16 or x.ndim != 3 or not x.is_cuda:
         raise TypeError(f"{name} must be a bf16 device tensor [tokens, heads, d]")
     total, h, dim = x.shape
-    if dim != d or (heads is not None and h != heads) or (x.stride(2) != 1 and d > 1):
+    stride, sh, s2 = x.stride()
+    if dim != d or (heads is not None and h != heads) or (s2 != 1 and d > 1):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {d}] with packed values, "
                          f"got {tuple(x.shape)}")
-    return total, x.stride(0) if total > 1 else 0, x.stride(1) if h > 1 else d
+    return total, h, stride if total > 1 else 0, sh if h > 1 else d
 
 
 def latent_append(latent, rope, cache, block_table, ctx_lens, cu_new, max_new, angles, norm=None, eps=1e-6, q_rope=None,
@@ -702,19 +716,19 @@ def latent_append(latent, rope, cache, block_table, ctx_lens, cu_new, max_new, a
     if total != total_r:
         raise ValueError(f"latent holds {total} tokens, rope {total_r}")
     ctx = _lengths(ctx_lens, "ctx_lens", batch)
-    _need(angles, "angles", (torch.float32,), 2)
-    if angles.shape[1] != dim // 8:
+    _plain(angles, "angles", _F32, 2)
+    positions, width = angles.shape
+    if width != dim // 8:
         raise ValueError(f"angles must be [positions, {dim // 8}], got {tuple(angles.shape)}")
     if norm is not None:
-        _need(norm, "norm", (torch.bfloat16,), 1)
-        if norm.shape[0] != dim:
-            raise ValueError(f"norm must hold {dim} values, got {norm.shape[0]}")
+        _plain(norm, "norm", _BF16, 1)
+        if len(norm) != dim:
+            raise ValueError(f"norm must hold {dim} values, got {len(norm)}")
     heads, q, q_to = 0, (None, 0, 0), (None, 0, 0)
     if q_rope is not None:
         q_out = q_rope if q_out is None else q_out
-        total_q, qs, qh = _heads(q_rope, "q_rope", None, dim // 8)
-        heads = q_rope.shape[1]
-        total_o, os_, oh = _heads(q_out, "q_out", heads, dim // 8)
+        total_q, heads, qs, qh = _heads(q_rope, "q_rope", None, dim // 8)
+        total_o, _, os_, oh = _heads(q_out, "q_out", heads, dim // 8)
         if total_q != total or total_o != total:
             raise ValueError(f"latent holds {total} tokens, q_rope {total_q}, q_out {total_o}")
         if heads:
@@ -722,7 +736,7 @@ def latent_append(latent, rope, cache, block_table, ctx_lens, cu_new, max_new, a
     elif q_out is not None:
         raise ValueError("q_out without q_rope")
     _check(lib().dg_latent_append(latent.data_ptr(), ls, rope.data_ptr(), rs, at_latent, at_rope, at_scales,
-                                  block_table.data_ptr(), ctx, cu_new.data_ptr(), angles.data_ptr(), angles.shape[0],
+                                  block_table.data_ptr(), ctx, cu_new.data_ptr(), angles.data_ptr(), positions,
                                   None if norm is None else norm.data_ptr(), eps, *q, *q_to, interleaved, batch, total,
                                   max_new, heads, dim, block, num_blocks, max_blocks, _stream()))
     return cache
@@ -733,9 +747,9 @@ def latent_gather(cache, block_table, cu, latent, rope, starts=None):
     [total, L]) and rope (bf16 [total, L/8]) is token starts[i] + j (starts None:
     j) of sequence i.  cu: int32 [batch + 1] running sums of the rows."""
     at_latent, at_rope, at_scales, dim, block, num_blocks, max_blocks, batch = _latent_shape(cache, block_table, cu)
-    _need(latent, "latent", (torch.bfloat16,), 2)
-    _need(rope, "rope", (torch.bfloat16,), 2)
-    total = latent.shape[0]
+    _plain(latent, "latent", _BF16, 2)
+    _plain(rope, "rope", _BF16, 2)
+    total = len(latent)
     if latent.shape != (total, dim) or rope.shape != (total, dim // 8):
         raise ValueError(f"rows must be [tokens, {dim}] and [tokens, {dim // 8}], got {tuple(latent.shape)}, {tuple(rope.shape)}")
     _check(lib().dg_latent_gather(at_latent, at_rope, at_scales, block_table.data_ptr(),
@@ -748,7 +762,7 @@ def latent_gather(cache, block_table, cu, latent, rope, starts=None):
 def _need_lse(lse, total, heads):
     if lse is None:
         return None
-    _need(lse, "lse", (torch.float32,), 2)
+    _plain(lse, "lse", _F32, 2)
     if lse.shape != (total, heads):
         raise ValueError(f"lse must be {(total, heads)}, got {tuple(lse.shape)}")
     return lse.data_ptr()
@@ -762,10 +776,9 @@ def latent_attention(q, q_rope, cache, block_table, kv_lens, cu_q, max_q, out, l
     token to token and head to head.  kv_lens counts the queries' own tokens;
     scale: (3/8 L) ** -0.5 if None, that of heads of L/4 + L/8 values."""
     at_latent, at_rope, at_scales, dim, block, num_blocks, max_blocks, batch = _latent_shape(cache, block_table, cu_q)
-    total, qs, qh = _heads(q, "q", None, dim)
-    heads = q.shape[1]
-    total_r, rs, rh = _heads(q_rope, "q_rope", heads, dim // 8)
-    total_o, os_, oh = _heads(out, "out", heads, dim)
+    total, heads, qs, qh = _heads(q, "q", None, dim)
+    total_r, _, rs, rh = _heads(q_rope, "q_rope", heads, dim // 8)
+    total_o, _, os_, oh = _heads(out, "out", heads, dim)
     if total_r != total or total_o != total:
         raise ValueError(f"q holds {total} tokens, q_rope {total_r}, out {total_o}")
     _check(lib().dg_latent_attention(q.data_ptr(), qs, qh, q_rope.data_ptr(), rs, rh, at_latent, at_rope, at_scales,
@@ -790,11 +803,12 @@ def latent_expanded_attention(q, kv, k_rope, cu_q, cu_kv, max_q, out, lse=None, 
     parts and values), k_rope (bf16 [total_kv, D/2]); out (bf16 [total, h, D]) and
     lse (fp32 [total, h], or None) are written in place.  cu_q, cu_kv: int32
     [batch + 1] running sums; a sequence's queries are its last tokens."""
-    _need(cu_q, "cu_q", (torch.int32,), 1)
-    _need(cu_kv, "cu_kv", (torch.int32,), 1)
-    _need(out, "out", (torch.bfloat16,), 3)
+    _plain(cu_q, "cu_q", _I32, 1)
+    _plain(cu_kv, "cu_kv", _I32, 1)
+    _plain(out, "out", _BF16, 3)
     total, heads, dim = out.shape
-    if cu_q.shape != cu_kv.shape or cu_q.shape[0] < 1:
+    batch = len(cu_q) - 1
+    if len(cu_kv) != batch + 1 or batch < 0:
         raise ValueError("cu_q and cu_kv must hold batch + 1 running sums each")
     total_q, qs = _packed(q, "q", heads, dim + dim // 2)
     total_kv, ks = _packed(kv, "kv", heads, 2 * dim)
@@ -805,5 +819,5 @@ def latent_expanded_attention(q, kv, k_rope, cu_q, cu_kv, max_q, out, lse=None, 
                                               cu_q.data_ptr(), cu_kv.data_ptr(), out.data_ptr(),
                                               _need_lse(lse, total, heads),
                                               (dim + dim // 2) ** -0.5 if scale is None else scale, causal,
-                                              cu_q.shape[0] - 1, total, total_kv, max_q, heads, dim, _stream()))
+                                              batch, total, total_kv, max_q, heads, dim, _stream()))
     return out
