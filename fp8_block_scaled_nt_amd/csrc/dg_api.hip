@@ -1129,16 +1129,13 @@ int check_strided(const void* x, int64_t stride, int64_t head_stride, int heads,
 // 8192 49 / 47; e4m3, 128 heads: 32 x up to 4096 94 / 72 / 70; 16 heads, 256 new
 // of 2048 61 / 50 / 50).  How many steps there are the host knows from the table and
 // the pool only: with tables much wider than the sequences it takes more rows.
-int latent_row_tiles(int max_q, int h_q, long long tokens, int workers, int* tiles) {
+int latent_row_tiles(int max_q, int h_q, long long tokens, int workers, const char* forced) {
+  for (int i = 0; forced && i < 3; ++i)
+    if (strcmp(forced, kLatentRows[i]) == 0) return 1 << i;
   const long long rows = (long long)max_q * h_q;
-  *tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  const long long each = (rows + 16 * *tiles - 1) / (16 * *tiles);
-  if ((tokens + 63) / 64 <= 4LL * workers / each) *tiles = 1;
-  const char* name;
-  if (int s = forced_name(&name)) return s;
-  for (int i = 0; name && i < 3; ++i)
-    if (strcmp(name, kLatentRows[i]) == 0) *tiles = 1 << i;
-  return DG_OK;
+  const int tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const long long each = (rows + 16 * tiles - 1) / (16 * tiles);
+  return each > 0 && (tokens + 63) / 64 <= 4LL * workers / each ? 1 : tiles;
 }
 size_t latent_part_floats(int workers, int tiles, int latent) { return (size_t)workers * 2 * 16 * tiles * (latent + 2); }
 size_t latent_part_bytes(int workers, int tiles, int latent) {
@@ -1926,11 +1923,12 @@ int dg_latent_attention_workspace_size(int latent_dim, int max_q, int h_q, size_
   if (int s = check_latent_dim(latent_dim)) return s;
   if (max_q < 0) return fail(DG_ERR_INVALID_ARGUMENT, "max_q must be >= 0 (got %d)", max_q);
   if (int s = check_latent_rows(max_q, h_q)) return s;
+  const char* forced;
+  if (int s = forced_name(&forced)) return s;
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
-  int tiles;
-  if (int s = latent_row_tiles(max_q, h_q, LLONG_MAX / 4096, info->cus, &tiles)) return s;  // the most that any tokens take
+  const int tiles = latent_row_tiles(max_q, h_q, LLONG_MAX / 4096, info->cus, forced);  // the most that any tokens take
   *bytes = latent_part_bytes(info->cus, tiles, latent_dim);
   return ok();
 }
@@ -1956,6 +1954,8 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   if (!aligned4(lse) || !aligned4(kv_lens) || !aligned4(cu_q))
     return fail(DG_ERR_MISALIGNED, "lse and lengths must be 4-byte aligned");
   if (batch == 0 || total == 0 || max_q == 0) return ok();
+  const char* forced;
+  if (int s = forced_name(&forced)) return s;
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
@@ -1979,10 +1979,9 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   p.most = max_q;
   p.h_q = h_q;
   p.workers = info->cus;
-  int tiles;
   const long long all_blocks = (long long)batch * max_blocks;
   const long long tokens = (all_blocks < num_blocks ? all_blocks : num_blocks) * block;
-  if (int s = latent_row_tiles(max_q, h_q, tokens, p.workers, &tiles)) return s;
+  const int tiles = latent_row_tiles(max_q, h_q, tokens, p.workers, forced);
   const LatentKernel k = latent_attn(latent_dim, cache_scales != nullptr, tiles);
   const int row_tiles = (int)(((long long)max_q * h_q + 16 * tiles - 1) / (16 * tiles));
   p.together = (long long)max_q * batch == total && row_tiles <= 8 ? row_tiles : 1;

@@ -521,8 +521,8 @@ int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const
  * q [total][h_q][latent], q_rope [total][h_q][P] and out [total][h_q][latent]
  * are bf16 with any strides (multiples of 8, 4 for out) from token to token and head to head;
  * lse is fp32 [total][h_q] or NULL; max_q is the most queries of one sequence.
- * A token whose latent or rope part is not finite makes the rows that see it
- * not finite and no others; what the cache holds past kv_lens[s] reaches none.
+ * A token whose latent or rope part is not finite can make the rows that see it
+ * not finite, and no others; what the cache holds past kv_lens[s] reaches none.
  * Scores, the softmax's running reference and sums and the output's
  * accumulator are fp32; for the second product each probability is rounded to
  * bf16, in steps of 64 tokens that some row does not see wholly to two bf16

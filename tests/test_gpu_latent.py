@@ -72,11 +72,13 @@ def check_out(out, lse, want, rest=2.0 ** -8):
     r, w, l = want
     got, got_lse = host(out), lse.cpu().numpy().astype(np.float64)
     bound = 2.0 ** -8 * np.abs(r) + (rest + 2.0 ** -11) * w
-    off = np.abs(got - r)
-    assert (off <= bound).all(), f"{np.nanmax(off / np.maximum(bound, 1e-30))} of the bound, NaN {np.isnan(got).sum()}"
-    seen = np.isfinite(l)
-    assert (np.abs(got_lse - l)[seen] <= 2.0 ** -12 + 2.0 ** -20 * np.abs(l)[seen]).all()
-    assert (got_lse[~seen] == -np.inf).all()
+    assert np.array_equal(np.isnan(got), np.isnan(r)) and np.array_equal(np.isnan(got_lse), np.isnan(l))
+    known = ~np.isnan(r)
+    off = np.abs(got - r)[known]
+    assert (off <= bound[known]).all(), f"{np.max(off / np.maximum(bound[known], 1e-30))} of the bound"
+    seen, none = np.isfinite(l), l == -np.inf
+    assert (np.abs(got_lse[seen] - l[seen]) <= 2.0 ** -12 + 2.0 ** -20 * np.abs(l[seen])).all()
+    assert (got_lse[none] == -np.inf).all()
 
 
 APPEND = [
