@@ -374,6 +374,7 @@ __device__ __forceinline__ uint32_t bf16_finite(uint32_t w) {
 }
 
 typedef __attribute__((address_space(3))) v4u lds_v4u;
+typedef __attribute__((address_space(3))) v2u lds_v2u;
 
 // Four bf16 of one channel and four tokens, from token-major rows: lane i of
 // 16 gives the address of four channels of token i / 4 and gets channel i.
@@ -596,6 +597,23 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
         }
         if (i == kDmas - 1) lds_dma_end(rr, lane);
       };
+      // Where a lane's pieces of a step lie: of keys (piece 2 g of a bf16 row, g of
+      // a row of codes) and rope parts, of p as it writes and reads it, and of four
+      // tokens' channels; other pieces come in by an exclusive or or an offset.
+      int group[RW];  // this wave's groups of 16 tokens; where two waves widen a group, it is the first of one of them
+#pragma unroll
+      for (int r = 0; r < RW; ++r) group[r] = RW == 1 ? wave : tw * 2 + (r ^ rw);
+      const uint32_t lane_k = a * Lds::kRow + (F8 ? (g ^ a) << 4 : (2 * g ^ latent_turn(a)) << 4);
+      const uint32_t lane_kr = Lds::kLatent + a * P * 2 + ((P == 64 ? 2 * g ^ (a >> 1 & 7) : g ^ (a >> 2 & 3)) << 4);
+      const uint32_t lane_p = lds_addr(lds + Lds::kP) + a * 128 + ((g ^ (a >> 1 & 7)) << 4);
+      const uint32_t lane_pw = lds_addr(lds + Lds::kP) + (rw * kN * 16 + a) * 128 + (((2 * group[0] + (g >> 1)) ^ (a >> 1 & 7)) << 4) + (g & 1) * 8;
+      uint32_t lane_v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int tk = 8 * g + 4 * h + (a >> 2);  // of 32; + 32 for the second half of the step
+        // piece 2 c + (a % 4) / 2 of the row, c = wave kC + i: i comes in by an exclusive or
+        lane_v[h] = tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ latent_turn(tk & 15)) << 4) + (a & 1) * 8;
+      }
       __syncthreads();  // the tile before is done with LDS
       if (tid < 2) s_flag[tid] = 0;
       look(t0);
@@ -619,11 +637,11 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           const int buf = latent_uniform(s - t0) & 1;
           uint8_t* const now = lds + buf * Lds::kBuffer;
           uint8_t* const wide = F8 ? lds + Lds::kWide : now;
-          // addresses are worked out anew in every step: kept over the loop they
-          // would take the registers that q and u need
+          // the rest of a lane's addresses is worked out in every step: kept over
+          // the loop they would take the registers that q and u need
           int here = lane;
           asm volatile("" : "+v"(here));
-          const int a = here & 15, g = here >> 4, turn = latent_turn(a);
+          const int a = here & 15, g = here >> 4;
           // Scores: tokens 16 group[r] + a of the step with rows 16 (rw kN + n)
           // + a, 64 channels at a time.  The next step's tokens set out
           // meanwhile, piece by piece between the products, which leave room.
@@ -638,15 +656,12 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             const int piece = j + j / 2 + i;
             if (i < 1 + j % 2 && piece < kEarly) stage(piece);
           };
-          // this wave's groups of 16 tokens; where two waves widen a group, it is the first of one of them
-          int group[RW];
           bool there[RW];
-          uint32_t at_k[RW];  // piece 2 g of a bf16 row, g of a row of codes
+          uint32_t at_k[RW];
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
-            group[r] = RW == 1 ? wave : tw * 2 + (r ^ rw);
             there[r] = s_there[buf * 4 + group[r]] != 0;
-            at_k[r] = lds_addr(now) + (16 * group[r] + a) * Lds::kRow + (F8 ? (g ^ a) << 4 : (2 * g ^ turn) << 4);
+            at_k[r] = lds_addr(now) + group[r] * (16 * Lds::kRow) + lane_k;
           }
           auto key_at = [&](int j, int h, int r) {
             const uint32_t bits = F8 ? (j & 3) * 64 : (j & 1) * 128 + h * 16;
@@ -669,7 +684,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 #pragma unroll
               for (int b = 0; b < L / 128; ++b) scale[r][b] = sc[b];
             }
-          const uint32_t at_w = lds_addr(wide) + (16 * group[0] + a) * (2 * L) + ((2 * g ^ turn) << 4);
+          const uint32_t at_w = lds_addr(wide) + (16 * group[0] + a) * (2 * L) + ((2 * g ^ latent_turn(a)) << 4);  // e4m3
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             if (j + 2 < kJ) fetch_k(j + 2);
@@ -705,11 +720,10 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           }
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
-            const uint8_t* const from = now + Lds::kLatent + (16 * group[r] + a) * (P * 2);
+            const uint32_t from = lds_addr(now) + group[r] * (16 * P * 2) + lane_kr;
 #pragma unroll
             for (int j = 0; j < kRopeFrags; ++j) {
-              const int slot = P == 64 ? (2 * g + j) ^ (a >> 1 & 7) : g ^ (a >> 2 & 3);
-              const v8bf kr = *(const v8bf*)(from + slot * 16);
+              const v8bf kr = __builtin_bit_cast(v8bf, *(const lds_v4u*)(uintptr_t)(from ^ (j * 16)));
 #pragma unroll
               for (int n = 0; n < kN; ++n) x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr, qrf[n][j], x[r][n], 0, 0, 0);
             }
@@ -749,8 +763,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
                 for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(w[e]);
                 sum[n] += (w[0] + w[1]) + (w[2] + w[3]);
                 const v2u packed = {pack2_bf16(w[0], w[1]), pack2_bf16(w[2], w[3])};
-                const int piece = 2 * group[r] + (g >> 1);
-                *(v2u*)(lds + Lds::kP + row * 128 + ((piece ^ (row >> 1 & 7)) << 4) + (g & 1) * 8) = packed;
+                *(lds_v2u*)(uintptr_t)((lane_pw ^ (r * 32)) + n * 2048) = packed;
                 if constexpr (MASKED) {
                   const v2u rest = {pack2_bf16(w[0] - __uint_as_float(packed[0] << 16), w[1] - __uint_as_float(packed[0] & 0xFFFF0000u)),
                                     pack2_bf16(w[2] - __uint_as_float(packed[1] << 16), w[3] - __uint_as_float(packed[1] & 0xFFFF0000u))};
@@ -770,17 +783,11 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const int row = 16 * n + a;
-              pf[k % kPf][n] = *(const v8bf*)(lds + Lds::kP + row * 128 + (((4 * k + g) ^ (row >> 1 & 7)) << 4));
+              pf[k % kPf][n] = __builtin_bit_cast(v8bf, *(const volatile lds_v4u*)(uintptr_t)((lane_p ^ (k * 64)) + n * 2048));
               if constexpr (MASKED) rest[n] = *(const v8bf*)(s_rest + (2 * k + (g >> 1)) * kRestGroup + row * 32 + (g & 1) * 16);
             }
           };
-          uint32_t at_v[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int tk = 8 * g + 4 * h + (a >> 2);  // of 32; + 32 for the second half of the step
-            // piece 2 c + (a % 4) / 2 of the row, c = wave kC + i: i comes in by an exclusive or
-            at_v[h] = lds_addr(wide) + tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ latent_turn(tk & 15)) << 4) + (a & 1) * 8;
-          }
+          const uint32_t at_v[2] = {lds_addr(wide) + lane_v[0], lds_addr(wide) + lane_v[1]};
           v4u v[kAhead + 1];
           auto fetch_v = [&](int i) {  // column tile i % kC, tokens 32 (i / kC) ..
 #pragma unroll
