@@ -1173,6 +1173,10 @@ template <int D, int MT>
 LatentKernel latent_expanded() {
   return {reinterpret_cast<const void*>(&dg::latent_expanded_kernel<D, MT>), 2 * dg::kLatentStep * (4 * D + D), nullptr};
 }
+LatentKernel latent_expanded(int d, int rows) {
+  return d == 128 ? (rows == 128 ? latent_expanded<128, 2>() : latent_expanded<128, 1>())
+                  : (rows == 128 ? latent_expanded<64, 2>() : latent_expanded<64, 1>());
+}
 
 std::once_flag g_latent_once;
 hipError_t g_latent_err = hipSuccess;
@@ -1180,7 +1184,6 @@ hipError_t g_latent_err = hipSuccess;
 // These kernels take more LDS than a launch may ask for unasked.
 int ensure_latent_attributes() {
   std::call_once(g_latent_once, []() {
-    const LatentKernel expanded[] = {latent_expanded<128, 2>(), latent_expanded<64, 2>()};
     auto allow = [](const LatentKernel& k) {
       const hipError_t e = hipFuncSetAttribute(k.fn, hipFuncAttributeMaxDynamicSharedMemorySize, k.smem);
       if (e != hipSuccess) g_latent_err = e;
@@ -1188,7 +1191,8 @@ int ensure_latent_attributes() {
     for (int latent : {256, 512})
       for (bool f8 : {false, true})
         for (int tiles : {1, 2, 4}) allow(latent_attn(latent, f8, tiles));
-    for (const LatentKernel& k : expanded) allow(k);
+    for (int d : {64, 128})
+      for (int rows : {64, 128}) allow(latent_expanded(d, rows));
   });
   if (g_latent_err != hipSuccess)
     return fail(DG_ERR_HIP, "hipFuncSetAttribute: %s", hipGetErrorString(g_latent_err));
@@ -2038,10 +2042,19 @@ int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint
   p.total_kv = total_kv;
   p.most = max_q < total ? max_q : total;
   p.h = heads;
-  constexpr int kRows = 128;
-  const long long tiles = ((long long)p.most + kRows - 1) / kRows;
+  // Workgroups of 128 queries of a head, or of 64 where there are no more of the
+  // former than CUs: a step then takes a workgroup, alone on its CU, less (us, 64 /
+  // 128, 32 heads of 128: 1 x 128 new of 2048 49 / 67, 1 x 512 of 2048 53 / 69, 1 x
+  // 1024 33 / 43, 4 x 256 of 2048 75 / 86; more of them than CUs: 4 x 512 of 2048 126
+  // / 97, 128 heads, 1 x 300 27 / 25, 4 x 2048 of 4096 738 / 559; heads of 64: 9 x up
+  // to 150, 5 heads 8.9 / 10.6, 4 x 1024 of 2048, 32 heads 131 / 101; a third step
+  // in flight changes nothing).
+  const auto tiles_of = [&](int rows) { return ((long long)p.most + rows - 1) / rows; };
+  const long long groups = heads * min(tiles_of(128) * batch, (long long)total / 128 + batch);  // at most, whatever the lengths
+  const int rows = groups > info->cus ? 128 : 64;
+  const long long tiles = tiles_of(rows);
   if (tiles > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many queries per sequence (%d)", p.most);
-  const LatentKernel k = head_dim == 128 ? latent_expanded<128, 2>() : latent_expanded<64, 2>();
+  const LatentKernel k = latent_expanded(head_dim, rows);
   void* args[] = {&p};
   return launch_plain("latent_expanded_attention", k.fn, dim3(heads, batch, (unsigned)tiles), 256, args, stream, k.smem);
 }

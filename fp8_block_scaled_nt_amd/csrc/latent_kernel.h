@@ -1022,7 +1022,7 @@ __device__ __forceinline__ int latent_turn8(int t) { return (t & 7) << 1 | (t >>
 // g .., which is what it wants as B operand if the values' transposing reads
 // take the tokens in that order: p stays in registers.
 template <int D, int MT>
-__global__ __launch_bounds__(256, MT > 2 ? 1 : 2) void latent_expanded_kernel(LatentExpandedParams p) {
+__global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedParams p) {
   constexpr int R = D / 2, kRows = 64 * MT, kRow = 4 * D, kPieces = kRow / 16;  // bytes and 16-byte pieces of a token's row
   constexpr int kBuffer = kLatentStep * (kRow + 2 * R), kN = D / 32, kR = R / 32;
   extern __shared__ __align__(1024) uint8_t lds[];

@@ -9,7 +9,7 @@ from fp8_block_scaled_nt_amd import build as B
 from tests.test_dma_guard_asm import m0_writes_outside_guards, unguarded_successors
 
 FORMS = [f"latent_attn_kernel<{L}, {f8}, {nt}>(LatentAttnParams)" for L in (256, 512) for f8 in ("false", "true") for nt in (1, 2, 4)]
-FORMS += [f"latent_expanded_kernel<{d}, 2>(LatentExpandedParams)" for d in (64, 128)]
+FORMS += [f"latent_expanded_kernel<{d}, {mt}>(LatentExpandedParams)" for d in (64, 128) for mt in (1, 2)]
 
 
 @pytest.fixture(scope="module")
