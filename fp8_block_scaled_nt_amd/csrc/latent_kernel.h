@@ -1011,9 +1011,13 @@ struct LatentExpandedParams {
   int causal, batch, total, total_kv, most, h;
 };
 
-// How the LDS rows are turned here: the 8 tokens of a transposing read are 4 g
-// .. 4 g + 3 of two lane groups.
-__device__ __forceinline__ int latent_turn8(int t) { return (t & 7) << 1 | (t >> 3 & 1); }
+// How the LDS rows are turned here.  The 8 tokens of half a transposing read are
+// 0 .. 7 or 8 .. 15 of 16: their pairs of pieces are told apart by t % 8.  A
+// row fragment's read passes 16 lanes at a time, lanes 0-3, 12-15 and 20-27 of 32
+// and the others: tokens 8 .. 11 take the odd pieces beside those of 4 .. 7, so
+// that lanes of two groups, whose pieces differ by one, do not meet either (with 8
+// .. 15 in the order of 0 .. 7 a quarter of the LDS cycles were conflicts).
+__device__ __forceinline__ int latent_turn8(int t) { return ((t ^ (t >> 1 & 4)) & 7) << 1 | (t >> 3 & 1); }
 
 // A workgroup of four waves takes 64 MT queries of one head, 16 MT of them a
 // wave, and walks all tokens that they see.  Keys and values come to LDS as
