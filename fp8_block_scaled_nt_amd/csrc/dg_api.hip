@@ -1120,8 +1120,18 @@ int check_strided(const void* x, int64_t stride, int64_t head_stride, int heads,
   return DG_OK;
 }
 
-// Tiles of 16 rows that a workgroup of absorbed attention takes at once: as many as one sequence's queries fill, up to four, if there are more
-// than four 64-token steps of such tiles for each workgroup; else one, as a
+// Rows that are written: no two of them may overlap, one of the strides has to step over all that the other one reaches.
+int check_apart(int64_t stride, int64_t head_stride, int total, int heads, int d, const char* name) {
+  const __int128 token = stride, head = head_stride;
+  const bool apart = total <= 1 || heads <= 1 ? total <= 1 || token >= d
+                                              : token >= (heads - 1) * head + d || (head >= (total - 1) * token + d && token >= d);
+  return apart ? DG_OK : fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: rows of %d tokens and %d heads overlap (strides %lld, %lld)", name,
+                              total, heads, (long long)stride, (long long)head_stride);
+}
+
+// Tiles of 16 rows that a workgroup of absorbed attention takes at once: as many
+// as one sequence's queries fill, up to four, if there are more than four
+// 64-token steps of such tiles for each workgroup; else one, as a
 // large tile's only step and part then cost more than reading the tokens again
 // (us with 16 / 32 / 64 rows, bf16, latents of 512, 128 heads: 1 x 4096 20 / 30 / 32,
 // 8 x 1024 23 / 28 / 33, 1 x 16384 30 / 34 / 40, 32 x 1024 35 / 35 / 38, 4 x 65536
@@ -1178,15 +1188,16 @@ LatentKernel latent_expanded(int d, int rows) {
                   : (rows == 128 ? latent_expanded<64, 2>() : latent_expanded<64, 1>());
 }
 
-std::once_flag g_latent_once;
-hipError_t g_latent_err = hipSuccess;
+std::once_flag g_latent_once[kMaxDevices];
+hipError_t g_latent_err[kMaxDevices];
 
-// These kernels take more LDS than a launch may ask for unasked.
-int ensure_latent_attributes() {
-  std::call_once(g_latent_once, []() {
-    auto allow = [](const LatentKernel& k) {
+// These kernels take more LDS than a launch may ask for unasked, on each device.
+int ensure_latent_attributes(int dev) {
+  std::call_once(g_latent_once[dev], [dev]() {
+    g_latent_err[dev] = hipSuccess;
+    auto allow = [dev](const LatentKernel& k) {
       const hipError_t e = hipFuncSetAttribute(k.fn, hipFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-      if (e != hipSuccess) g_latent_err = e;
+      if (e != hipSuccess) g_latent_err[dev] = e;
     };
     for (int latent : {256, 512})
       for (bool f8 : {false, true})
@@ -1194,8 +1205,8 @@ int ensure_latent_attributes() {
     for (int d : {64, 128})
       for (int rows : {64, 128}) allow(latent_expanded(d, rows));
   });
-  if (g_latent_err != hipSuccess)
-    return fail(DG_ERR_HIP, "hipFuncSetAttribute: %s", hipGetErrorString(g_latent_err));
+  if (g_latent_err[dev] != hipSuccess)
+    return fail(DG_ERR_HIP, "hipFuncSetAttribute: %s", hipGetErrorString(g_latent_err[dev]));
   return DG_OK;
 }
 
@@ -1855,6 +1866,7 @@ int dg_latent_append(const uint16_t* latent, int64_t latent_stride, const uint16
     if (h_q < 1 || h_q > 32767) return fail(DG_ERR_INVALID_ARGUMENT, "h_q must be 1..32767 (got %d)", h_q);
     if (int s = check_strided(q, q_stride, q_head_stride, h_q, rope_dim, 8, "q")) return s;
     if (int s = check_strided(q_out, q_out_stride, q_out_head_stride, h_q, rope_dim, 8, "q_out")) return s;
+    if (int s = check_apart(q_out_stride, q_out_head_stride, total, h_q, rope_dim, "q_out")) return s;
     if (q == q_out && (q_stride != q_out_stride || q_head_stride != q_out_head_stride))
       return fail(DG_ERR_INVALID_ARGUMENT, "in place q and q_out must have the same strides");
   }
@@ -1955,6 +1967,7 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   if (int s = check_strided(q, q_stride, q_head_stride, h_q, latent_dim, 8, "q")) return s;
   if (int s = check_strided(q_rope, q_rope_stride, q_rope_head_stride, h_q, latent_dim / 8, 8, "q_rope")) return s;
   if (int s = check_strided(out, out_stride, out_head_stride, h_q, latent_dim, 8, "out")) return s;
+  if (int s = check_apart(out_stride, out_head_stride, total, h_q, latent_dim, "out")) return s;
   if (!aligned4(lse) || !aligned4(kv_lens) || !aligned4(cu_q))
     return fail(DG_ERR_MISALIGNED, "lse and lengths must be 4-byte aligned");
   if (batch == 0 || total == 0 || max_q == 0) return ok();
@@ -1963,7 +1976,7 @@ int dg_latent_attention(const uint16_t* q, int64_t q_stride, int64_t q_head_stri
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
-  if (int s = ensure_latent_attributes()) return s;
+  if (int s = ensure_latent_attributes(dev)) return s;
   p.q = q;
   p.qr = q_rope;
   p.q_stride = q_stride;
@@ -2023,7 +2036,7 @@ int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
-  if (int s = ensure_latent_attributes()) return s;
+  if (int s = ensure_latent_attributes(dev)) return s;
   dg::LatentExpandedParams p{};
   p.q = q;
   p.kv = kv;

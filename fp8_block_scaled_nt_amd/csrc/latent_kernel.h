@@ -22,8 +22,6 @@
 
 namespace dg {
 
-
-
 struct LatentCache {
   uint8_t* latent;  // bf16 or e4m3
   uint16_t* rope;
@@ -1229,7 +1227,7 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
             }
           }
         }
-        block_barrier();  // all are done with this buffer: their reads have returned, as products waited for them
+        lds_barrier();  // all are done with this buffer: their reads have returned
         stage(s + 2, buf);
       }
     };

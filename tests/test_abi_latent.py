@@ -114,3 +114,17 @@ def test_forced_forms(lib, monkeypatch, name, status):
     assert call(lib.dg_latent_attention, ATTEND) == call(lib.dg_kv8_attention, KV8) == status
     assert lib.dg_latent_attention_workspace_size(512, 1, 8, ctypes.byref(size)) == status
     assert call(lib.dg_latent_attention, ATTEND, total=0) == 0
+
+
+@pytest.mark.parametrize("stride,head,total,heads,status", [
+    (4096, 512, 5, 8, 4), (512, 512 * 5, 5, 8, 4), (512, 512, 5, 1, 4), (0, 512, 1, 8, 4), (8192, 520, 5, 8, 4), (1 << 62, 512, 5, 8, 4),
+    (0, 512, 5, 8, 2), (504, 512, 5, 1, 2), (4088, 512, 5, 8, 2), (512, 512, 5, 8, 2), (512, 512 * 5 - 8, 5, 8, 2), (504, 1 << 62, 5, 8, 2),
+])
+@no_gpu
+def test_rows_that_are_written_lie_apart(lib, stride, head, total, heads, status):
+    # a call that passes ends at the missing device
+    changed = dict(o_stride=stride, o_head=head, total=total, h_q=heads)
+    assert call(lib.dg_latent_attention, ATTEND, **changed) == status
+    changed.update(o_stride=stride // 8, o_head=head // 8)
+    if all(x % 64 == 0 for x in (stride, head)):
+        assert call(lib.dg_latent_append, dict(APPEND, q_out=ctypes.c_void_p(0x20000)), **changed) == status
