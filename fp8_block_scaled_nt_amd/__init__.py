@@ -648,6 +648,14 @@ def _plain(t, name, dtype, ndim):
         _need(t, name, (dtype,), ndim)
 
 
+def _here(*tensors):
+    """Kernels run on the current device: a tensor of another one is refused."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensors must be on the current device (cuda:{here}), got one on {t.device}")
+
+
 def _latent_shape(cache, block_table, cu):
     """(latent, rope, scales pointers, L, block, num_blocks, max_blocks, batch) of a cache and its tables, checked."""
     latent, rope, scales = cache
@@ -735,6 +743,7 @@ def latent_append(latent, rope, cache, block_table, ctx_lens, cu_new, max_new, a
             q, q_to = (q_rope.data_ptr(), qs, qh), (q_out.data_ptr(), os_, oh)
     elif q_out is not None:
         raise ValueError("q_out without q_rope")
+    _here(latent, rope, *cache, block_table, ctx_lens, cu_new, angles, norm, q_rope, q_out)
     _check(lib().dg_latent_append(latent.data_ptr(), ls, rope.data_ptr(), rs, at_latent, at_rope, at_scales,
                                   block_table.data_ptr(), ctx, cu_new.data_ptr(), angles.data_ptr(), positions,
                                   None if norm is None else norm.data_ptr(), eps, *q, *q_to, interleaved, batch, total,
@@ -752,6 +761,7 @@ def latent_gather(cache, block_table, cu, latent, rope, starts=None):
     total = len(latent)
     if latent.shape != (total, dim) or rope.shape != (total, dim // 8):
         raise ValueError(f"rows must be [tokens, {dim}] and [tokens, {dim // 8}], got {tuple(latent.shape)}, {tuple(rope.shape)}")
+    _here(*cache, block_table, cu, latent, rope, starts)
     _check(lib().dg_latent_gather(at_latent, at_rope, at_scales, block_table.data_ptr(),
                                   None if starts is None else _lengths(starts, "starts", batch), cu.data_ptr(),
                                   latent.data_ptr(), rope.data_ptr(), batch, total, dim, block, num_blocks, max_blocks,
@@ -781,6 +791,7 @@ def latent_attention(q, q_rope, cache, block_table, kv_lens, cu_q, max_q, out, l
     total_o, _, os_, oh = _heads(out, "out", heads, dim)
     if total_r != total or total_o != total:
         raise ValueError(f"q holds {total} tokens, q_rope {total_r}, out {total_o}")
+    _here(q, q_rope, *cache, block_table, kv_lens, cu_q, out, lse)
     _check(lib().dg_latent_attention(q.data_ptr(), qs, qh, q_rope.data_ptr(), rs, rh, at_latent, at_rope, at_scales,
                                      block_table.data_ptr(), _lengths(kv_lens, "kv_lens", batch), cu_q.data_ptr(),
                                      out.data_ptr(), os_, oh, _need_lse(lse, total, heads),
@@ -815,6 +826,7 @@ def latent_expanded_attention(q, kv, k_rope, cu_q, cu_kv, max_q, out, lse=None, 
     total_r, rs = _rows(k_rope, "k_rope", dim // 2)
     if total_q != total or total_r != total_kv:
         raise ValueError(f"out holds {total} tokens, q {total_q}; kv {total_kv}, k_rope {total_r}")
+    _here(q, kv, k_rope, cu_q, cu_kv, out, lse)
     _check(lib().dg_latent_expanded_attention(q.data_ptr(), qs, kv.data_ptr(), ks, k_rope.data_ptr(), rs,
                                               cu_q.data_ptr(), cu_kv.data_ptr(), out.data_ptr(),
                                               _need_lse(lse, total, heads),

@@ -41,8 +41,8 @@
  *   such a growth is refused with DG_ERR_WORKSPACE and nothing is enqueued:
  *   size the workspace first with dg_reserve_workspace(bytes, stream), bytes
  *   from dg_dense_workspace_size (dg_bf16_w4_workspace_size,
- *   dg_kv8_attention_workspace_size, dg_latent_attention_workspace_size).  A captured call keeps using the workspace
- *   its capture stream had; a replay must not overlap in time with other
+ *   dg_kv8_attention_workspace_size, dg_latent_attention_workspace_size).  A
+ *   captured call keeps using the workspace its capture stream had; a replay must not overlap in time with other
  *   split-K work on that same workspace (replaying on the capture stream, or
  *   on any stream ordered with it, is safe).  dg_fp8_gemm_nt_noalloc uses a
  *   static per-GPU array instead and allocates nothing.
@@ -486,9 +486,12 @@ int dg_kv8_attention_workspace_size(int d, size_t* bytes);
  * with norm bf16 [latent] and angles fp32 [positions][P].  If q is not NULL,
  * the rope parts of the h_q query heads of each token (q_stride elements from
  * token to token, q_head_stride from head to head) are turned alike and
- * written to q_out, which may be q itself.  Tokens at positions outside [0,
- * positions) are ignored.  amax counts finite values; infinities saturate, NaN
- * is stored as NaN (with a norm either makes the whole token NaN).
+ * written to q_out, which may be q itself (else q_out overlaps no input); its
+ * rows must lie apart.  Tokens at positions outside [0, positions) are ignored;
+ * no two tokens of a call may have the same place in the cache.  amax counts
+ * finite values; infinities saturate, NaN is stored as NaN.  With a norm a NaN
+ * makes the whole token NaN, and an infinity itself NaN and the rest of its
+ * token 0.  At most 2^25 tokens a call.
  */
 int dg_latent_append(const uint16_t* latent, int64_t latent_stride, const uint16_t* rope, int64_t rope_stride,
                      void* cache_latent, uint16_t* cache_rope, float* cache_scales, const int32_t* block_table,
@@ -502,7 +505,7 @@ int dg_latent_append(const uint16_t* latent, int64_t latent_stride, const uint16
  * Cached tokens as packed bf16 rows, latent [total][latent] and rope [total][P]:
  * row cu[s] + i is token starts[s] + i of sequence s (starts NULL: from 0 on).
  * e4m3 latents come out as the values they stand for.  Rows of tokens that the
- * table has no block for keep what they held.
+ * table has no block for keep what they held.  At most 2^25 rows a call.
  */
 int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const float* cache_scales,
                      const int32_t* block_table, const int32_t* starts, const int32_t* cu, uint16_t* latent,
@@ -519,8 +522,9 @@ int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const
  * with scale >= 0, over the tokens j up to its own position if causal, all
  * kv_lens[s] otherwise.  A row that sees no token gets out = 0 and lse = -inf.
  * q [total][h_q][latent], q_rope [total][h_q][P] and out [total][h_q][latent]
- * are bf16 with any strides (multiples of 8, 4 for out) from token to token and head to head;
- * lse is fp32 [total][h_q] or NULL; max_q is the most queries of one sequence.
+ * are bf16, with any strides from token to token and from head to head that are
+ * multiples of 8; out's rows must lie apart.  lse is fp32 [total][h_q] or NULL;
+ * max_q is the most queries of one sequence (max_q * h_q at most 2^30).
  * A token whose latent or rope part is not finite can make the rows that see it
  * not finite, and no others; what the cache holds past kv_lens[s] reaches none.
  * Scores, the softmax's running reference and sums and the output's
