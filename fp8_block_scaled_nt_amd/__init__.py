@@ -650,10 +650,11 @@ def _plain(t, name, dtype, ndim):
 
 def _here(*tensors):
     """Kernels run on the current device: a tensor of another one is refused."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"tensors must be on the current device (cuda:{here}), got one on {t.device}")
+    if torch.cuda.device_count() > 1:
+        here = torch.cuda.current_device()
+        for t in tensors:
+            if t is not None and t.get_device() != here:
+                raise ValueError(f"tensors must be on the current device (cuda:{here}), got one on {t.device}")
 
 
 def _latent_shape(cache, block_table, cu):

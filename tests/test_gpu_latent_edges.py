@@ -86,6 +86,7 @@ def test_tensors_of_another_device_are_refused(gpu, monkeypatch):
     out, angles, rope = torch.zeros_like(q), torch.zeros((16, 32), device=gpu), qr[:, 0].contiguous()
     packed = q[:, 0].contiguous()
     here = torch.cuda.current_device()
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: here + 1)      # seen from another one
     for call in (lambda: dg.latent_append(packed, rope, on, t, i32([0], gpu), cu, 2, angles),
                  lambda: dg.latent_gather(on, t, cu, packed, rope),
