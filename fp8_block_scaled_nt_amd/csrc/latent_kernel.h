@@ -99,7 +99,11 @@ __device__ __forceinline__ void latent_rotate(v4u (&x)[2], const v4f (&c)[2], co
 
 // One wave takes one token: its latent, its rope part, and (blockIdx.y) some
 // of the queries' heads.  A lane turns eight pairs of a head; the cosines and
-// sines that it needs are the same for every head.
+// sines that it needs are the same for every head, so they are read once, and
+// the norm's sum needs no LDS.  Few tokens are bound by the launch and a chain
+// of loads (lengths, table, write): 64 tokens of 512, 8 heads 4.2 us.  Many are
+// bound by memory: 4 prompts up to 4096 of 512 into e4m3, 32 heads 28.8 us, 121
+// MB read and written (4.2 TB/s).
 constexpr int kLatentHeads = 32;  // query heads of one wave
 
 template <int L, bool F8, bool PAIRS>
@@ -211,7 +215,9 @@ __device__ __forceinline__ v4u latent_widen(uint32_t lo, uint32_t hi, float scal
 
 // One wave takes eight rows; a lane takes 16 bytes of a token at a time, so
 // that a load brings 1 KB of one to four tokens, and all of them are on their
-// way together.
+// way together.  Bound by memory: 4 x up to 32768 tokens of 512 out of e4m3 40.3
+// us, 4.2 TB/s read and written (one row a wave 46.5 us a call); 7 x up to 777 of
+// 256 3.6 us, the launch and a chain of three loads.
 constexpr int kLatentGather = 8;  // rows of a wave
 
 template <int L, bool F8>
@@ -430,6 +436,19 @@ struct LatentLds {
 //
 // Tiles that a share's end cuts leave their parts in the workspace, and
 // latent_join_kernel adds them up.
+//
+// p meets c as bf16, 8 bits, as wide as c itself: its error, up to 2^-8 of each
+// p and of either sign, stays below out's own rounding unless the values cancel,
+// while fp16 would not hold c's range.  A step that some row does not see
+// wholly may be all that a row sees: there p goes in two pieces, 16 bits.
+//
+// What bounds it, by case (latents of 512): with few rows HBM - 64 x up to 8192
+// tokens, 16 rows each, bf16 77 us, 5 TB/s, at a copy's rate; with 128 rows the
+// CU - 4 x 65536, bf16 97 to 117 us by the clock, 730 TFLOP/s at best, MFMA busy
+// a third of the wave cycles and waits another third (LDS, barriers: p is shared
+// between the waves); 32 x up to 4096 in e4m3 58 us, where widening makes it 4.1
+// VALU instructions an MFMA instead of 2.4; 1 x 777 of 256 7.6 us, latency of the
+// prologue.
 template <int L, bool F8, int NT>
 __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p) {
   using Lds = LatentLds<L, F8, NT>;
@@ -908,6 +927,10 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 // Adds up the parts of the tiles that shares cut, in an order that does not
 // change from call to call.  The workgroups share out all pieces of such tiles:
 // kPer times 16 rows by 16 channels, of which each wave takes every fourth part.
+// (4 x 65536 with 128 heads took 141 us with sixteen workgroups a tile, 123 like
+// this.)  Bound by the launch and two chained loads: 4 us where there is one tile,
+// 5.7 us behind 64 x 8192, 10.5 us behind 4 x 65536 and 32 x 4096 with 128 heads,
+// up to 67 MB of parts that the L2s and the Infinity Cache hold.
 template <int L, int NT>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
   constexpr int kRows = 16 * NT, kPer = 4, kPieces = L / 16 * NT / kPer;
@@ -1022,7 +1045,14 @@ __device__ __forceinline__ int latent_turn8(int t) { return ((t ^ (t >> 1 & 4)) 
 // they lie in memory, two steps at a time in flight.  The scores' tiles are
 // dealt so that a lane ends up with p of tokens 32 k + 4 g .. and 32 k + 16 + 4
 // g .., which is what it wants as B operand if the values' transposing reads
-// take the tokens in that order: p stays in registers.
+// take the tokens in that order: p stays in registers.  p is rounded to bf16, in
+// two pieces where a step has masks, as in the absorbed form.
+//
+// Bound by MFMA and the softmax's VALU work taking turns on a SIMD (two waves of
+// it overlap in part: 3.3 VALU instructions an MFMA, 28 % of the wave cycles
+// wait): 1 x 8192, 32 heads of 128, causal 666 to 714 us, up to 1030 TFLOP/s
+// of 1212 of a large library product; 4 x up to 2048 of 4096 303 to 334 us; 9 x up to
+// 150, 5 heads of 64 8 us, latency.
 template <int D, int MT>
 __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedParams p) {
   constexpr int R = D / 2, kRows = 64 * MT, kRow = 4 * D, kPieces = kRow / 16;  // bytes and 16-byte pieces of a token's row
