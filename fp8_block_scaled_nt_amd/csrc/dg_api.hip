@@ -245,6 +245,8 @@ constexpr const char* kKv8Split = "kv8_split";
 constexpr const char* kKv8Prompt = "kv8_prompt";
 // rows of a tile of absorbed attention over latents
 constexpr const char* kLatentRows[] = {"latent_rows16", "latent_rows32", "latent_rows64"};
+// and queries of a workgroup of expanded attention
+constexpr const char* kLatentPrompt[] = {"latent_prompt16", "latent_prompt32", "latent_prompt64", "latent_prompt128"};
 
 // DG_FORCE_CONFIG=<name> pins the configuration of the variant it names (for
 // tuning sweeps); an unknown name is an error rather than silently ignored.
@@ -259,6 +261,7 @@ int forced_name(const char** name) {
   known = known || find_skinny(e) != nullptr || strcmp(e, kKv8Split) == 0 || strcmp(e, kKv8Prompt) == 0 ||
           strcmp(e, kW4RowsName) == 0 || strcmp(e, kW4TileName) == 0;
   for (const char* rows : kLatentRows) known = known || strcmp(e, rows) == 0;
+  for (const char* rows : kLatentPrompt) known = known || strcmp(e, rows) == 0;
   if (!known) return fail(DG_ERR_INVALID_ARGUMENT, "DG_FORCE_CONFIG names no configuration: %s", e);
   *name = e;
   return DG_OK;
@@ -1179,14 +1182,17 @@ LatentKernel latent_attn(int latent, bool f8, int tiles) {
                        : (f8 ? latent_attn<256, true>(tiles) : latent_attn<256, false>(tiles));
 }
 
-template <int D, int MT>
+template <int D, int MT, bool SPLIT>
 LatentKernel latent_expanded() {
-  return {reinterpret_cast<const void*>(&dg::latent_expanded_kernel<D, MT>), 2 * dg::kLatentStep * (4 * D + D), nullptr};
+  return {reinterpret_cast<const void*>(&dg::latent_expanded_kernel<D, MT, SPLIT>), 2 * dg::latent_expanded_step(SPLIT) * (4 * D + D),
+          nullptr};
 }
-LatentKernel latent_expanded(int d, int rows) {
-  return d == 128 ? (rows == 128 ? latent_expanded<128, 2>() : latent_expanded<128, 1>())
-                  : (rows == 128 ? latent_expanded<64, 2>() : latent_expanded<64, 1>());
+template <int D>
+LatentKernel latent_expanded(int rows) {
+  return rows == 128 ? latent_expanded<D, 2, false>() : rows == 64 ? latent_expanded<D, 1, false>()
+         : rows == 32 ? latent_expanded<D, 2, true>() : latent_expanded<D, 1, true>();
 }
+LatentKernel latent_expanded(int d, int rows) { return d == 128 ? latent_expanded<128>(rows) : latent_expanded<64>(rows); }
 
 std::once_flag g_latent_once[kMaxDevices];
 hipError_t g_latent_err[kMaxDevices];
@@ -1203,7 +1209,7 @@ int ensure_latent_attributes(int dev) {
       for (bool f8 : {false, true})
         for (int tiles : {1, 2, 4}) allow(latent_attn(latent, f8, tiles));
     for (int d : {64, 128})
-      for (int rows : {64, 128}) allow(latent_expanded(d, rows));
+      for (int rows : {16, 32, 64, 128}) allow(latent_expanded(d, rows));
   });
   if (g_latent_err[dev] != hipSuccess)
     return fail(DG_ERR_HIP, "hipFuncSetAttribute: %s", hipGetErrorString(g_latent_err[dev]));
@@ -2033,6 +2039,8 @@ int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint
   if (!aligned16(out) || !aligned4(lse) || !aligned4(cu_q) || !aligned4(cu_kv))
     return fail(DG_ERR_MISALIGNED, "out must be 16-byte aligned, lse and lengths 4-byte");
   if (batch == 0 || total == 0 || max_q == 0) return ok();
+  const char* forced;
+  if (int s = forced_name(&forced)) return s;
   int dev;
   DeviceInfo* info;
   if (int s = current_device(&dev, &info)) return s;
@@ -2055,16 +2063,30 @@ int dg_latent_expanded_attention(const uint16_t* q, int64_t q_stride, const uint
   p.total_kv = total_kv;
   p.most = max_q < total ? max_q : total;
   p.h = heads;
-  // Workgroups of 128 queries of a head, or of 64 where there are no more of the
-  // former than CUs: a step then takes a workgroup, alone on its CU, less (us, 64 /
-  // 128, 32 heads of 128: 1 x 128 new of 2048 49 / 67, 1 x 512 of 2048 53 / 69, 1 x
-  // 1024 33 / 43, 4 x 256 of 2048 75 / 86; more of them than CUs: 4 x 512 of 2048 126
-  // / 97, 128 heads, 1 x 300 27 / 25, 4 x 2048 of 4096 738 / 559; heads of 64: 9 x up
-  // to 150, 5 heads 8.9 / 10.6, 4 x 1024 of 2048, 32 heads 131 / 101; a third step
-  // in flight changes nothing).
+  // Queries of a head that a workgroup takes: 128, or 64 where there would be no
+  // more workgroups of 128 than CUs or none would be more than half full, as a
+  // step then takes a workgroup, alone on its CU, less; and 32 or 16, with the
+  // tokens shared out between the waves, where all workgroups of that many are
+  // resident at once, one a CU (heads of 128) or two (of 64): the way through the
+  // tokens is a quarter as long, but each workgroup fetches all of them again.
+  // us with 16 / 32 / 64 / 128 queries, heads of 128:
+  //   32 heads, 1 x 128 new of 2048    27 / 35 / 49 / 67     8 heads, 1 x 4 of 8192     77 / 107 / 166 / 224
+  //   16 heads, 8 x 20 of up to 4096   62 / 74 / 115 / 144   24 heads, 1 x 256 of 2048  45 / 35 / 50 / 69
+  //   40 heads, 1 x 128 of 2048        50 / 36 / 51 / 71     36 heads, 1 x 256 of 2048  72 / 64 / 51 / 70
+  //   32 heads, 1 x 512 of 2048        91 / 65 / 53 / 70     32 heads, 1 x 1024         85 / 59 / 34 / 44
+  //   32 heads, 4 x 512 of 2048       372 / 246 / 125 / 99   16 heads, 30 x 8 of 500    24 / 29 / 24 / 28
+  // heads of 64:
+  //   5 heads, 9 x up to 150           7.0 / 7.7 / 8.9 / 10  16 heads, 1 x 512 of 4096  39 / 39 / 64 / 83
+  //   32 heads, 1 x 512 of 1024        23 / 16 / 19 / 25     32 heads, 4 x up to 1024 of 2048  186 / 99 / 60 / 62
   const auto tiles_of = [&](int rows) { return ((long long)p.most + rows - 1) / rows; };
-  const long long groups = heads * min(tiles_of(128) * batch, (long long)total / 128 + batch);  // at most, whatever the lengths
-  const int rows = groups > info->cus ? 128 : 64;
+  const auto groups = [&](int rows) {  // at most, whatever the lengths
+    const long long by_longest = tiles_of(rows) * batch, by_total = total / rows + batch;
+    return heads * (by_longest < by_total ? by_longest : by_total);
+  };
+  const int resident = head_dim == 128 ? info->cus : 2 * info->cus;
+  int rows = groups(16) <= resident ? 16 : groups(32) <= resident ? 32 : groups(128) <= info->cus || p.most <= 64 ? 64 : 128;
+  for (int i = 0; forced && i < 4; ++i)
+    if (strcmp(forced, kLatentPrompt[i]) == 0) rows = 16 << i;
   const long long tiles = tiles_of(rows);
   if (tiles > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many queries per sequence (%d)", p.most);
   const LatentKernel k = latent_expanded(head_dim, rows);

@@ -1040,6 +1040,9 @@ struct LatentExpandedParams {
 // .. 15 in the order of 0 .. 7 a quarter of the LDS cycles were conflicts).
 __device__ __forceinline__ int latent_turn8(int t) { return ((t ^ (t >> 1 & 4)) & 7) << 1 | (t >> 3 & 1); }
 
+// Tokens of a step.
+constexpr int latent_expanded_step(bool split) { return split ? 128 : 64; }
+
 // A workgroup of four waves takes 64 MT queries of one head, 16 MT of them a
 // wave, and walks all tokens that they see.  Keys and values come to LDS as
 // they lie in memory, two steps at a time in flight.  The scores' tiles are
@@ -1048,15 +1051,23 @@ __device__ __forceinline__ int latent_turn8(int t) { return ((t ^ (t >> 1 & 4)) 
 // take the tokens in that order: p stays in registers.  p is rounded to bf16, in
 // two pieces where a step has masks, as in the absorbed form.
 //
+// SPLIT: few queries.  A workgroup takes 16 MT of them, all in every wave, and the
+// waves share out the tokens: of a step of 128 each brings 32, works on them
+// without a barrier, and the four parts meet in LDS at the end.  Bound by the
+// latency of a step's DMA, two of them in flight: 1.2 us a step where 8 workgroups
+// run (8 heads, 4 queries of 8192 tokens 77 us, 166 with 64 MT queries each), 1.6
+// where every CU has one.
+//
 // Bound by MFMA and the softmax's VALU work taking turns on a SIMD (two waves of
 // it overlap in part: 3.3 VALU instructions an MFMA, 28 % of the wave cycles
 // wait): 1 x 8192, 32 heads of 128, causal 666 to 714 us, up to 1030 TFLOP/s
-// of 1212 of a large library product; 4 x up to 2048 of 4096 303 to 334 us; 9 x up to
-// 150, 5 heads of 64 8 us, latency.
-template <int D, int MT>
+// of 1212 of a large library product; 4 x up to 2048 of 4096 303 to 334 us.
+template <int D, int MT, bool SPLIT = false>
 __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedParams p) {
-  constexpr int R = D / 2, kRows = 64 * MT, kRow = 4 * D, kPieces = kRow / 16;  // bytes and 16-byte pieces of a token's row
-  constexpr int kBuffer = kLatentStep * (kRow + 2 * R), kN = D / 32, kR = R / 32;
+  constexpr int R = D / 2, kRows = SPLIT ? 16 * MT : 64 * MT, kRow = 4 * D, kPieces = kRow / 16;  // bytes and 16-byte pieces of a token's row
+  constexpr int kStep = latent_expanded_step(SPLIT), kOwn = kStep / 4;  // tokens of a step, and those that a wave brings
+  constexpr int kTok = SPLIT ? kOwn : kStep;                            // and those that it works on
+  constexpr int kBuffer = kStep * (kRow + 2 * R), kN = D / 32, kR = R / 32;
   extern __shared__ __align__(1024) uint8_t lds[];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
   const int head = blockIdx.x, seq = blockIdx.y;
@@ -1072,7 +1083,7 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
   if (row0 < 0) return;
   const int pos = kv - all;
   auto sees = [&](int i) { return p.causal ? max(min(pos + i + 1, kv), 0) : kv; };
-  const int wave0 = row0 + wave * 16 * MT;
+  const int wave0 = SPLIT ? row0 : row0 + wave * 16 * MT;
   const int any_hi = sees(min(row0 + kRows, count) - 1);
   const int wave_hi = wave0 < count ? sees(min(wave0 + 16 * MT, count) - 1) : 0;
 
@@ -1100,36 +1111,39 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
   // g ..), of a rope part, and of four values (token 4 g + a / 4, channels 4 (a %
   // 4) ..); other channels come in by an exclusive or, other tokens by an offset.
   const uint32_t lane_k = a * kRow + ((g ^ latent_turn8(a)) << 4);
-  const uint32_t lane_r = kLatentStep * kRow + a * 2 * R + ((R == 64 ? g ^ (a >> 1 & 7) : g ^ (a >> 2 & 3)) << 4);
+  const uint32_t lane_r = a * 2 * R + ((R == 64 ? g ^ (a >> 1 & 7) : g ^ (a >> 2 & 3)) << 4);
   const int tk = 4 * g + (a >> 2);
   const uint32_t lane_v = tk * kRow + (((D / 8 + (a >> 1 & 1)) ^ latent_turn8(tk)) << 4) + (a & 1) * 8;
 
-  // This wave's 16 tokens of a step.
+  // This wave's tokens of a step.
   auto stage = [&](int step, int buf) {
-    const int token = step * kLatentStep + wave * 16;
-    const int valid = min(max(kv - token, 0), 16);
-    const int at = first_kv + min(token, kv);
     uint8_t* const to = lds + buf * kBuffer;
     const uint32_t pitch = (uint32_t)p.kv_stride * 2, pitch_r = (uint32_t)p.kr_stride * 2;
-    const v4i_rsrc rk = make_rsrc(p.kv + (long long)at * p.kv_stride + (long long)head * (2 * D), valid ? (valid - 1) * pitch + kRow : 0);
-    constexpr int kPerDma = 64 / kPieces;
 #pragma unroll
-    for (int i = 0; i < 16 / kPerDma; ++i) {
-      const int t = i * kPerDma + lane / kPieces, piece = (lane % kPieces) ^ latent_turn8(t);
-      lds_dma16(rk, t * pitch + piece * 16, 0, to + wave * 16 * kRow + i * 1024);
-    }
-    const v4i_rsrc rr = make_rsrc(p.kr + (long long)at * p.kr_stride, valid ? (valid - 1) * pitch_r + 2 * R : 0);
+    for (int o = 0; o < kOwn; o += 16) {
+      const int own = wave * kOwn + o, token = step * kStep + own;
+      const int valid = min(max(kv - token, 0), 16);
+      const int at = first_kv + min(token, kv);
+      const v4i_rsrc rk = make_rsrc(p.kv + (long long)at * p.kv_stride + (long long)head * (2 * D), valid ? (valid - 1) * pitch + kRow : 0);
+      constexpr int kPerDma = 64 / kPieces;
 #pragma unroll
-    for (int i = 0; i < R / 32; ++i) {
-      const int t = R == 64 ? i * 8 + lane / 8 : lane / 4;
-      const int piece = R == 64 ? lane % 8 ^ (t >> 1 & 7) : lane % 4 ^ (t >> 2 & 3);
-      lds_dma16(rr, t * pitch_r + piece * 16, 0, to + kLatentStep * kRow + wave * 16 * R * 2 + i * 1024);
+      for (int i = 0; i < 16 / kPerDma; ++i) {
+        const int t = i * kPerDma + lane / kPieces, piece = (lane % kPieces) ^ latent_turn8(t);
+        lds_dma16(rk, t * pitch + piece * 16, 0, to + own * kRow + i * 1024);
+      }
+      const v4i_rsrc rr = make_rsrc(p.kr + (long long)at * p.kr_stride, valid ? (valid - 1) * pitch_r + 2 * R : 0);
+#pragma unroll
+      for (int i = 0; i < R / 32; ++i) {
+        const int t = R == 64 ? i * 8 + lane / 8 : lane / 4;
+        const int piece = R == 64 ? lane % 8 ^ (t >> 1 & 7) : lane % 4 ^ (t >> 2 & 3);
+        lds_dma16(rr, t * pitch_r + piece * 16, 0, to + kStep * kRow + own * R * 2 + i * 1024);
+      }
+      if (o + 16 == kOwn) lds_dma_end(rr, lane);
     }
-    lds_dma_end(rr, lane);
   };
-  constexpr int kEvents = (16 / (64 / kPieces) + R / 32) * kVmPerDma + 1;  // of one step, as vmcnt sees them
+  constexpr int kEvents = kOwn / 16 * (16 / (64 / kPieces) + R / 32) * kVmPerDma + 1;  // of one step, as vmcnt sees them
 
-  const int last = (any_hi + kLatentStep - 1) / kLatentStep;
+  const int last = (any_hi + kStep - 1) / kStep;
   if (last > 0) {
     stage(0, 0);
     stage(1, 1);  // past the last step: zeros
@@ -1138,22 +1152,26 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
       constexpr bool MASKED = decltype(form)::value;
 #pragma unroll 1
       for (; s < until; ++s) {
-        const int base = s * kLatentStep, buf = s & 1;
-        const uint8_t* const now = lds + buf * kBuffer;
+        const int base = s * kStep + (SPLIT ? wave * kTok : 0), buf = s & 1;
         wait_vmem<kEvents>();  // this step has landed, the next may be under way
-        block_barrier();
+        if constexpr (SPLIT)
+          asm volatile("" ::: "memory");
+        else
+          block_barrier();
         if (base < wave_hi) {
-          float t[MT][16];
-          const uint32_t at = lds_addr(now);
+          float t[MT][kTok / 4];
+          const uint32_t now = lds_addr(lds + buf * kBuffer);
+          const uint32_t at = now + (SPLIT ? wave * kTok * kRow : 0);
+          const uint32_t at_r = now + kStep * kRow + (SPLIT ? wave * kTok * 2 * R : 0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < kTok / 16; ++j) {
             v4f x[MT];
 #pragma unroll
             for (int n = 0; n < MT; ++n) x[n] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < kN + kR; ++k) {
               const v4u key = k < kN ? *(const lds_v4u*)(uintptr_t)(((at + lane_k) ^ (k * 64)) + j * 16 * kRow)
-                                     : *(const lds_v4u*)(uintptr_t)(((at + lane_r) ^ ((k - kN) * 64)) + j * 32 * R);
+                                     : *(const lds_v4u*)(uintptr_t)(((at_r + lane_r) ^ ((k - kN) * 64)) + j * 32 * R);
 #pragma unroll
               for (int n = 0; n < MT; ++n)
                 x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, key), qf[n][k], x[n], 0, 0, 0);
@@ -1163,7 +1181,7 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
 #pragma unroll
               for (int e = 0; e < 4; ++e) t[n][4 * j + e] = x[n][e];
           }
-          v4u pw[MT][2], rest[MT][2];
+          v4u pw[MT][kTok / 32], rest[MT][kTok / 32];
           uint32_t seen[MT];
 #pragma unroll
           for (int n = 0; n < MT; ++n) {
@@ -1171,7 +1189,7 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
             if constexpr (MASKED) {
               seen[n] = 0;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
+              for (int i = 0; i < kTok / 4; ++i) {
                 const bool is = base + 16 * (i / 4) + 4 * g + i % 4 < hi[n];
                 t[n][i] = is ? t[n][i] : -__builtin_huge_valf();  // the scale is not 0: it stays so
                 seen[n] |= is ? 1u << i : 0u;
@@ -1179,15 +1197,15 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
             }
             // how far the scores are from the reference; the largest is taken of
             // these, as products' results would be made canonical for it first
-            float d[16], top = -__builtin_huge_valf();
+            float d[kTok / 4], top = -__builtin_huge_valf();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) d[i] = __builtin_fmaf(t[n][i], p.scale_log2, -m[n]);
+            for (int i = 0; i < kTok / 4; ++i) d[i] = __builtin_fmaf(t[n][i], p.scale_log2, -m[n]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, d[i]);
+            for (int i = 0; i < kTok / 4; ++i) top = fmaxf(top, d[i]);
             if (__any(top > 0.f)) {
               top = -__builtin_huge_valf();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) top = fmaxf(top, t[n][i]);
+              for (int i = 0; i < kTok / 4; ++i) top = fmaxf(top, t[n][i]);
               top = fmaxf(top, __shfl_xor(top, 16, 64));
               top = fmaxf(top, __shfl_xor(top, 32, 64)) * p.scale_log2;
               const float ref = top > m[n] ? top + kLatentLead : m[n], shrink = top > m[n] ? __builtin_amdgcn_exp2f(m[n] - ref) : 1.f;
@@ -1196,11 +1214,11 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
               for (int c = 0; c < D / 16; ++c) u[n][c] *= shrink;
               m[n] = ref;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) d[i] = __builtin_fmaf(t[n][i], p.scale_log2, -ref);
+              for (int i = 0; i < kTok / 4; ++i) d[i] = __builtin_fmaf(t[n][i], p.scale_log2, -ref);
             }
             float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
+            for (int i = 0; i < kTok / 4; i += 2) {
               const float p0 = __builtin_amdgcn_exp2f(d[i]), p1 = __builtin_amdgcn_exp2f(d[i + 1]);
               sum[0] += p0;
               sum[1] += p1;
@@ -1215,7 +1233,7 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
           for (int c = 0; c < D / 16; ++c) {
             const uint32_t at_v = (at + lane_v) ^ (c * 32);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < kTok / 32; ++k) {
               v4u v;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
@@ -1257,12 +1275,18 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
             }
           }
         }
-        lds_barrier();  // all are done with this buffer: their reads have returned
+        if constexpr (SPLIT) {
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of the buffer have returned
+          asm volatile("" ::: "memory");
+        } else {
+          lds_barrier();  // all are done with this buffer: their reads have returned
+        }
         stage(s + 2, buf);
       }
     };
     // steps that every row of the workgroup sees wholly, and those with masks
-    steps(min(sees(row0) / kLatentStep, last), std::false_type{});
+    steps(min(sees(row0) / kStep, last), std::false_type{});
     steps(last, std::true_type{});
     wait_vmem_all();  // no LDS DMA may be in flight past this point
   }
@@ -1270,14 +1294,55 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
   for (int n = 0; n < MT; ++n) {
     l[n] += __shfl_xor(l[n], 16, 64);
     l[n] += __shfl_xor(l[n], 32, 64);
+  }
+  // channels c .. + 3 of row n 16 + a; l == 0: it sees no token
+  auto write = [&](int n, int c, v4f x, float mx, float sum, bool with_lse) {
     const int i = wave0 + n * 16 + a;
-    if (i >= count) continue;
+    if (i >= count) return;
     const size_t row = (size_t)(first + i) * p.h + head;
-    const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];  // l == 0: the row sees no token
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *(v2u*)(p.out + row * D + c) = v2u{pack2_bf16(x[0] * inv, x[1] * inv), pack2_bf16(x[2] * inv, x[3] * inv)};
+    if (p.lse && with_lse) p.lse[row] = sum == 0.f ? -__builtin_huge_valf() : (mx + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+  };
+  if constexpr (SPLIT) {
+    // the waves' parts, in their order; wave w adds up a quarter of the channels
+    v4f* const s_u = (v4f*)lds;                                     // [4][MT][D / 16][64]
+    float* const s_ml = (float*)(lds + 4 * MT * (D / 16) * 1024);  // [4][2][16 MT]
+    __syncthreads();
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c)
-      *(v2u*)(p.out + row * D + c * 16 + g * 4) = v2u{pack2_bf16(u[n][c][0] * inv, u[n][c][1] * inv), pack2_bf16(u[n][c][2] * inv, u[n][c][3] * inv)};
-    if (p.lse && g == 0) p.lse[row] = l[n] == 0.f ? -__builtin_huge_valf() : (m[n] + __builtin_amdgcn_logf(l[n])) * 0.69314718055994530942f;
+    for (int n = 0; n < MT; ++n) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) s_u[((wave * MT + n) * (D / 16) + c) * 64 + lane] = u[n][c];
+      if (g == 0) {
+        s_ml[(wave * 2 + 0) * 16 * MT + n * 16 + a] = m[n];
+        s_ml[(wave * 2 + 1) * 16 * MT + n * 16 + a] = l[n];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < MT; ++n) {
+      float f[4], top = kLatentLow, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w * 2 * 16 * MT + n * 16 + a]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        f[w] = __builtin_amdgcn_exp2f(s_ml[w * 2 * 16 * MT + n * 16 + a] - top);
+        sum += s_ml[(w * 2 + 1) * 16 * MT + n * 16 + a] * f[w];
+      }
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) {
+        const int c = wave * (D / 64) + k;
+        v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) x += s_u[((w * MT + n) * (D / 16) + c) * 64 + lane] * f[w];
+        write(n, c * 16 + g * 4, x, top, sum, c == 0 && g == 0);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) write(n, c * 16 + g * 4, u[n][c], m[n], l[n], c == 0 && g == 0);
   }
 }
 

@@ -128,3 +128,11 @@ def test_rows_that_are_written_lie_apart(lib, stride, head, total, heads, status
     changed.update(o_stride=stride // 8, o_head=head // 8)
     if all(x % 64 == 0 for x in (stride, head)):
         assert call(lib.dg_latent_append, dict(APPEND, q_out=ctypes.c_void_p(0x20000)), **changed) == status
+
+
+@pytest.mark.parametrize("name,status", [("latent_prompt16", NO_DEVICE), ("latent_prompt128", NO_DEVICE), ("latent_prompt48", 1)])
+@no_gpu
+def test_forced_forms_of_prompts(lib, monkeypatch, name, status):
+    monkeypatch.setenv("DG_FORCE_CONFIG", name)
+    assert call(lib.dg_latent_expanded_attention, EXPAND) == call(lib.dg_latent_attention, ATTEND) == status
+    assert call(lib.dg_latent_expanded_attention, EXPAND, total=0) == 0

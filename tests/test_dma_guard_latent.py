@@ -10,6 +10,7 @@ from tests.test_dma_guard_asm import m0_writes_outside_guards, unguarded_success
 
 FORMS = [f"latent_attn_kernel<{L}, {f8}, {nt}>(LatentAttnParams)" for L in (256, 512) for f8 in ("false", "true") for nt in (1, 2, 4)]
 FORMS += [f"latent_expanded_kernel<{d}, {mt}>(LatentExpandedParams)" for d in (64, 128) for mt in (1, 2)]
+FORMS += [f"latent_expanded_kernel<{d}, {mt}, true>(LatentExpandedParams)" for d in (64, 128) for mt in (1, 2)]
 
 
 @pytest.fixture(scope="module")
