@@ -13,6 +13,8 @@ Bounds, for bf16 half steps of 2^-8 relative:
   lse        e, and a few roundings of itself: 2^-12 + 2^-20 |r|
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -24,6 +26,16 @@ from tests import gpu_harness as H
 from tests.test_gpu_kv8 import bf16, i32, pages, running
 
 pytestmark = pytest.mark.gpu
+
+
+class OwnStream(torch.cuda.ExternalStream):
+    """A new stream.  torch's own come from a pool of 32 and are handed out again,
+    with the workspaces that other tests have made them."""
+
+    def __new__(cls):
+        at = ctypes.c_void_p()
+        assert dg.lib().hipStreamCreate(ctypes.byref(at)) == 0
+        return super().__new__(cls, at.value)
 
 
 def dev_bf16(x, dev):

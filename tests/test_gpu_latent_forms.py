@@ -188,7 +188,7 @@ def test_same_bits_and_two_streams(rows, gpu):
     args = [T.dev_bf16(q, gpu), T.dev_bf16(qr, gpu), T.upload(cache, gpu), i32(table, gpu), i32(lens, gpu), i32([0, 1, 2, 3], gpu), 1]
     outs = [torch.empty((3, 64, 512), dtype=torch.bfloat16, device=gpu) for _ in range(9)]
     dg.latent_attention(*args, outs[0])
-    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    side = [T.OwnStream(), T.OwnStream()]
     for s in side:
         s.wait_stream(torch.cuda.current_stream())
     for i, o in enumerate(outs[1:]):
@@ -296,7 +296,7 @@ def test_decode_loop_in_a_graph(rows, gpu):
         dg.latent_attention(q[..., :L], turned, cache, t, lens, cu, 1, out, lse)
         ctx.copy_(lens)
 
-    side = torch.cuda.Stream()
+    side = T.OwnStream()
     dg.reserve_workspace(dg.latent_attention_workspace_size(L, 1, heads), side)
     side.wait_stream(torch.cuda.current_stream())
     torch.cuda.synchronize()
@@ -327,7 +327,7 @@ def test_capture_needs_a_reserved_workspace(gpu):
     cache, table = T.filled(rng, [40], 16, 256, False)
     q, qr = (T.dev_bf16(y, gpu) for y in queries(rng, 1, 4, 256))
     out, c, t, kv, cu = torch.empty_like(q), T.upload(cache, gpu), i32(table, gpu), i32([40], gpu), i32([0, 1], gpu)
-    side = torch.cuda.Stream()
+    side = T.OwnStream()
     side.wait_stream(torch.cuda.current_stream())
     torch.cuda.synchronize()
     with pytest.raises(dg.DGError) as refused:

@@ -14,6 +14,9 @@ import importlib.util
 import os
 
 import pytest
+import torch
+
+from tests.test_gpu_latent import OwnStream
 
 pytestmark = pytest.mark.gpu
 
@@ -31,7 +34,9 @@ def example():
 @pytest.mark.parametrize("heads,latent,lens,fmt,bound", [
     (8, 512, (300, 1, 130), "e4m3", 0.06), (8, 512, (300, 1, 130), "bf16", 0.02), (5, 256, (70,), "bf16", 0.02),
     (64, 256, tuple(range(3, 40, 2)), "e4m3", 0.06)])
-def test_layer(gpu, example, heads, latent, lens, fmt, bound):
+def test_layer(gpu, example, monkeypatch, heads, latent, lens, fmt, bound):
+    of_torch = torch.cuda.Stream
+    monkeypatch.setattr(torch.cuda, "Stream", lambda **which: of_torch(**which) if which else OwnStream())
     print(f"[case] latent layer {heads} x {latent}, {len(lens)} prompts, {fmt}", flush=True)
     error, _ = example.serve(512, heads, latent, lens, steps=12, fmt=fmt, chunk=128)
     assert 0 < error < bound
