@@ -675,7 +675,7 @@ def _latent_shape(cache, block_table, cu):
     if scales is not None and scales.shape != (num_blocks, block, dim // 128):
         raise ValueError(f"scales {tuple(scales.shape)} do not fit latent {tuple(latent.shape)}")
     batch, max_blocks = block_table.shape
-    if len(cu) != batch + 1:
+    if cu.shape[0] != batch + 1:
         raise ValueError("the block table and cu (batch + 1) disagree on the batch")
     return (latent.data_ptr(), rope.data_ptr(), None if scales is None else scales.data_ptr(), dim, block, num_blocks,
             max_blocks, batch)
@@ -683,8 +683,8 @@ def _latent_shape(cache, block_table, cu):
 
 def _lengths(x, name, batch):
     _plain(x, name, _I32, 1)
-    if len(x) != batch:
-        raise ValueError(f"{name} must hold {batch} lengths, got {len(x)}")
+    if x.shape[0] != batch:
+        raise ValueError(f"{name} must hold {batch} lengths, got {x.shape[0]}")
     return x.data_ptr()
 
 
@@ -731,8 +731,8 @@ def latent_append(latent, rope, cache, block_table, ctx_lens, cu_new, max_new, a
         raise ValueError(f"angles must be [positions, {dim // 8}], got {tuple(angles.shape)}")
     if norm is not None:
         _plain(norm, "norm", _BF16, 1)
-        if len(norm) != dim:
-            raise ValueError(f"norm must hold {dim} values, got {len(norm)}")
+        if norm.shape[0] != dim:
+            raise ValueError(f"norm must hold {dim} values, got {norm.shape[0]}")
     heads, q, q_to = 0, (None, 0, 0), (None, 0, 0)
     if q_rope is not None:
         q_out = q_rope if q_out is None else q_out
@@ -759,7 +759,7 @@ def latent_gather(cache, block_table, cu, latent, rope, starts=None):
     at_latent, at_rope, at_scales, dim, block, num_blocks, max_blocks, batch = _latent_shape(cache, block_table, cu)
     _plain(latent, "latent", _BF16, 2)
     _plain(rope, "rope", _BF16, 2)
-    total = len(latent)
+    total = latent.shape[0]
     if latent.shape != (total, dim) or rope.shape != (total, dim // 8):
         raise ValueError(f"rows must be [tokens, {dim}] and [tokens, {dim // 8}], got {tuple(latent.shape)}, {tuple(rope.shape)}")
     _here(*cache, block_table, cu, latent, rope, starts)
@@ -819,8 +819,8 @@ def latent_expanded_attention(q, kv, k_rope, cu_q, cu_kv, max_q, out, lse=None, 
     _plain(cu_kv, "cu_kv", _I32, 1)
     _plain(out, "out", _BF16, 3)
     total, heads, dim = out.shape
-    batch = len(cu_q) - 1
-    if len(cu_kv) != batch + 1 or batch < 0:
+    batch = cu_q.shape[0] - 1
+    if cu_kv.shape[0] != batch + 1 or batch < 0:
         raise ValueError("cu_q and cu_kv must hold batch + 1 running sums each")
     total_q, qs = _packed(q, "q", heads, dim + dim // 2)
     total_kv, ks = _packed(kv, "kv", heads, 2 * dim)
