@@ -404,6 +404,20 @@ __device__ __forceinline__ void lds_dma_end(v4i_rsrc rs, uint32_t voff) {
                : "=&s"(exec_save) : "v"(voff), "s"(rs) : "memory", "scc");
 }
 
+// Eight wait states: what a vector instruction has to keep from the matrix
+// instruction (16x16x32 in bf16, four passes) whose result it reads.  The asm has
+// the results as operands, so it stands behind their products.  It is for products
+// that a branch over a side block follows: the compiler looks for what still has
+// to be waited for from the reader backwards, through the side block first, and
+// does not pass the block before the branch a second time, so the way around the
+// side block got no wait (the forms of 16 and 32 rows read scores after 2 to 7
+// states, and now and then got what the last product had not added yet).
+__device__ __forceinline__ void mfma_settle(v4f (&x)[1][1]) { asm volatile("s_nop 7" : "+v"(x[0][0])); }
+__device__ __forceinline__ void mfma_settle(v4f (&x)[1][2]) { asm volatile("s_nop 7" : "+v"(x[0][0]), "+v"(x[0][1])); }
+__device__ __forceinline__ void mfma_settle(v4f (&x)[2][2]) {
+  asm volatile("s_nop 7" : "+v"(x[0][0]), "+v"(x[0][1]), "+v"(x[1][0]), "+v"(x[1][1]));
+}
+
 // LDS of the absorbed kernel, in bytes.
 template <int L, bool F8, int NT>
 struct LatentLds {
@@ -745,6 +759,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
               for (int n = 0; n < kN; ++n) x[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kr, qrf[n][j], x[r][n], 0, 0, 0);
             }
           }
+          mfma_settle(x);  // for the branch below
           // lane: row 16 (rw kN + n) + a, tokens 4 g + e of a group of 16
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
