@@ -377,6 +377,11 @@ __device__ __forceinline__ uint32_t bf16_finite(uint32_t w) {
   return (w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFFu : w;
 }
 
+// 1 in bf16 for each half of a dword of two bf16 that is not finite, else 0.
+__device__ __forceinline__ uint32_t bf16_not_finite(uint32_t w) {
+  return ((w & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
+}
+
 typedef __attribute__((address_space(3))) v4u lds_v4u;
 typedef __attribute__((address_space(3))) v2u lds_v2u;
 
@@ -434,7 +439,7 @@ struct LatentLds {
   static constexpr bool kRestOverRope = 16 * P * 2 >= 16 * NT * 32;
   static constexpr int kRest = kP + 16 * NT * 128;
   static constexpr int kMax = kRest + (kRestOverRope ? 0 : 4 * 16 * NT * 32);  // [4][rows] floats
-  static constexpr int kFlags = kMax + 4 * 16 * NT * 4;       // [2] a reference moves, [2][4] a group's block is there
+  static constexpr int kFlags = kMax + 4 * 16 * NT * 4;       // [2] a reference moves, [2][4] a group's block is there, [2] a row sees a score of -inf
   static constexpr int kBox = kFlags + 64;
   static constexpr int kBytes = kBox + 64;
 };
@@ -475,6 +480,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
   float* const s_max = (float*)(lds + Lds::kMax);
   int* const s_flag = (int*)(lds + Lds::kFlags);
   int* const s_there = s_flag + 2;
+  int* const s_inf = s_there + 8;
   long long* const box = (long long*)(lds + Lds::kBox);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, a = lane & 15, g = lane >> 4;
   const int rw = wave / (4 / RW), tw = wave % (4 / RW);
@@ -646,7 +652,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
         lane_v[h] = tk * (2 * L) + (((2 * wave * kC + (a >> 1 & 1)) ^ latent_turn(tk & 15)) << 4) + (a & 1) * 8;
       }
       __syncthreads();  // the tile before is done with LDS
-      if (tid < 2) s_flag[tid] = 0;
+      if (tid < 2) s_flag[tid] = s_inf[tid] = 0;
       look(t0);
       stage_at(t0, page_of(t0), 0);
       look(t0 + 1);
@@ -761,6 +767,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           }
           mfma_settle(x);  // for the branch below
           // lane: row 16 (rw kN + n) + a, tokens 4 g + e of a group of 16
+          bool inf = false;
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
             const int token = s * kLatentStep + 16 * group[r] + 4 * g;
@@ -771,7 +778,10 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
               for (int n = 0; n < kN; ++n) {
                 const int seen = is ? hi[n] - token : 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[r][n][e] = e < seen ? x[r][n][e] : -__builtin_huge_valf();
+                for (int e = 0; e < 4; ++e) {
+                  if constexpr (MASKED) inf |= e < seen && x[r][n][e] == -__builtin_huge_valf();
+                  x[r][n][e] = e < seen ? x[r][n][e] : -__builtin_huge_valf();
+                }
               }
             }
           }
@@ -806,6 +816,8 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
           };
           weigh();
           if (__any(most > 0.f) && here == 0) s_flag[s & 1] = 1;
+          if constexpr (MASKED)
+            if (__any(inf) && here == 0) s_inf[s & 1] = 1;
           lds_barrier();
           // u += c^T p^T, this wave's channels; the first operands are on their
           // way before it is known that p stays
@@ -865,7 +877,9 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             fetch_p(0);
             if constexpr (!MASKED) fetch_p(1);
           }
+          const bool odd = MASKED && s_inf[s & 1] != 0;
           if (tid == 0) s_flag[(s & 1) ^ 1] = 0;
+          if (MASKED && tid == 0) s_inf[(s & 1) ^ 1] = 0;
 #pragma unroll
           for (int n = 0; n < kN; ++n) l[n] += sum[n];
 #pragma unroll
@@ -877,7 +891,8 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
             v4u w = v[i % (kAhead + 1)];
             if constexpr (MASKED) {
               // a token that some rows see and others do not must reach the
-              // former only: what is not finite has made their sums NaN already
+              // former only: what is not finite has made their sums NaN already,
+              // or is dealt with below
 #pragma unroll
               for (int e = 0; e < 4; ++e) w[e] = bf16_finite(w[e]);
 #pragma unroll
@@ -889,6 +904,35 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
               u[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), pf[k % kPf][n], u[n][c], 0, 0, 0);
             if (kEarly + i < kDmas) stage(kEarly + i);
             if (i == (kDmas - kEarly < kC ? kC : 2 * kC - 1)) stage_at(s + 2, s + 2 < last ? page2 : -1, buf);  // for the next step to send for
+          }
+          if (odd) {
+            // A row sees a token with a score of -inf and a weight of 0: 0 times
+            // infinity makes each channel NaN that is infinite there.  A product
+            // of what is not finite with what a row sees finds these.
+#pragma unroll
+            for (int i = 0; i < 2 * kC; ++i) {
+              const int c = i % kC, k = i / kC;
+              v4u w;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const v2u x = lds_turned((at_v[h] ^ (c * 32)) + k * 32 * 2 * L);
+                w[2 * h] = bf16_not_finite(x[0]);
+                w[2 * h + 1] = bf16_not_finite(x[1]);
+              }
+              if (!__any((w[0] | w[1] | w[2] | w[3]) != 0)) continue;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const int row = min(row0 + 16 * n + a, rows - 1);
+                const int seen = latent_sees(p, sq, row / p.h_q) - (s * kLatentStep + 32 * k + 8 * g);
+                v4u sees;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sees[e] = (2 * e < seen ? 0x3F80u : 0u) | (2 * e + 1 < seen ? 0x3F800000u : 0u);
+                const v4f count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, sees),
+                                                                         v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[n][c][e] = count[e] > 0.f ? __builtin_nanf("") : u[n][c][e];
+              }
+            }
           }
           static_assert(kDmas - kEarly < 2 * kC, "all pieces have set out before the next ones' places are worked out");
           // the next step has landed, and everybody is done with this one
@@ -1263,8 +1307,7 @@ __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedP
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   fin[e] = bf16_finite(v[e]);
-                  const uint32_t lo = (v[e] & 0x7F80u) == 0x7F80u, up = (v[e] & 0x7F800000u) == 0x7F800000u;
-                  ind[e] = lo * 0x3F80u | up * 0x3F800000u;
+                  ind[e] = bf16_not_finite(v[e]);
                 }
                 if (__any((ind[0] | ind[1] | ind[2] | ind[3]) != 0)) {
 #pragma unroll

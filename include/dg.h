@@ -527,6 +527,8 @@ int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const
  * max_q is the most queries of one sequence (max_q * h_q at most 2^30).
  * A token whose latent or rope part is not finite can make the rows that see it
  * not finite, and no others; what the cache holds past kv_lens[s] reaches none.
+ * Where its score is -inf its weight is 0, and 0 times an infinite latent makes
+ * that channel of the row NaN and leaves the others.
  * Scores, the softmax's running reference and sums and the output's
  * accumulator are fp32; for the second product each probability is rounded to
  * bf16, in steps of 64 tokens that some row does not see wholly to two bf16
