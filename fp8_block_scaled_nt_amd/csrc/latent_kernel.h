@@ -121,8 +121,8 @@ __global__ __launch_bounds__(256) void latent_append_kernel(LatentAppendParams p
   if (seq >= p.batch) return;
   const int i = t - p.cu[seq];
   if (i < 0 || i >= p.most) return;
-  const long long pos64 = (long long)max(p.ctx[seq], 0) + i;
-  if (pos64 >= p.positions) return;
+  const long long pos64 = (long long)p.ctx[seq] + i;
+  if (pos64 < 0 || pos64 >= p.positions) return;
   const int pos = (int)pos64;
   const float* at = p.angles + (size_t)pos * P + j * 8;
   const v4f cs[2] = {*(const v4f*)at, *(const v4f*)(at + 4)};
@@ -233,8 +233,8 @@ __global__ __launch_bounds__(256) void latent_gather_kernel(LatentGatherParams p
     while (seq < p.batch && p.cu[seq + 1] <= t) ++seq;  // as a rule none: t is of the wave's first sequence
     if (t >= p.total || seq >= p.batch) return -1;
     const int i = t - p.cu[seq];
-    const long long pos = (long long)(p.starts ? max(p.starts[seq], 0) : 0) + i;
-    if (i < 0 || pos > 0x7FFFFFFFLL) return -1;
+    const long long pos = (long long)(p.starts ? p.starts[seq] : 0) + i;
+    if (i < 0 || pos < 0 || pos > 0x7FFFFFFFLL) return -1;
     const int page = latent_page(p.c, seq, (int)pos);
     return page < 0 ? -1 : ((long long)page << p.c.block_log2) + ((int)pos & (p.c.block - 1));
   };

@@ -53,7 +53,7 @@ def append_ref(latent, rope, cache, table, ctx, cu, angles, norm=None, eps=1e-6,
     for seq in range(table.shape[0]):
         for i in range(int(cu[seq + 1] - cu[seq])):
             row, pos = int(cu[seq]) + i, int(ctx[seq]) + i
-            if pos >= angles.shape[0]:
+            if not 0 <= pos < angles.shape[0]:
                 continue
             if q is not None:
                 turned[row] = rotate(q[row], angles[pos], interleaved)
@@ -75,7 +75,7 @@ def tokens_of(cache, table, seq, first, count):
     blocks, block, L = latent.shape
     c, r, there = np.zeros((count, L)), np.zeros((count, rope.shape[2])), np.zeros(count, bool)
     for i in range(count):
-        page = page_of(table, blocks, seq, first + i, block)
+        page = page_of(table, blocks, seq, first + i, block) if first + i >= 0 else None
         if page is None:
             continue
         at = (page, (first + i) % block)

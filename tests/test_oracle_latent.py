@@ -101,3 +101,15 @@ def test_rows_that_see_nothing_and_equal_scores():
     table[0, 1] = 99                                                         # tokens 16 .. 19 are nobody's
     out, _, lse = R.attention_ref(np.zeros((1, 1, 256)), np.zeros((1, 1, 32)), cache, table, [20], [0, 1], 1.0)
     assert np.allclose(out[0, 0], c[:16].mean(0)) and np.isclose(lse[0, 0], np.log(16))
+
+
+def test_places_before_the_first_token():
+    rng = np.random.default_rng(7)
+    empty, table = caches(rng, 20, 16, 256)
+    c, r, an = rng.standard_normal((6, 256)), rng.standard_normal((6, 32)), rng.standard_normal((9, 32))
+    cache, q = R.append_ref(c, r, empty, table, [-4], [0, 6], an, q=r[:, None])
+    want, _ = R.append_ref(c[4:], r[4:], empty, table, [0], [0, 2], an)
+    assert np.array_equal(cache[0], want[0], equal_nan=True) and np.array_equal(cache[1], want[1], equal_nan=True)
+    assert np.isnan(q[:4]).all() and np.isfinite(q[4:]).all()
+    got, _, there = R.tokens_of(cache, table, 0, -3, 5)
+    assert there.tolist() == [False] * 3 + [True] * 2 and np.array_equal(got[3:], c[4:])
