@@ -717,7 +717,7 @@ def latent_append(latent, rope, cache, block_table, ctx_lens, cu_new, max_new, a
     [L] bf16 is given) and rope parts (bf16 [total, L/8], turned by their
     positions) behind the ctx_lens[i] cached tokens of each sequence, in place;
     slices of a wider projection serve.  angles: fp32 [positions, L/8], cosines
-    then sines.  q_rope (bf16 [total, heads, L/8], any strides) are the queries'
+    then sines.  q_rope (bf16 [total, heads, L/8], strides as in latent_attention) are the queries'
     rope parts, turned alike into q_out (in place if None)."""
     at_latent, at_rope, at_scales, dim, block, num_blocks, max_blocks, batch = _latent_shape(cache, block_table, cu_new)
     total, ls = _rows(latent, "latent", dim)
@@ -784,7 +784,8 @@ def latent_attention(q, q_rope, cache, block_table, kv_lens, cu_q, max_q, out, l
     L], the queries' key parts times the up-projection's key weights) and q_rope
     (bf16 [total, h, L/8]); out (bf16 [total, h, L]) and lse (fp32 [total, h], or
     None) are written in place.  q, q_rope and out may have any strides from
-    token to token and head to head.  kv_lens counts the queries' own tokens;
+    token to token and head to head that are multiples of 8, q and q_rope the same
+    row for all tokens or heads (expand).  kv_lens counts the queries' own tokens;
     scale: (3/8 L) ** -0.5 if None, that of heads of L/4 + L/8 values."""
     at_latent, at_rope, at_scales, dim, block, num_blocks, max_blocks, batch = _latent_shape(cache, block_table, cu_q)
     total, heads, qs, qh = _heads(q, "q", None, dim)

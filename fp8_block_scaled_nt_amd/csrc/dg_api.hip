@@ -1112,22 +1112,24 @@ int check_latent_cache(const void* latent, const void* rope, const void* scales,
   return DG_OK;
 }
 
-// Rows of heads with strides of their own: from token to token and from head to head.
+// Rows of heads with strides of their own: from token to token and from head to
+// head, either of which may be 0, one row for all; rows that are written have to
+// pass check_apart too.
 int check_strided(const void* x, int64_t stride, int64_t head_stride, int heads, int d, int unit, const char* name) {
   if ((reinterpret_cast<uintptr_t>(x) & (unit * 2 - 1)) != 0)
     return fail(DG_ERR_MISALIGNED, "%s must be %d-byte aligned", name, unit * 2);
   if (stride < 0 || head_stride < 0 || stride % unit != 0 || head_stride % unit != 0 ||
-      (heads > 1 && head_stride < d))
-    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: strides must be multiples of %d elements, and at least %d from head to "
-                "head (got %lld, %lld)", name, unit, d, (long long)stride, (long long)head_stride);
+      (heads > 1 && head_stride != 0 && head_stride < d))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: strides must be multiples of %d elements, and 0 or at least %d from head "
+                "to head (got %lld, %lld)", name, unit, d, (long long)stride, (long long)head_stride);
   return DG_OK;
 }
 
 // Rows that are written: no two of them may overlap, one of the strides has to step over all that the other one reaches.
 int check_apart(int64_t stride, int64_t head_stride, int total, int heads, int d, const char* name) {
   const __int128 token = stride, head = head_stride;
-  const bool apart = total <= 1 || heads <= 1 ? total <= 1 || token >= d
-                                              : token >= (heads - 1) * head + d || (head >= (total - 1) * token + d && token >= d);
+  const bool apart = (total <= 1 || token >= d) && (heads <= 1 || head >= d) &&
+                     (total <= 1 || heads <= 1 || token >= (heads - 1) * head + d || head >= (total - 1) * token + d);
   return apart ? DG_OK : fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: rows of %d tokens and %d heads overlap (strides %lld, %lld)", name,
                               total, heads, (long long)stride, (long long)head_stride);
 }

@@ -472,8 +472,8 @@ int dg_kv8_attention_workspace_size(int d, size_t* bytes);
  * elements may be NULL.
  *
  * dg_latent_append takes the latent and rope parts of new tokens, bf16 rows
- * with *_stride elements (a multiple of 8) from token to token, so slices of
- * one projection's output serve as they are.  Token i of sequence s stands at
+ * with *_stride elements (a multiple of 8, at least the row) from token to token,
+ * so slices of one projection's output serve as they are.  Token i of sequence s stands at
  * position ctx_lens[s] + i.  Into its place go
  *
  *   y = norm * c / sqrt(mean(c^2) + eps), or c if norm is NULL, in fp32: rounded
@@ -485,9 +485,9 @@ int dg_kv8_attention_workspace_size(int d, size_t* bytes);
  *
  * with norm bf16 [latent] and angles fp32 [positions][P].  If q is not NULL,
  * the rope parts of the h_q query heads of each token (q_stride elements from
- * token to token, q_head_stride from head to head) are turned alike and
- * written to q_out, which may be q itself (else q_out overlaps no input); its
- * rows must lie apart.  Tokens at positions outside [0, positions) are ignored;
+ * token to token, q_head_stride from head to head, strides as in
+ * dg_latent_attention) are turned alike and written to q_out, which may be q
+ * itself (else q_out overlaps no input); its rows must lie apart.  Tokens at positions outside [0, positions) are ignored;
  * no two tokens of a call may have the same place in the cache.  amax counts
  * finite values; infinities saturate, NaN is stored as NaN.  With a norm a NaN
  * makes the whole token NaN, and an infinity itself NaN and the rest of its
@@ -523,7 +523,8 @@ int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const
  * kv_lens[s] otherwise.  A row that sees no token gets out = 0 and lse = -inf.
  * q [total][h_q][latent], q_rope [total][h_q][P] and out [total][h_q][latent]
  * are bf16, with any strides from token to token and from head to head that are
- * multiples of 8; out's rows must lie apart.  lse is fp32 [total][h_q] or NULL;
+ * multiples of 8, from head to head 0 (one row for all heads) or at least the row;
+ * out's rows must lie apart.  lse is fp32 [total][h_q] or NULL;
  * max_q is the most queries of one sequence (max_q * h_q at most 2^30).
  * A token whose latent or rope part is not finite can make the rows that see it
  * not finite, and no others; what the cache holds past kv_lens[s] reaches none.
@@ -555,7 +556,8 @@ int dg_latent_attention_workspace_size(int latent_dim, int max_q, int h_q, size_
  *
  * q bf16 [total][heads][D + P] and kv bf16 [total_kv][heads][2 D] (key part,
  * then value; an up-projection's output as it stands), k_rope bf16 [total_kv][P],
- * with *_stride elements (a multiple of 8, less than 2^26) from token to token;
+ * with *_stride elements (a multiple of 8, at least the row, for kv and k_rope
+ * less than 2^26) from token to token;
  * cu_q, cu_kv int32 [batch + 1] running sums; out bf16 [total][heads][D], lse
  * fp32 [total][heads] or NULL; head_dim D is 128 or 64, P = D / 2.  Masks, rows
  * that see nothing, precision and determinism as in dg_latent_attention; a
