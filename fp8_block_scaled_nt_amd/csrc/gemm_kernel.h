@@ -185,9 +185,13 @@ __device__ __forceinline__ void lds_dma16_stream(v4i_rsrc rs, uint32_t voff, uin
                : "=&s"(exec_save) : "v"(voff), "s"(rs), "s"(soff), "s"(lds_addr(lds_dst)) : "memory", "m0", "scc");
 }
 
+// The s_nop makes it five wait states from the asm's begin to the DMA, what a
+// buffer access owes to a vector instruction that wrote its scalar registers: the
+// descriptors of the scales may come back from spilled lanes (v_readlane) just
+// before, and the compiler does not look into the asm for it.
 __device__ __forceinline__ void lds_dma4(v4i_rsrc rs, uint32_t voff, uint32_t soff, void* lds_dst) {
   uint64_t exec_save;
-  asm volatile(DG_M0_GUARD "s_mov_b32 m0, %4\n\ts_mov_b64 exec, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+  asm volatile("s_nop 0\n\t" DG_M0_GUARD "s_mov_b32 m0, %4\n\ts_mov_b64 exec, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                : "=&s"(exec_save) : "v"(voff), "s"(rs), "s"(soff), "s"(lds_addr(lds_dst)) : "memory", "m0", "scc");
 }
 #undef DG_M0_GUARD

@@ -209,3 +209,8 @@ def test_no_product_is_read_early(kernels):
 def test_no_transcendental_is_read_early(kernels):
     wrong = [(name, *x) for name, early in kernels for x in early if x[0] == "transcendental"]
     assert not wrong, wrong[:10]
+
+
+def test_no_scalar_is_used_early(kernels):
+    wrong = [(name, *x) for name, early in kernels for x in early if x[0] == "scalar of a vector"]
+    assert not wrong, wrong[:10]
