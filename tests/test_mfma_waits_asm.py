@@ -3,8 +3,8 @@ overwrites their results, in the generated gfx950 code (no GPU needed).
 
 A result of a matrix instruction may be read by a vector or memory instruction,
 or taken as A or B by another matrix instruction, passes + 4 wait states after
-it at the earliest (an instruction counts one, s_nop N counts N + 1); nothing in
-the hardware waits for it.  The compiler adds the waits, but its search
+it at the earliest, and the sum that it started from overwritten after passes - 1
+(an instruction counts one, s_nop N counts N + 1); nothing in the hardware waits.  The compiler adds the waits, but its search
 misses a way: where a branch leads around a side block, it walks back through
 the side block and does not pass the block before the branch again.  This test
 compiles the library's device code and walks every way forward from every matrix
@@ -114,6 +114,8 @@ class Function:
                     elif j.c & i.writes and j.c != i.writes and states < i.passes + 2:
                         found.append(("part of a sum", i.text, j.text, states, i.passes + 2))
                     return i.writes <= j.writes
+                if j.valu and j.writes & (i.c - i.writes) and states < i.passes - 1:
+                    found.append(("sum overwritten", i.text, j.text, states, i.passes - 1))
                 if (j.valu or j.memory) and (j.reads | j.writes) & i.writes:
                     found.append(("product's result", i.text, j.text, states, i.passes + 4))
                     return True
@@ -170,6 +172,9 @@ def test_straight_lines():
     assert found(PRODUCT, PRODUCT, "\ts_nop 7", use) == []
     assert found(PRODUCT, PRODUCT.replace("v[8:11]", "v[0:3]")) == [("product of a product", 0)]
     assert found(PRODUCT, "\tv_mfma_f32_16x16x32_bf16 v[4:7], v[8:11], v[12:15], v[2:5]") == [("part of a sum", 0)]
+    apart = "\tv_mfma_f32_16x16x32_bf16 v[0:3], v[8:11], v[12:15], v[4:7]"
+    assert found(apart, "\ts_nop 1", "\tv_mov_b32_e32 v7, 0") == [("sum overwritten", 2)]
+    assert found(apart, "\ts_nop 2", "\tv_mov_b32_e32 v7, 0") == []
     wide = "\tv_mfma_f32_16x16x128_f8f6f4 v[0:3], v[8:15], v[16:23], 0"
     assert found(wide, "\ts_nop 10", use) == [("product's result", 11)] and found(wide, "\ts_nop 11", use) == []
     assert found(wide + " cbsz:4 blgp:4", "\ts_nop 7", use) == []
@@ -202,7 +207,8 @@ def kernels(tmp_path_factory):
 
 
 def test_no_product_is_read_early(kernels):
-    wrong = [(name, *x) for name, early in kernels for x in early if x[0] in ("product's result", "product of a product", "part of a sum")]
+    wrong = [(name, *x) for name, early in kernels for x in early
+             if x[0] in ("product's result", "product of a product", "part of a sum", "sum overwritten")]
     assert not wrong, wrong[:10]
 
 
