@@ -573,7 +573,7 @@ def _packed(x, name, heads, d):
     if h != heads or dim != d:
         raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(x.shape)}")
     stride, s1, s2 = x.stride()
-    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+    if total > 0 and ((s2 != 1 and d > 1) or (s1 != d and heads > 1)):  # without tokens the strides mean nothing
         raise ValueError(f"the heads of a token of {name} must lie packed")
     return total, stride if total > 1 else heads * d
 
@@ -694,7 +694,7 @@ def _rows(x, name, d):
         raise TypeError(f"{name} must be a bf16 device tensor [tokens, d]")
     total, dim = x.shape
     stride, s1 = x.stride()
-    if dim != d or (s1 != 1 and d > 1):
+    if dim != d or (s1 != 1 and d > 1 and total > 0):
         raise ValueError(f"{name} must be [tokens, {d}] with packed values, got {tuple(x.shape)}")
     return total, stride if total > 1 else -(-d // 8) * 8
 
@@ -705,10 +705,10 @@ def _heads(x, name, heads, d):
         raise TypeError(f"{name} must be a bf16 device tensor [tokens, heads, d]")
     total, h, dim = x.shape
     stride, sh, s2 = x.stride()
-    if dim != d or (heads is not None and h != heads) or (s2 != 1 and d > 1):
+    if dim != d or (heads is not None and h != heads) or (s2 != 1 and d > 1 and total > 0):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {d}] with packed values, "
                          f"got {tuple(x.shape)}")
-    return total, h, stride if total > 1 else 0, sh if h > 1 else d
+    return total, h, stride if total > 1 else 0, sh if h > 1 and total > 0 else d
 
 
 def latent_append(latent, rope, cache, block_table, ctx_lens, cu_new, max_new, angles, norm=None, eps=1e-6, q_rope=None,
