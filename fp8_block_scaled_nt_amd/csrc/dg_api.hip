@@ -1143,7 +1143,11 @@ int check_apart(int64_t stride, int64_t head_stride, int total, int heads, int d
 // 244 / 148 / 112; 64 heads: 64 x 512 24 / 29 / 34; 32 heads: 1 x 8192 23 / 32, 16 x
 // 8192 49 / 47; e4m3, 128 heads: 32 x up to 4096 94 / 72 / 70; 16 heads, 256 new
 // of 2048 61 / 50 / 50).  How many steps there are the host knows from the table and
-// the pool only: with tables much wider than the sequences it takes more rows.
+// the pool only, lengths being on the device: with a pool and tables much larger than
+// the sequences it takes more rows than it should, and fewer where many sequences
+// share a small pool's pages (us in a pool as large as the sequences / 16 times as
+// large: 1 x 4096 20 / 33, 8 x 1024 23 / 33, 3 new of each of 16 x 2048 in e4m3 with 20
+// heads 31 / 40; 32 x 4096 that share their pages 102, with 64 rows 66).
 int latent_row_tiles(int max_q, int h_q, long long tokens, int workers, const char* forced) {
   for (int i = 0; forced && i < 3; ++i)
     if (strcmp(forced, kLatentRows[i]) == 0) return 1 << i;

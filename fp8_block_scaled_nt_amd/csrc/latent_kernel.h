@@ -446,8 +446,9 @@ struct LatentLds {
 
 // A unit of work is a 64-token step of a tile of 16 NT rows; a workgroup of
 // four waves takes an equal share of all units, in the order (sequence, tile,
-// step).  In a step wave w brings tokens 16 w .. 16 w + 15 to LDS, two steps
-// ahead of their use.  For the scores the waves share out the tokens, and for
+// step).  In a step wave w sends for tokens 16 w .. 16 w + 15 of the next one, and
+// has them in LDS at its end; their blocks are looked up four steps ahead.  For
+// the scores the waves share out the tokens, and for
 // more than 32 rows (RW = 2) tokens and rows, each half of both, as q for all
 // rows would not fit in the registers beside u.  p passes through LDS, and
 // wave w adds up channels w L / 4 .. of every row.  So a token's latent is
@@ -457,17 +458,20 @@ struct LatentLds {
 // latent_join_kernel adds them up.
 //
 // p meets c as bf16, 8 bits, as wide as c itself: its error, up to 2^-8 of each
-// p and of either sign, stays below out's own rounding unless the values cancel,
-// while fp16 would not hold c's range.  A step that some row does not see
+// p and of either sign, is of the size of out's own rounding where a row weighs
+// many values that cancel (against 64 bits, relative to all outputs, 0.0017 to
+// 0.0023, where out's rounding alone gives 0.0016 to 0.0017) and less elsewhere;
+// fp16 would not hold c's range, and a second piece would be another product.  A step that some row does not see
 // wholly may be all that a row sees: there p goes in two pieces, 16 bits.
 //
-// What bounds it, by case (latents of 512): with few rows HBM - 64 x up to 8192
-// tokens, 16 rows each, bf16 77 us, 5 TB/s, at a copy's rate; with 128 rows the
-// CU - 4 x 65536, bf16 97 to 117 us by the clock, 730 TFLOP/s at best, MFMA busy
-// a third of the wave cycles and waits another third (LDS, barriers: p is shared
-// between the waves); 32 x up to 4096 in e4m3 58 us, where widening makes it 4.1
-// VALU instructions an MFMA instead of 2.4; 1 x 777 of 256 7.6 us, latency of the
-// prologue.
+// What bounds it, by case (latents of 512, without the join): with few rows HBM -
+// 64 x up to 8192 tokens, 16 rows each, bf16 77 us, 5 TB/s, at a copy's rate; with
+// 128 rows the CU - 4 x 65536, bf16, 97 to 120 us from run to run as the clock goes;
+// 99.7 us is 732 TFLOP/s, and a wave then has 209 thousand cycles (2.1 GHz) for 32
+// steps: a third of MFMA, a fifth of VALU work, waits (LDS, barriers: p is shared
+// between the waves) 31 %; 32 x up to 4096 in e4m3 59 us, where widening makes it
+// 4.1 VALU instructions an MFMA instead of 2.4; 1 x 777 of 256 7.9 us, latency of
+// the prologue.
 template <int L, bool F8, int NT>
 __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p) {
   using Lds = LatentLds<L, F8, NT>;
@@ -988,7 +992,7 @@ __global__ __launch_bounds__(256, 1) void latent_attn_kernel(LatentAttnParams p)
 // kPer times 16 rows by 16 channels, of which each wave takes every fourth part.
 // (4 x 65536 with 128 heads took 141 us with sixteen workgroups a tile, 123 like
 // this.)  Bound by the launch and two chained loads: 4 us where there is one tile,
-// 5.7 us behind 64 x 8192, 10.5 us behind 4 x 65536 and 32 x 4096 with 128 heads,
+// 5.8 us behind 64 x 8192, 10.3 to 11.2 us behind 4 x 65536 and 32 x 4096 with 128 heads,
 // up to 67 MB of parts that the L2s and the Infinity Cache hold.
 template <int L, int NT>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentAttnParams p) {
@@ -1119,8 +1123,9 @@ constexpr int latent_expanded_step(bool split) { return split ? 128 : 64; }
 //
 // Bound by MFMA and the softmax's VALU work taking turns on a SIMD (two waves of
 // it overlap in part: 3.3 VALU instructions an MFMA, 28 % of the wave cycles
-// wait): 1 x 8192, 32 heads of 128, causal 666 to 714 us, up to 1030 TFLOP/s
-// of 1212 of a large library product; 4 x up to 2048 of 4096 303 to 334 us.
+// wait): 1 x 8192, 32 heads of 128, causal 663 to 714 us, up to 1037 TFLOP/s
+// of 1212 of a large library product; 4 x up to 2048 of 4096 290 to 338 us, where a
+// tile has half as many steps for its prologue and its steps with masks.
 template <int D, int MT, bool SPLIT = false>
 __global__ __launch_bounds__(256, 2) void latent_expanded_kernel(LatentExpandedParams p) {
   constexpr int R = D / 2, kRows = SPLIT ? 16 * MT : 64 * MT, kRow = 4 * D, kPieces = kRow / 16;  // bytes and 16-byte pieces of a token's row

@@ -533,7 +533,11 @@ int dg_latent_gather(const void* cache_latent, const uint16_t* cache_rope, const
  * Scores, the softmax's running reference and sums and the output's
  * accumulator are fp32; for the second product each probability is rounded to
  * bf16, in steps of 64 tokens that some row does not see wholly to two bf16
- * pieces.  The same call gives the same bits.  Needs
+ * pieces.  The same call gives the same bits.  How many rows a workgroup takes goes
+ * by max_q, h_q and the tokens that the table and the pool have room for, not by the
+ * lengths, so a captured call keeps it: in a pool much larger than what its
+ * sequences hold a short call takes longer, and last bits may differ from one pool
+ * to another.  Needs
  * dg_latent_attention_workspace_size bytes of the stream's workspace (reserve
  * it before capturing); the work is shared out on the device from the lengths
  * it finds there.
