@@ -10,8 +10,9 @@ the side block and does not pass the block before the branch again.  This test
 compiles the library's device code and walks every way forward from every matrix
 instruction, over branches and around loops.
 
-Also: a transcendental's result is used one wait state later at the earliest,
-and a buffer or global access uses scalar registers five states after a vector
+Also: a transcendental's result is used one wait state later at the earliest, a
+vector instruction's result two states later by a matrix instruction or an exchange
+between lanes, and a buffer or global access uses scalar registers five states after a vector
 instruction wrote them (the lane-less guard loads of the LDS DMA, which touch no
 memory, aside)."""
 
@@ -132,6 +133,14 @@ class Function:
                     return True
                 return False
 
+            def exchange(j, states, i=i):
+                lanes = "permlane" in j.op or re.search("quad_perm|row_", j.text)
+                if (j.mfma and j.reads & i.writes) or (lanes and (j.reads | (j.writes if "permlane" in j.op else set())) & i.writes):
+                    found.append(("vector into a product or another lane", i.text, j.text, states, 2))
+                return i.writes <= j.writes
+
+            if i.valu:
+                self.walk(at, 2, exchange)
             if i.mfma:
                 self.walk(at, i.passes + 4, matrix)
             elif i.valu and i.op.startswith(TRANSCENDENTAL):
@@ -191,6 +200,9 @@ def test_the_way_around_a_side_block():
 
 
 def test_other_waits():
+    assert found("\tv_mov_b32_e32 v9, 0", "\ts_nop 0", PRODUCT) == [("vector into a product or another lane", 1)]
+    assert found("\tv_mov_b32_e32 v9, 0", "\ts_nop 1", PRODUCT) == []
+    assert found("\tv_mov_b32_e32 v9, 0", "\tv_permlane32_swap_b32_e32 v8, v9") == [("vector into a product or another lane", 0)]
     assert found("\tv_exp_f32_e32 v1, v2", "\tv_add_f32_e32 v3, v1, v1") == [("transcendental", 0)]
     assert found("\tv_exp_f32_e32 v1, v2", "\tv_exp_f32_e32 v4, v5", "\tv_add_f32_e32 v3, v1, v1") == []
     read = "\tv_readlane_b32 s7, v9, 3"
@@ -214,6 +226,11 @@ def test_no_product_is_read_early(kernels):
 
 def test_no_transcendental_is_read_early(kernels):
     wrong = [(name, *x) for name, early in kernels for x in early if x[0] == "transcendental"]
+    assert not wrong, wrong[:10]
+
+
+def test_no_vector_is_used_early(kernels):
+    wrong = [(name, *x) for name, early in kernels for x in early if x[0] == "vector into a product or another lane"]
     assert not wrong, wrong[:10]
 
 
